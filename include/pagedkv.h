@@ -48,7 +48,10 @@ typedef enum pkv_device_error {
                                 index = seq * max_blocks_per_seq + logical block     */
     PKV_DEVERR_SEQ_LEN = 3,  /* seq_len < 0, or more tokens than the block table or
                                 max_seq_len allow; index = seq                         */
-    PKV_DEVERR_TIMEOUT = 4   /* a staging wait gave up (about 2 s); index = CTA id   */
+    PKV_DEVERR_TIMEOUT = 4,  /* a staging wait gave up (about 2 s); index = CTA id   */
+    PKV_DEVERR_POSITION = 5, /* position outside [0, max_position); index = token    */
+    PKV_DEVERR_PATH = 6      /* accepted path not ascending or past the block table;
+                                index = seq                                           */
 } pkv_device_error;
 
 /*
@@ -340,6 +343,185 @@ int pkv_chunk_attention(void *out, const void *q, const void *k_cache, const voi
 size_t pkv_chunk_workspace_bytes(int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
                                  int32_t head_dim, int32_t num_query_tokens,
                                  int32_t max_query_len, int32_t max_seq_len);
+
+/* ------------------------------------------------------------------------
+ * One speculative step around the cache: the new tokens' queries, keys and
+ * values leave the QKV product (pkv_norm_rope_write), a tree of drafted tokens
+ * is verified against the cache (pkv_tree_attention), and the accepted path's
+ * rows move to the positions they will keep (pkv_tree_accept).  The first one
+ * serves decode and prefill steps alike. */
+
+/* Norm and rotation of pkv_norm_rope_write. */
+typedef struct pkv_norm_rope {
+    const void *q_weight;  /* device fp16 [head_dim], or NULL: queries not normed */
+    const void *k_weight;  /* device fp16 [head_dim], or NULL: keys not normed    */
+    float eps;             /* added to the mean square, >= 0                      */
+    const float *cos_sin;  /* device fp32 [max_position][rot_dim]: rot_dim/2 cosines,
+                              then rot_dim/2 sines; NULL iff rot_dim == 0         */
+    int64_t max_position;  /* rows of cos_sin                                     */
+    int32_t rot_dim;       /* leading dims of each head rotated: a multiple of 16
+                              in [0, head_dim]                                    */
+    int32_t interleaved;   /* pairs: 0 (d, d + rot_dim/2); 1 (2i, 2i + 1)         */
+} pkv_norm_rope;
+
+/*
+ * Per-head norm of queries and keys, rotation by position, and the cache
+ * write, in one pass over the QKV product's rows.  For every token t with
+ * slot_mapping[t] >= 0, every head row x of q and k:
+ *     n_d = x_d * w_d / sqrt(mean_d x_d^2 + eps)       (n = x without a weight)
+ *     a' = a cos_i - b sin_i,  b' = b cos_i + a sin_i   for pair i = (a, b) of n
+ *                                                       at positions[t]
+ * computed in fp32 and rounded once.  Rotated queries go to q_out; rotated
+ * keys, and values as they are, to the slot's rows of k_cache and v_cache.
+ *  q, k, v       device fp16, token t's rows at t*stride elements, its heads
+ *                packed [num_heads | num_kv_heads][head_dim]: the three may be
+ *                slices of one packed row.  Strides are multiples of 8.
+ *  q_out         device fp16 [num_tokens, num_heads, head_dim]; may be q itself
+ *                when q is packed (q_stride == num_heads*head_dim), and must not
+ *                overlap the inputs otherwise.
+ *  positions     device int64 [num_tokens].  A position outside [0,
+ *                max_position) skips its token, recorded (PKV_DEVERR_POSITION);
+ *                not read when rot_dim == 0 (then it may be NULL).
+ *  slot_mapping  as pkv_cache_write: a negative slot is padding -- the token is
+ *                skipped, its q_out row left as it was -- and a slot past the
+ *                cache skips the token, recorded (PKV_DEVERR_SLOT).
+ *  k_cache, v_cache  fp16 [num_blocks, block_size, num_kv_heads, head_dim].
+ * Ordering: the call may start before an earlier kernel of the stream that
+ * signals programmatic launch completion has finished, and waits for it before
+ * it reads or writes anything; it never signals early itself, so a decode or
+ * tree attention after it sees its queries.
+ * Supported: head_dim 64 or 128.  Returns PKV_OK (num_tokens == 0 launches
+ * nothing), PKV_ERR_NULL, PKV_ERR_INVALID, PKV_ERR_UNSUPPORTED,
+ * PKV_ERR_ALIGNMENT (16-byte pointers; 8 for int64), PKV_ERR_CUDA.
+ */
+int pkv_norm_rope_write(void *q_out, const void *q, const void *k, const void *v,
+                        int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                        const pkv_norm_rope *norm_rope, const int64_t *positions,
+                        const int64_t *slot_mapping, int64_t num_tokens, void *k_cache,
+                        void *v_cache, int32_t num_heads, int32_t num_kv_heads,
+                        int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                        pkv_stream_t stream);
+
+/* The same into FP8 caches (layout and quantisation of pkv_cache_write_fp8):
+ * keys are quantised from their fp32 values, not rounded to fp16 first. */
+int pkv_norm_rope_write_fp8(void *q_out, const void *q, const void *k, const void *v,
+                            int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                            const pkv_norm_rope *norm_rope, const int64_t *positions,
+                            const int64_t *slot_mapping, int64_t num_tokens, void *k_cache,
+                            void *v_cache, float *k_scale, float *v_scale, int32_t num_heads,
+                            int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                            int64_t num_blocks, pkv_stream_t stream);
+
+/*
+ * Rows of an FP8 cache read back in 16 bits (the inverse of
+ * pkv_cache_write_fp8): row t of k (and v) is value(code) * scale of slot
+ * slot_mapping[t], rounded to fp16 once.  A negative slot leaves its rows as
+ * they were; a slot past the cache too, recorded (PKV_DEVERR_SLOT).  Several
+ * tokens may read one slot.
+ *  k, v   device fp16 [num_tokens, num_kv_heads, head_dim], written; v, v_cache
+ *         and v_scale all NULL or all set.
+ * head_dim 64 or 128.  Ordering as pkv_norm_rope_write.  Returns PKV_OK,
+ * PKV_ERR_NULL, PKV_ERR_INVALID, PKV_ERR_UNSUPPORTED, PKV_ERR_ALIGNMENT (rows
+ * 32, caches 16, slots 8, scales 4 bytes), PKV_ERR_CUDA.
+ */
+int pkv_cache_read_fp8(void *k, void *v, const int64_t *slot_mapping, int64_t num_tokens,
+                       const void *k_cache, const void *v_cache, const float *k_scale,
+                       const float *v_scale, int32_t num_kv_heads, int32_t head_dim,
+                       int32_t block_size, int64_t num_blocks, pkv_stream_t stream);
+
+/* Largest max_query_len of pkv_tree_attention. */
+#define PKV_MAX_TREE_NODES 256
+
+/*
+ * Attention of a tree of drafted tokens per sequence over the paged cache.
+ * As pkv_chunk_attention, sequence i's last Q = query_start[i+1] -
+ * query_start[i] tokens are the drafted ones, already in the cache; but which
+ * of them a drafted token sees is given by a mask instead of their order:
+ * query row r sees every position 0 .. L-Q-1 and drafted token j (position
+ * L-Q+j) exactly when bit j % 64 of tree_mask[r*mask_words + j/64] is set
+ * (bits at and past Q are ignored; a token sees itself only if its own bit is
+ * set).  A row that sees nothing, and a row whose visible scores are all minus
+ * infinity, gives zeros.  What a masked position holds -- infinities and NaN
+ * included -- does not reach the rows that do not see it.
+ *   tree_mask      device uint64 [num_query_tokens][mask_words], with
+ *                  max_query_len <= 64*mask_words
+ *   max_query_len  host bound on every Q, at most PKV_MAX_TREE_NODES
+ *   workspace      pkv_tree_workspace_bytes(...) bytes of device scratch; its
+ *                  contents need no preparation and carry nothing from call to
+ *                  call.  Calls that share a workspace must not overlap.
+ *   other arguments, supported shapes, skipped sequences and blocks as
+ *   pkv_chunk_attention.
+ * Ordering: the call may start before an earlier kernel that signals
+ * programmatic launch completion has finished, and waits for it before it
+ * reads or writes anything.
+ * Returns PKV_OK (no sequence or no query token launches nothing),
+ * PKV_ERR_NULL, PKV_ERR_INVALID, PKV_ERR_UNSUPPORTED, PKV_ERR_ALIGNMENT (16
+ * bytes; 8 for the mask, 4 for int32), PKV_ERR_WORKSPACE, PKV_ERR_CUDA.
+ */
+int pkv_tree_attention(void *out, const void *q, const void *k_cache, const void *v_cache,
+                       const int32_t *block_tables, const int32_t *seq_lens,
+                       const int32_t *query_start, const uint64_t *tree_mask,
+                       int32_t mask_words, float scale, int32_t num_heads,
+                       int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                       int32_t num_seqs, int32_t max_blocks_per_seq, int32_t num_query_tokens,
+                       int32_t max_query_len, int32_t max_seq_len, int64_t num_blocks,
+                       void *workspace, size_t workspace_bytes, pkv_stream_t stream);
+
+/* The same over FP8 caches, read as value(code) * scale of their rows (layout
+ * of pkv_cache_write_fp8; caches and scales 16-byte aligned). */
+int pkv_tree_attention_fp8(void *out, const void *q, const void *k_cache, const void *v_cache,
+                           const float *k_scale, const float *v_scale,
+                           const int32_t *block_tables, const int32_t *seq_lens,
+                           const int32_t *query_start, const uint64_t *tree_mask,
+                           int32_t mask_words, float scale, int32_t num_heads,
+                           int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                           int32_t num_seqs, int32_t max_blocks_per_seq,
+                           int32_t num_query_tokens, int32_t max_query_len,
+                           int32_t max_seq_len, int64_t num_blocks, void *workspace,
+                           size_t workspace_bytes, pkv_stream_t stream);
+
+/* Workspace bytes of either tree attention for these bounds on the current
+ * device (0 for an invalid shape). */
+size_t pkv_tree_workspace_bytes(int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
+                                int32_t head_dim, int32_t num_query_tokens,
+                                int32_t max_query_len, int32_t max_seq_len);
+
+/* One cache of pkv_tree_accept. */
+typedef struct pkv_cache_desc {
+    void *cache;   /* device byte allocation holding the view              */
+    pkv_view view; /* view.layer is the first layer moved                  */
+} pkv_cache_desc;
+
+#define PKV_MAX_ACCEPT_DEPTH 256
+
+/*
+ * Keep an accepted path of every sequence's drafted tree: with ctx =
+ * ctx_lens[i] tokens before the tree, the row of drafted token path[i][d]
+ * (position ctx + path[i][d]) moves to position ctx + d, for d = 0, 1, ...
+ * until the first negative entry, in every cache of descs and each of
+ * num_layers layers from view.layer on -- as if every row were read before any
+ * is written.  Rows are moved byte for byte.
+ *  descs         HOST array of num_descs (0..PKV_MAX_WRITE_DESCS); read during
+ *                the call only.  Quantised caches pass their scales as caches
+ *                of their own (row_width 4*num_kv_heads).
+ *  path          device int32 [num_seqs, max_depth]; its entries before the
+ *                first negative one must ascend strictly, and their positions
+ *                lie inside the block table: else the sequence is left as it
+ *                was and recorded (PKV_DEVERR_PATH).  A sequence that names a
+ *                block outside [0, num_blocks) for one of these positions is
+ *                left as it was and recorded (PKV_DEVERR_BLOCK_ID).
+ *  ctx_lens      device int32 [num_seqs].
+ *  block_tables  device int32 [num_seqs, max_blocks_per_seq].  Sequences must
+ *                not share the blocks that rows move in.
+ * Any block_size.  max_depth at most PKV_MAX_ACCEPT_DEPTH.  Ordering as
+ * pkv_norm_rope_write.  Returns PKV_OK (nothing to move launches nothing),
+ * PKV_ERR_NULL, PKV_ERR_INVALID, PKV_ERR_UNSUPPORTED, PKV_ERR_ALIGNMENT,
+ * PKV_ERR_CUDA.
+ */
+int pkv_tree_accept(const pkv_cache_desc *descs, int32_t num_descs, int32_t num_layers,
+                    const int32_t *path, int32_t max_depth, const int32_t *ctx_lens,
+                    const int32_t *block_tables, int32_t num_seqs, int32_t max_blocks_per_seq,
+                    int32_t block_size, int64_t num_blocks, pkv_stream_t stream);
 
 /* Bytes of the built-in scratch of pkv_decode_attention_noalloc (16 MiB). */
 #define PKV_NOALLOC_SCRATCH_BYTES ((size_t)16 << 20)

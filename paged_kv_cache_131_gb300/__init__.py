@@ -18,7 +18,10 @@ __all__ = [
     "pkv_cache_write", "pkv_decode_attention", "pkv_decode_workspace_bytes",
     "pkv_decode_workspace_init", "pkv_get_device_error", "pkv_status_string",
     "pkv_last_error_string", "pkv_version", "EXPORTED_SYMBOLS", "pkv_chunk_attention",
-    "pkv_chunk_workspace_bytes",
+    "pkv_chunk_workspace_bytes", "pkv_norm_rope", "pkv_cache_desc", "pkv_norm_rope_write",
+    "pkv_norm_rope_write_fp8", "pkv_cache_read_fp8", "pkv_tree_attention",
+    "pkv_tree_attention_fp8", "pkv_tree_workspace_bytes", "pkv_tree_accept",
+    "PKV_MAX_TREE_NODES", "PKV_MAX_ACCEPT_DEPTH",
     "PKV_COMPUTE_AUTO", "PKV_COMPUTE_SIMT", "PKV_COMPUTE_MMA", "PKV_SCHEDULE_AUTO",
     "PKV_SCHEDULE_GRID", "PKV_SCHEDULE_BALANCED", "DEVICE_ERRORS",
 ]
@@ -28,7 +31,9 @@ library_path = os.path.join(_HERE, "libpagedkv.so")
 
 PKV_COMPUTE_AUTO, PKV_COMPUTE_SIMT, PKV_COMPUTE_MMA = 0, 1, 2
 PKV_SCHEDULE_AUTO, PKV_SCHEDULE_GRID, PKV_SCHEDULE_BALANCED = 0, 1, 2
-DEVICE_ERRORS = {0: "none", 1: "slot", 2: "block_id", 3: "seq_len", 4: "timeout"}
+PKV_MAX_TREE_NODES, PKV_MAX_ACCEPT_DEPTH = 256, 256
+DEVICE_ERRORS = {0: "none", 1: "slot", 2: "block_id", 3: "seq_len", 4: "timeout", 5: "position",
+                 6: "path"}
 
 EXPORTED_SYMBOLS = [
     "pkv_cache_write", "pkv_decode_attention", "pkv_decode_attention_ex",
@@ -36,7 +41,9 @@ EXPORTED_SYMBOLS = [
     "pkv_get_device_error", "pkv_status_string", "pkv_last_error_string", "pkv_version",
     "pkv_decode_attention_noalloc", "pkv_cache_write_multi", "pkv_copy_blocks",
     "pkv_cache_write_fp8", "pkv_decode_attention_fp8", "pkv_chunk_attention",
-    "pkv_chunk_workspace_bytes",
+    "pkv_chunk_workspace_bytes", "pkv_norm_rope_write", "pkv_norm_rope_write_fp8",
+    "pkv_cache_read_fp8", "pkv_tree_attention", "pkv_tree_attention_fp8",
+    "pkv_tree_workspace_bytes", "pkv_tree_accept",
 ]
 
 
@@ -62,6 +69,17 @@ class pkv_write_desc(ctypes.Structure):
 class pkv_decode_options(ctypes.Structure):
     _fields_ = [("partition_size", ctypes.c_int32), ("compute", ctypes.c_int32),
                 ("schedule", ctypes.c_int32)]
+
+
+class pkv_norm_rope(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("cos_sin", ctypes.c_void_p),
+                ("max_position", ctypes.c_int64), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
+class pkv_cache_desc(ctypes.Structure):
+    _fields_ = [("cache", ctypes.c_void_p), ("view", pkv_view)]
 
 
 _lib = None
@@ -104,6 +122,24 @@ def load(path: str | None = None):
                                         _p]
     lib.pkv_chunk_workspace_bytes.restype = _sz
     lib.pkv_chunk_workspace_bytes.argtypes = [_i32] * 7
+    nrw = [_p, _p, _p, _p, _i64, _i64, _i64, ctypes.POINTER(pkv_norm_rope), _p, _p, _i64, _p, _p]
+    lib.pkv_norm_rope_write.restype = ctypes.c_int
+    lib.pkv_norm_rope_write.argtypes = nrw + [_i32, _i32, _i32, _i32, _i64, _p]
+    lib.pkv_norm_rope_write_fp8.restype = ctypes.c_int
+    lib.pkv_norm_rope_write_fp8.argtypes = nrw + [_p, _p, _i32, _i32, _i32, _i32, _i64, _p]
+    lib.pkv_cache_read_fp8.restype = ctypes.c_int
+    lib.pkv_cache_read_fp8.argtypes = [_p, _p, _p, _i64, _p, _p, _p, _p, _i32, _i32, _i32, _i64,
+                                       _p]
+    tree = [_p, _p, _p, _i32, ctypes.c_float] + [_i32] * 9 + [_i64, _p, _sz, _p]
+    lib.pkv_tree_attention.restype = ctypes.c_int
+    lib.pkv_tree_attention.argtypes = [_p] * 5 + tree
+    lib.pkv_tree_attention_fp8.restype = ctypes.c_int
+    lib.pkv_tree_attention_fp8.argtypes = [_p] * 7 + tree
+    lib.pkv_tree_workspace_bytes.restype = _sz
+    lib.pkv_tree_workspace_bytes.argtypes = [_i32] * 7
+    lib.pkv_tree_accept.restype = ctypes.c_int
+    lib.pkv_tree_accept.argtypes = [ctypes.POINTER(pkv_cache_desc), _i32, _i32, _p, _i32, _p, _p,
+                                    _i32, _i32, _i32, _i64, _p]
     lib.pkv_decode_workspace_bytes.restype = _sz
     lib.pkv_decode_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32, _i32]
     lib.pkv_decode_workspace_bytes_ex.restype = _sz
@@ -315,6 +351,239 @@ def pkv_decode_attention_fp8(out, q, k_cache, v_cache, k_scale, v_scale, block_t
         block_tables.shape[1], int(max_seq_len), int(num_blocks), _dev(workspace, "workspace"),
         workspace.numel() * workspace.element_size(), _stream(stream))
     return _check(st, "pkv_decode_attention_fp8") if check else st
+
+
+def _shape(t, name, want):
+    """Refuse a tensor whose shape is not ``want``."""
+    if t is None:
+        raise ValueError(f"{name} is missing")
+    if tuple(t.shape) != tuple(want):
+        raise ValueError(f"{name} must have shape {tuple(want)}, got {tuple(t.shape)}")
+
+
+def _on_current_device(**tensors):
+    """Refuse tensors that are not on the current CUDA device: the launch goes to
+    a stream of that device."""
+    import torch
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name} is on {t.device}, not on the current device")
+
+
+def _token_rows(t, name):
+    """(device pointer, token stride in elements) of fp16 rows [T, heads, D] whose
+    heads are packed; tokens may be strided (a slice of a packed QKV row)."""
+    import torch
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.float16 or t.dim() != 3:
+        raise ValueError(f"{name} must be float16 [tokens, heads, head_dim]")
+    T, h, D = t.shape
+    if (D > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: a token's heads must be packed")
+    return t.data_ptr(), t.stride(0) if T > 1 else h * D
+
+
+def _norm_rope_write(name, q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, scales,
+                     cos_sin, q_weight, k_weight, eps, interleaved, block_size, num_blocks,
+                     stream, check):
+    import torch
+    T, H, D = q.shape
+    Hk = k.shape[1]
+    kind = torch.float16 if scales is None else torch.uint8
+    _on_current_device(q_out=q_out, q=q, k=k, v=v, positions=positions, slot_mapping=slot_mapping,
+                       k_cache=k_cache, v_cache=v_cache, cos_sin=cos_sin, q_weight=q_weight,
+                       k_weight=k_weight)
+    _shape(q_out, "q_out", (T, H, D))
+    _shape(k, "k", (T, Hk, D))
+    _shape(v, "v", (T, Hk, D))
+    _shape(slot_mapping, "slot_mapping", (T,))
+    _shape(k_cache, "k_cache", (num_blocks, block_size, Hk, D))
+    _shape(v_cache, "v_cache", (num_blocks, block_size, Hk, D))
+    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _shape(w, n, (D,))
+    if cos_sin is None:
+        max_pos, rot = 0, 0
+    else:
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [max_position, rot_dim]")
+        max_pos, rot = cos_sin.shape
+        _shape(positions, "positions", (T,))
+    nr = pkv_norm_rope(_dev(q_weight, "q_weight", torch.float16),
+                       _dev(k_weight, "k_weight", torch.float16), eps,
+                       _dev(cos_sin, "cos_sin", torch.float32), max_pos, rot, int(interleaved))
+    qp, qs = _token_rows(q, "q")
+    kp, ks = _token_rows(k, "k")
+    vp, vs = _token_rows(v, "v")
+    args = [_dev(q_out, "q_out", torch.float16), qp, kp, vp, qs, ks, vs, ctypes.byref(nr),
+            _dev(positions, "positions", torch.int64) if rot else None,
+            _dev(slot_mapping, "slot_mapping", torch.int64), T, _dev(k_cache, "k_cache", kind),
+            _dev(v_cache, "v_cache", kind)]
+    if scales is not None:
+        _on_current_device(k_scale=scales[0], v_scale=scales[1])
+        for s, n in zip(scales, ("k_scale", "v_scale")):
+            _shape(s, n, (num_blocks, block_size, Hk))
+            args.append(_dev(s, n, torch.float32))
+    st = getattr(load(), name)(*args, H, Hk, D, block_size, num_blocks, _stream(stream))
+    return _check(st, name) if check else st
+
+
+def pkv_norm_rope_write(q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, cos_sin=None,
+                        q_weight=None, k_weight=None, eps: float = 1e-6,
+                        interleaved: bool = False, block_size: int = 16, num_blocks: int = 0,
+                        stream=None, check: bool = True) -> int:
+    """Per-head norm, rotation and cache write in one pass: see pkv_norm_rope_write
+    in pagedkv.h.
+
+    q [T, H, D], k, v [T, Hk, D]: CUDA fp16, tokens may be strided; q_out: CUDA
+    fp16 [T, H, D]; positions, slot_mapping: CUDA int64 [T]; caches: CUDA fp16
+    [NB, bs, Hk, D]; cos_sin: CUDA fp32 [max_position, rot_dim] or None;
+    q_weight, k_weight: CUDA fp16 [D] or None.
+    """
+    return _norm_rope_write("pkv_norm_rope_write", q_out, q, k, v, positions, slot_mapping,
+                            k_cache, v_cache, None, cos_sin, q_weight, k_weight, eps, interleaved,
+                            block_size, num_blocks, stream, check)
+
+
+def pkv_norm_rope_write_fp8(q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, k_scale,
+                            v_scale, cos_sin=None, q_weight=None, k_weight=None,
+                            eps: float = 1e-6, interleaved: bool = False, block_size: int = 16,
+                            num_blocks: int = 0, stream=None, check: bool = True) -> int:
+    """pkv_norm_rope_write into E4M3 caches (uint8 [NB, bs, Hk, D]) and fp32 scales
+    [NB, bs, Hk]: see pagedkv.h."""
+    return _norm_rope_write("pkv_norm_rope_write_fp8", q_out, q, k, v, positions, slot_mapping,
+                            k_cache, v_cache, (k_scale, v_scale), cos_sin, q_weight, k_weight, eps,
+                            interleaved, block_size, num_blocks, stream, check)
+
+
+def pkv_cache_read_fp8(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, block_size: int,
+                       num_blocks: int, stream=None, check: bool = True) -> int:
+    """Rows of E4M3 caches read back into fp16 k, v [T, Hk, D]: see pkv_cache_read_fp8
+    in pagedkv.h (v, v_cache, v_scale may all be None)."""
+    import torch
+    T, Hk, D = k.shape
+    _on_current_device(k=k, v=v, slot_mapping=slot_mapping, k_cache=k_cache, v_cache=v_cache,
+                       k_scale=k_scale, v_scale=v_scale)
+    _shape(slot_mapping, "slot_mapping", (T,))
+    for x, c, s, n in ((k, k_cache, k_scale, "k"), (v, v_cache, v_scale, "v")):
+        if x is None and c is None and s is None and n == "v":
+            continue
+        _shape(x, n, (T, Hk, D))
+        _shape(c, n + "_cache", (num_blocks, block_size, Hk, D))
+        _shape(s, n + "_scale", (num_blocks, block_size, Hk))
+    st = load().pkv_cache_read_fp8(
+        _dev(k, "k", torch.float16), _dev(v, "v", torch.float16),
+        _dev(slot_mapping, "slot_mapping", torch.int64), T,
+        _dev(k_cache, "k_cache", torch.uint8), _dev(v_cache, "v_cache", torch.uint8),
+        _dev(k_scale, "k_scale", torch.float32), _dev(v_scale, "v_scale", torch.float32),
+        Hk, D, block_size, num_blocks, _stream(stream))
+    return _check(st, "pkv_cache_read_fp8") if check else st
+
+
+def _tree_attention(name, out, q, k_cache, v_cache, scales, block_tables, seq_lens, query_start,
+                    tree_mask, scale, num_heads, num_kv_heads, head_dim, block_size,
+                    max_query_len, max_seq_len, num_blocks, workspace, stream, check):
+    import torch
+    _on_current_device(out=out, q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                       seq_lens=seq_lens, query_start=query_start, tree_mask=tree_mask,
+                       workspace=workspace)
+    if q.dim() != 3 or block_tables.dim() != 2 or tree_mask.dim() != 2:
+        raise ValueError("q must be [Tq, H, D], block_tables [S, MB], tree_mask [Tq, words]")
+    Tq, S = q.shape[0], seq_lens.numel()
+    _shape(q, "q", (Tq, num_heads, head_dim))
+    _shape(out, "out", (Tq, num_heads, head_dim))
+    _shape(query_start, "query_start", (S + 1,))
+    _shape(block_tables, "block_tables", (S, block_tables.shape[1]))
+    _shape(tree_mask, "tree_mask", (Tq, tree_mask.shape[1]))
+    kind = torch.float16 if scales is None else torch.uint8
+    args = [_dev(out, "out", torch.float16), _dev(q, "q", torch.float16)]
+    for c, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _shape(c, n, (num_blocks, block_size, num_kv_heads, head_dim))
+        args.append(_dev(c, n, kind))
+    if scales is not None:
+        _on_current_device(k_scale=scales[0], v_scale=scales[1])
+        for s, n in zip(scales, ("k_scale", "v_scale")):
+            _shape(s, n, (num_blocks, block_size, num_kv_heads))
+            args.append(_dev(s, n, torch.float32))
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        ws_ptr, ws_bytes = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+    st = getattr(load(), name)(
+        *args, _dev(block_tables, "block_tables", torch.int32),
+        _dev(seq_lens, "seq_lens", torch.int32), _dev(query_start, "query_start", torch.int32),
+        _dev(tree_mask, "tree_mask", torch.int64), tree_mask.shape[1], float(scale), num_heads,
+        num_kv_heads, head_dim, block_size, S, block_tables.shape[1], Tq, int(max_query_len),
+        int(max_seq_len), int(num_blocks), ws_ptr, ws_bytes, _stream(stream))
+    return _check(st, name) if check else st
+
+
+def pkv_tree_attention(out, q, k_cache, v_cache, block_tables, seq_lens, query_start, tree_mask,
+                       scale: float, num_heads: int, num_kv_heads: int, head_dim: int,
+                       block_size: int, max_query_len: int, max_seq_len: int, num_blocks: int,
+                       workspace=None, stream=None, check: bool = True) -> int:
+    """Attention of a tree of drafted tokens per sequence: see pkv_tree_attention in
+    pagedkv.h.
+
+    out, q: CUDA fp16 [Tq, H, D]; caches: CUDA fp16 [NB, bs, Hk, D];
+    block_tables: CUDA int32 [S, MB]; seq_lens: CUDA int32 [S]; query_start:
+    CUDA int32 [S + 1]; tree_mask: CUDA int64 [Tq, words] (bit j % 64 of word
+    j // 64: sees drafted token j); workspace: CUDA uint8 tensor of
+    pkv_tree_workspace_bytes(...) bytes.
+    """
+    return _tree_attention("pkv_tree_attention", out, q, k_cache, v_cache, None, block_tables,
+                           seq_lens, query_start, tree_mask, scale, num_heads, num_kv_heads,
+                           head_dim, block_size, max_query_len, max_seq_len, num_blocks, workspace,
+                           stream, check)
+
+
+def pkv_tree_attention_fp8(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens,
+                           query_start, tree_mask, scale: float, num_heads: int,
+                           num_kv_heads: int, head_dim: int, block_size: int, max_query_len: int,
+                           max_seq_len: int, num_blocks: int, workspace=None, stream=None,
+                           check: bool = True) -> int:
+    """pkv_tree_attention over E4M3 caches (uint8) and fp32 scales: see pagedkv.h."""
+    return _tree_attention("pkv_tree_attention_fp8", out, q, k_cache, v_cache, (k_scale, v_scale),
+                           block_tables, seq_lens, query_start, tree_mask, scale, num_heads,
+                           num_kv_heads, head_dim, block_size, max_query_len, max_seq_len,
+                           num_blocks, workspace, stream, check)
+
+
+def pkv_tree_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                             num_query_tokens: int, max_query_len: int, max_seq_len: int) -> int:
+    return int(load().pkv_tree_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim,
+                                               num_query_tokens, max_query_len, max_seq_len))
+
+
+def pkv_tree_accept(caches, num_layers: int, path, ctx_lens, block_tables, block_size: int,
+                    num_blocks: int, stream=None, check: bool = True) -> int:
+    """Move the cache rows of each sequence's accepted path to their positions: see
+    pkv_tree_accept in pagedkv.h.
+
+    caches: sequence of (cache, view) with a CUDA tensor and a pkv_view-like view;
+    path: CUDA int32 [S, max_depth], negative past a path's end; ctx_lens: CUDA
+    int32 [S]; block_tables: CUDA int32 [S, MB].
+    """
+    import torch
+    _on_current_device(path=path, ctx_lens=ctx_lens, block_tables=block_tables)
+    if path.dim() != 2 or block_tables.dim() != 2:
+        raise ValueError("path must be [S, max_depth], block_tables [S, MB]")
+    S = path.shape[0]
+    _shape(ctx_lens, "ctx_lens", (S,))
+    _shape(block_tables, "block_tables", (S, block_tables.shape[1]))
+    arr = (pkv_cache_desc * max(1, len(caches)))()
+    for i, (cache, view) in enumerate(caches):
+        _on_current_device(**{f"caches[{i}]": cache})
+        arr[i] = pkv_cache_desc(_dev(cache, f"caches[{i}]"), _as_view(view))
+    st = load().pkv_tree_accept(
+        arr, len(caches), num_layers, _dev(path, "path", torch.int32), path.shape[1],
+        _dev(ctx_lens, "ctx_lens", torch.int32), _dev(block_tables, "block_tables", torch.int32),
+        S, block_tables.shape[1], block_size, num_blocks, _stream(stream))
+    return _check(st, "pkv_tree_accept") if check else st
 
 
 def pkv_decode_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,

@@ -20,7 +20,8 @@ HEADER = os.path.join(ROOT, "include", "pagedkv.h")
 
 SOURCES = ["pkv_api.cu", "pkv_write.cu", "pkv_write_fp8.cu", "pkv_blocks.cu", "pkv_decode_api.cu", "pkv_decode_grid.cu",
            "pkv_decode_balanced.cu", "pkv_decode_noalloc.cu", "pkv_tensor_map.cu",
-           "pkv_chunk.cu"]
+           "pkv_chunk.cu", "pkv_norm_rope.cu", "pkv_read_fp8.cu", "pkv_tree.cu",
+           "pkv_tree_accept.cu"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
     "-O3", "-lineinfo", "-std=c++17",
