@@ -447,7 +447,7 @@ int pkv_cache_read_fp8(void *k, void *v, const int64_t *slot_mapping, int64_t nu
  *                  max_query_len <= 64*mask_words
  *   max_query_len  host bound on every Q, at most PKV_MAX_TREE_NODES
  *   workspace      pkv_tree_workspace_bytes(...) bytes of device scratch,
- *                  32-byte aligned; its contents need no preparation and carry nothing from call to
+ *                  16-byte aligned; its contents need no preparation and carry nothing from call to
  *                  call.  Calls that share a workspace must not overlap.
  *   other arguments, supported shapes, skipped sequences and blocks as
  *   pkv_chunk_attention.

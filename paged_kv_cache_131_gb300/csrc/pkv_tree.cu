@@ -19,18 +19,20 @@
 // about 128 rows per KV head; the tensor pipe and the exponentials above.
 //
 // Per CTA, warp-specialised, every hand-off an mbarrier with a bounded wait:
-//  * warp 0 walks the stretch, publishes its pieces, stages a piece's query
-//    tile and its keys (tensor copies of 16 rows x 128 bytes, a 3-step ring);
-//    warp 1 stages the values (a 3-step ring);
-//  * warp 2 issues S = Q K^T into one of two score buffers, so the scores of
-//    the next step are computed while the softmax works on this one;
+//  * warp 0 walks the stretch, publishes its pieces and stages their keys
+//    (tensor copies of 16 rows x 128 bytes, a 3-step ring); warp 1 stages the
+//    values (a 3-step ring);
+//  * warp 2 stages a piece's query tile and issues S = Q K^T into one of two
+//    score buffers, so the scores of the next step are computed while the
+//    softmax works on this one;
 //  * warps 3-10, two threads per row: the softmax of the chunk kernel (running
 //    reference maximum that moves by more than 2^8 only, fp16 weights back to
 //    tensor memory), with the tree's mask;
 //  * warp 11 issues O += P V.  Value rows behind the sequence's end hold
-//    anything and are zeroed first; drafted rows may be masked for some query
-//    rows, and 0 x NaN is NaN, so their non-finite elements are zeroed too and
-//    added, where visible, when the piece's O is read out.
+//    anything and are zeroed first (by the softmax warps); drafted rows may be
+//    masked for some query rows, and 0 x NaN is NaN, so their non-finite
+//    elements are zeroed too and added, where visible, when the piece's O is
+//    read out.
 // Rows of a tile past the last drafted one cost no softmax work: a warp whose
 // 16 rows are all past it only passes the barriers on.
 //
@@ -184,12 +186,10 @@ constexpr int kMergeRows = 8;
 
 // What a stretch's first border says about the item it falls into.
 struct Border {
-    int64_t item0;  // the item's first unit
-    int64_t units;  // units of the whole list
-    int32_t steps;  // the item's steps; 0: the border cuts no item, or is not
-                    // the item's first border
-    int32_t rows;   // query rows of the tile
-    int32_t q0;     // first query token of the tile
+    int32_t pieces;  // of the item; 0: the border cuts none, or is not the
+                     // item's first border
+    int32_t rows;    // query rows of the tile
+    int32_t q0;      // first query token of the tile
     int32_t kvh;
 };
 
@@ -205,11 +205,15 @@ struct TileParams {
 
 // A piece as warp 0 hands it to the other warps: steps [step0, step0 + nsteps)
 // of an item.
-struct Piece {
+struct PieceHead {
     int seq, kvh, tile, step0;
     int nsteps, nblk, L, Q;
     int q0, slot, done, pad;  // slot: partial state, or -1 for a whole item
 };
+struct Piece : PieceHead {
+    int ids[32];  // of the piece's first blocks (-1: none, or out of range)
+};
+constexpr int kValidRing = 8;  // steps whose blocks' validity is kept (see the softmax)
 
 template <int D>
 struct Geo {
@@ -224,9 +228,10 @@ struct Geo {
     static constexpr int kBars = 4 + 2 + 2 * kKStages + 2 * kVStages + 4 + 4 + 2;
     static constexpr int kOffPiece = kOffBar + kBars * 8;
     static constexpr int kOffFlags = kOffPiece + 2 * static_cast<int>(sizeof(Piece));
-    static constexpr int kOffMisc = kOffFlags + kFlagWords * 4;
+    static constexpr int kOffValid = kOffFlags + 3 * kFlagWords * 4;  // (see the softmax)
+    static constexpr int kOffMisc = kOffValid + kValidRing * 4;
     static constexpr int kOffScan = kOffMisc + 16;  // the prologue's words
-    static constexpr int kBytes = kOffScan + (kTileThreads / 32 + 2) * 8;
+    static constexpr int kBytes = kOffScan + (kTileThreads / 32 + 4) * 8;
 };
 
 int tile_smem_bytes(int D) {
@@ -297,11 +302,30 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     return d;
 }
 
-// 32 bytes to global memory (32-byte aligned).
-__device__ __forceinline__ void store32(void *dst, const uint32_t (&r)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
+// Transposes N x N 16-byte elements held by groups of N lanes (N = 4 or 8):
+// afterwards element c of lane t of a group is element t of the group's lane c.
+template <int N>
+__device__ __forceinline__ void lane_transpose(uint4 (&x)[N], int lane) {
+#pragma unroll
+    for (int m = 1; m < N; m <<= 1) {
+        const bool up = lane & m;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (i & m) continue;
+            uint4 &lo = x[i], &hi = x[i | m];
+            uint4 s = up ? lo : hi;
+            s.x = __shfl_xor_sync(0xffffffffu, s.x, m);
+            s.y = __shfl_xor_sync(0xffffffffu, s.y, m);
+            s.z = __shfl_xor_sync(0xffffffffu, s.z, m);
+            s.w = __shfl_xor_sync(0xffffffffu, s.w, m);
+            if (up) lo = s;
+            else hi = s;
+        }
+    }
+}
+
+__device__ __forceinline__ void prefetch_l1(const void *p) {
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
 }
 
 // Units of an item: its steps and kItemUnits for its start-up.
@@ -313,14 +337,19 @@ __device__ __forceinline__ int step_at(int64_t x, int steps) {
     return s <= 0 ? 0 : s >= steps ? steps : static_cast<int>(s);
 }
 
-// First unit of CTA c's stretch.
-__device__ __forceinline__ int64_t stretch(int64_t units, int c, int ctas) {
-    return units * c / ctas;
+// First unit of CTA c's stretch, of `busy` = min(CTAs, units) that have one
+// (so no stretch is empty).
+__device__ __forceinline__ int64_t stretch(int64_t units, int c, int busy) {
+    return units * c / busy;
 }
 
 struct SeqGeo {
     int L, Q, q0, tiles, steps;
 };
+
+__device__ __forceinline__ SeqGeo make_geo(int L, int Q, int q0, int G) {
+    return SeqGeo{L, Q, q0, (Q * G + kRows - 1) / kRows, (L + kStepKeys - 1) / kStepKeys};
+}
 
 // Geometry of sequence s; false if it has no rows or is invalid (recorded when
 // `report`).
@@ -334,11 +363,7 @@ __device__ __forceinline__ bool seq_geo(const TreeParams &p, int s, int G, bool 
         if (report) record_error(p.err, PKV_DEVERR_SEQ_LEN, s);
         return false;
     }
-    sg.L = L;
-    sg.Q = Q;
-    sg.q0 = q0;
-    sg.tiles = (Q * G + kRows - 1) / kRows;
-    sg.steps = (L + kStepKeys - 1) / kStepKeys;
+    sg = make_geo(L, Q, q0, G);
     return Q > 0;
 }
 
@@ -392,6 +417,60 @@ __device__ __forceinline__ uint64_t visible(const uint64_t *mask, int words, int
     return n >= 64 ? m : n <= 0 ? 0ull : m & ((1ull << n) - 1);
 }
 
+// Byte offset of 16-byte unit i (row-major) of a staged value tile.
+template <int CH>
+__device__ __forceinline__ int v_unit(int i) {
+    const int t = i / (8 * CH), u = i % (8 * CH);
+    return (t >> 4) * (CH * kBS * 128) + (u >> 3) * (kBS * 128) + (t & 15) * 128 + (u & 7) * 16;
+}
+
+// The fp16 pair w with infinities and NaN zeroed.
+__device__ __forceinline__ uint32_t finite_halves(uint32_t w) {
+    if ((w & 0x7C00u) == 0x7C00u) w &= 0xFFFF0000u;
+    if ((w & 0x7C000000u) == 0x7C000000u) w &= 0x0000FFFFu;
+    return w;
+}
+
+// The value tile `vb` of a step that reaches past the context: rows at and past
+// the sequence's end hold anything and are zeroed; of the drafted rows (key ctx
+// on) the non-finite elements are zeroed and the row flagged.  `keys` of the
+// step's keys, the first of them key0, are staged; thread i of kScanners.  A
+// unit is 16 bytes, kScan of them in flight per thread.
+constexpr int kScanners = kSoftmaxWarps * 32;
+template <int CH>
+__device__ __forceinline__ void clean_values(uint8_t *vb, int key0, int keys, int ctx, int L,
+                                             uint32_t *flags, int thread) {
+    constexpr int kUnits = 8 * CH;  // units of a row
+    constexpr int kScan = 4;
+    const int end = keys * kUnits;
+    for (int i0 = max(ctx - key0, 0) * kUnits + thread; i0 < end; i0 += kScanners * kScan) {
+        uint4 x[kScan];
+#pragma unroll
+        for (int k = 0; k < kScan; ++k)
+            x[k] = *reinterpret_cast<const uint4 *>(vb + v_unit<CH>(min(i0 + kScanners * k, end - 1)));
+#pragma unroll
+        for (int k = 0; k < kScan; ++k) {
+            const int i = i0 + kScanners * k;
+            const int key = key0 + i / kUnits;
+            // all ones in an exponent carry into its sign's place
+            const uint32_t bad = (((x[k].x & 0x7C007C00u) + 0x04000400u) |
+                                  ((x[k].y & 0x7C007C00u) + 0x04000400u) |
+                                  ((x[k].z & 0x7C007C00u) + 0x04000400u) |
+                                  ((x[k].w & 0x7C007C00u) + 0x04000400u)) & 0x80008000u;
+            if (i >= end || (bad == 0 && key < L)) continue;
+            uint4 *at = reinterpret_cast<uint4 *>(vb + v_unit<CH>(i));
+            if (key >= L) {
+                *at = make_uint4(0u, 0u, 0u, 0u);
+            } else {
+                *at = make_uint4(finite_halves(x[k].x), finite_halves(x[k].y),
+                                 finite_halves(x[k].z), finite_halves(x[k].w));
+                atomicOr(&flags[(key - ctx) >> 5], 1u << ((key - ctx) & 31));
+            }
+        }
+    }
+    fence_proxy_async_smem();
+}
+
 // Block id of entry b of a sequence, or -1 when out of range (recorded when
 // `report`).
 __device__ __forceinline__ int block_id(const TreeParams &p, int seq, int b, bool report) {
@@ -416,9 +495,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const Bars br{sb + Gm::kOffBar};
     Piece *pieces = reinterpret_cast<Piece *>(smem + Gm::kOffPiece);
     uint32_t *flags = reinterpret_cast<uint32_t *>(smem + Gm::kOffFlags);
+    volatile uint32_t *valid = reinterpret_cast<volatile uint32_t *>(smem + Gm::kOffValid);
     volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(smem + Gm::kOffMisc);
     int64_t *scan = reinterpret_cast<int64_t *>(smem + Gm::kOffScan);
-    volatile int64_t *start = scan + kTileThreads / 32;  // sequence, its first unit
+    volatile int64_t *start = scan + kTileThreads / 32;  // sequence, its first unit, L | Q, q0
 
     const int Hk = p.num_kv_heads, H = p.num_heads;
     const int G = H / Hk, logG = __ffs(G) - 1;
@@ -428,7 +508,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int s = 0; s < 2; ++s) {
             mbar_init(br.piece_full(s), 1);
             mbar_init(br.piece_empty(s), kPieceReaders);
-            mbar_init(br.s_full(s), 1);
+            mbar_init(br.s_full(s), 2);
             mbar_init(br.s_free(s), kSoftmaxWarps);
             mbar_init(br.p_full(s), kSoftmaxWarps);
             mbar_init(br.pv_done(s), 1);
@@ -444,12 +524,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             mbar_init(br.v_empty(s), 1);
         }
         mbar_init(br.o_free(), kSoftmaxWarps);
-        mbar_init(br.scanned(), 1);
+        mbar_init(br.scanned(), kSoftmaxWarps);
         fence_mbarrier_init();
         prefetch_tensormap(&tp.tm_k);
         prefetch_tensormap(&tp.tm_v);
         prefetch_tensormap(&tp.tm_q);
     }
+    if (threadIdx.x < 3 * kFlagWords) flags[threadIdx.x] = 0;
     if (warp == 2) {
         tc::tmem_alloc(sb + Gm::kOffMisc, kTmemCols);
         tc::tmem_relinquish();
@@ -457,8 +538,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     grid_dependency_wait();
     grid_launch_dependents();  // the merge: it waits for this grid
 
-    // ---- the list's length, and where this CTA's stretch starts
+    // ---- the list's length, and where this CTA's stretch starts: the thread
+    // that holds the sequence its first unit falls into says so (with more
+    // sequences than threads, in a second pass)
     int64_t units = 0;
+    const bool one_pass = p.num_seqs <= kTileThreads;
     for (int s0 = 0; s0 < p.num_seqs; s0 += kTileThreads) {
         const int s = s0 + threadIdx.x;
         SeqGeo sg;
@@ -466,17 +550,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         int64_t total;
         const int64_t w = has ? seq_units(sg, Hk) : 0;
         const int64_t before = cta_scan(w, scan, total);
-        if (p.num_seqs <= kTileThreads) {  // the usual case: one pass
-            const int64_t u0 = stretch(total, cta, ctas);
+        units += total;
+        if (one_pass && total > 0) {
+            const int64_t u0 = stretch(total, cta, static_cast<int>(min(static_cast<int64_t>(ctas), total)));
             if (w > 0 && before <= u0 && u0 < before + w) {
                 start[0] = s;
                 start[1] = before;
+                start[2] = static_cast<int64_t>(sg.L) << 32 | static_cast<unsigned>(sg.Q);
+                start[3] = sg.q0;
             }
         }
-        units += total;
     }
-    const int64_t u0 = stretch(units, cta, ctas), u1 = stretch(units, cta + 1, ctas);
-    if (p.num_seqs > kTileThreads) {
+    const int busy = static_cast<int>(min(static_cast<int64_t>(ctas), units));  // CTAs with a stretch
+    const int64_t u0 = busy ? stretch(units, cta, busy) : 0;
+    const int64_t u1 = busy ? stretch(units, cta + 1, busy) : 0;
+    if (!one_pass && cta < busy) {
         int64_t run = 0;
         for (int s0 = 0; s0 < p.num_seqs; s0 += kTileThreads) {
             const int s = s0 + threadIdx.x;
@@ -488,6 +576,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (w > 0 && before <= u0 && u0 < before + w) {
                 start[0] = s;
                 start[1] = before;
+                start[2] = static_cast<int64_t>(sg.L) << 32 | static_cast<unsigned>(sg.Q);
+                start[3] = sg.q0;
             }
             run += total;
         }
@@ -496,62 +586,59 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = misc[0];
-    const int seq0 = static_cast<int>(start[0]);
-    const int64_t seq0_unit = start[1];
-
-    if (units == 0) {
-        if (threadIdx.x == 0) tp.borders[cta].steps = 0;
+    if (cta >= busy) {
+        if (threadIdx.x == 0) tp.borders[cta].pieces = 0;
     } else if (warp == 0) {
         // ===================== pieces, query tiles and keys =====================
-        int seq = seq0;
-        int64_t first = seq0_unit;  // the sequence's first unit
+        int seq = static_cast<int>(start[0]);
+        int64_t first = start[1];  // the sequence's first unit
         int64_t u = u0;
-        SeqGeo sg;
-        seq_geo(p, seq, G, false, sg);
+        SeqGeo sg = make_geo(static_cast<int>(start[2] >> 32), static_cast<int>(start[2]),
+                             static_cast<int>(start[3]), G);
+        // the place of the stretch's start in its item, kept from piece to piece
+        int n = sg.steps + kItemUnits;
+        int item = static_cast<int>((u - first) / n);
+        int x = static_cast<int>(u - first - static_cast<int64_t>(item) * n);
+        // the border at u0, for the merge (every CTA writes one, whether or not
+        // its stretch holds a step)
         if (lane == 0) {
-            // the border at u0, for the merge
-            const int64_t n = sg.steps + kItemUnits;
-            const int item = static_cast<int>((u0 - first) / n);
-            const int64_t a = first + item * n;
-            Border b;
-            b.item0 = a;
-            b.units = units;
-            const bool cuts = step_at(u0 - a, sg.steps) > 0 &&
-                              (cta == 0 || step_at(stretch(units, cta - 1, ctas) - a, sg.steps) == 0);
+            Border border;
+            const int64_t a = u0 - x;
             const int tile = item % sg.tiles;
-            b.steps = cuts ? sg.steps : 0;
-            b.rows = min(kRows, sg.Q * G - tile * kRows);
-            b.q0 = sg.q0 + tile * (kRows >> logG);
-            b.kvh = item / sg.tiles;
-            tp.borders[cta] = b;
+            const bool cuts = cta > 0 && step_at(x, sg.steps) > 0 &&
+                              step_at(stretch(units, cta - 1, busy) - a, sg.steps) == 0;
+            // pieces: the CTA before this one, and those up to the item's last unit
+            border.pieces =
+                cuts ? static_cast<int>(((a + n) * busy - 1) / units) - (cta - 1) + 1 : 0;
+            border.rows = min(kRows, sg.Q * G - tile * kRows);
+            border.q0 = sg.q0 + tile * (kRows >> logG);
+            border.kvh = item / sg.tiles;
+            tp.borders[cta] = border;
         }
-        int gs = 0;  // steps staged
-        bool ok = true;
-        for (int it = 0; ok;) {
-            // the next piece
-            Piece pc;
+        __syncwarp();
+        // The next piece of the stretch, and the ids of its first blocks.
+        auto next_piece = [&](PieceHead &pc, int &ids) {
             pc.done = 1;
+            ids = -1;
             while (u < u1) {
-                const int64_t n = sg.steps + kItemUnits;
-                const int64_t item = (u - first) / n;
-                if (item >= static_cast<int64_t>(Hk) * sg.tiles) {  // the next sequence with rows
-                    first += seq_units(sg, Hk);
-                    do ++seq;
-                    while (seq < p.num_seqs && !seq_geo(p, seq, G, false, sg));
-                    if (seq >= p.num_seqs) {  // (not reached: u1 is inside the list)
-                        u = u1;
-                        break;
+                if (x == n) {  // the next item
+                    x = 0;
+                    if (++item == Hk * sg.tiles) {  // of the next sequence with rows
+                        item = 0;
+                        do ++seq;
+                        while (seq < p.num_seqs && !seq_geo(p, seq, G, false, sg));
+                        if (seq >= p.num_seqs) return;  // (not reached: u1 is inside the list)
+                        n = sg.steps + kItemUnits;
                     }
-                    continue;
                 }
-                const int64_t a = first + item * n;
-                const int64_t end = min(u1, a + n);
-                const int s0 = step_at(u - a, sg.steps), s1 = step_at(end - a, sg.steps);
-                u = end;
+                const int take = static_cast<int>(min(u1 - u, static_cast<int64_t>(n - x)));
+                const int s0 = step_at(x, sg.steps), s1 = step_at(x + take, sg.steps);
+                u += take;
+                x += take;
                 if (s1 == s0) continue;
                 pc.seq = seq;
-                pc.kvh = static_cast<int>(item) / sg.tiles;
-                pc.tile = static_cast<int>(item) % sg.tiles;
+                pc.kvh = item / sg.tiles;
+                pc.tile = item - pc.kvh * sg.tiles;
                 pc.step0 = s0;
                 pc.nsteps = s1 - s0;
                 pc.nblk = min((sg.L + kBS - 1) / kBS - s0 * kStepBlocks, pc.nsteps * kStepBlocks);
@@ -560,54 +647,64 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 pc.q0 = sg.q0;
                 pc.slot = s0 == 0 && s1 == sg.steps ? -1 : 2 * cta + (s0 == 0);
                 pc.done = 0;
-                break;
+                if (lane < pc.nblk) ids = block_id(p, seq, s0 * kStepBlocks + lane, true);
+                return;
             }
+        };
+        PieceHead cur;
+        int cur_ids;
+        next_piece(cur, cur_ids);
+        int gs = 0;  // steps staged
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
             const int rec = it & 1;
             if (it >= 2 && !wait_all(br.piece_empty(rec), ((it >> 1) - 1) & 1)) {
                 ok = false;
                 break;
             }
-            if (lane == 0) {
-                pieces[rec] = pc;
-                mbar_arrive(br.piece_full(rec));
-            }
-            if (pc.done) break;
-            // its query tile, once the previous piece's last scores are done
-            if (it >= 1 && !wait_all(br.q_empty(), (it - 1) & 1)) {
-                ok = false;
-                break;
-            }
-            if (lane == 0) mbar_arrive_expect_tx(br.q_full(), Gm::kQ);
+            pieces[rec].ids[lane] = cur_ids;
+            if (lane == 0) static_cast<PieceHead &>(pieces[rec]) = cur;
             __syncwarp();
-            if (lane < CH)
-                tensor_g2s_3d(sb + lane * (kRows * 128), &tp.tm_q, 128 * lane, pc.kvh * G,
-                              pc.q0 + pc.tile * (kRows >> logG), br.q_full());
-            ++it;
-            // its keys: the ids of 32 blocks at a time, one per lane
-            const int b0 = pc.step0 * kStepBlocks;
-            int ids = lane < pc.nblk ? block_id(p, pc.seq, b0 + lane, true) : -1;
-            for (int n = 0; n < pc.nsteps; ++n, ++gs) {
+            if (lane == 0) mbar_arrive(br.piece_full(rec));
+            if (cur.done) break;
+            // its keys: the ids of 32 blocks at a time, one per lane, the next
+            // ones -- of this piece or the next -- looked up a window ahead
+            const int b0 = cur.step0 * kStepBlocks;
+            PieceHead nxt;
+            int nxt_ids = -1, ids = cur_ids, ahead = -1;
+            for (int n = 0; n < cur.nsteps; ++n, ++gs) {
                 const int ks = gs % kKStages;
                 const int at = n * kStepBlocks;
-                if (at != 0 && (at & 31) == 0)
-                    ids = at + lane < pc.nblk ? block_id(p, pc.seq, b0 + at + lane, true) : -1;
+                if ((at & 31) == 0) {
+                    if (at != 0) ids = ahead;
+                    const int b = at + 32 + lane;
+                    ahead = b < cur.nblk ? block_id(p, cur.seq, b0 + b, true) : -1;
+                }
                 if (gs >= kKStages && !wait_all(br.k_empty(ks), ((gs / kKStages) - 1) & 1)) {
                     ok = false;
                     break;
                 }
-                const int nb = min(kStepBlocks, pc.nblk - at);
-                if (lane == 0) mbar_arrive_expect_tx(br.k_full(ks), nb * CH * kBS * 128);
-                __syncwarp();
+                const int nb = min(kStepBlocks, cur.nblk - at);
                 // lane l: block l / CH of the step, chunk l % CH (a bad block
                 // reads rows before the cache: zeros)
                 const int b = min(lane / CH, kStepBlocks - 1), c = lane % CH;
                 const int id = __shfl_sync(0xffffffffu, ids, (at & 31) + b);
+                const uint32_t good = __ballot_sync(0xffffffffu, id >= 0 || lane >= nb * CH);
+                if (lane == 0) {
+                    valid[gs % kValidRing] = good;
+                    mbar_arrive_expect_tx(br.k_full(ks), nb * CH * kBS * 128);
+                }
+                __syncwarp();
                 if (lane < nb * CH)
                     tensor_g2s_3d(sb + Gm::kOffK + ks * Gm::kK + c * (kStepKeys * 128) +
                                       b * (kBS * 128),
-                                  &tp.tm_k, 0, id >= 0 ? id * kBS : -kBS, pc.kvh * CH + c,
+                                  &tp.tm_k, 0, id >= 0 ? id * kBS : -kBS, cur.kvh * CH + c,
                                   br.k_full(ks));
+                // (when the ring is full: the look-ups wait for memory)
+                if (n == min(kKStages, cur.nsteps) - 1) next_piece(nxt, nxt_ids);
             }
+            cur = nxt;
+            cur_ids = nxt_ids;
         }
         if (!ok) {
             if (lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT, cta);
@@ -627,17 +724,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 ok = false;
                 break;
             }
-            const Piece pc = pieces[rec];
+            const PieceHead pc = pieces[rec];
+            int ids = pieces[rec].ids[lane];
             __syncwarp();
             if (lane == 0) mbar_arrive(br.piece_empty(rec));
             if (pc.done) break;
             const int b0 = pc.step0 * kStepBlocks;
-            int ids = lane < pc.nblk ? block_id(p, pc.seq, b0 + lane, false) : -1;
+            int ahead = -1;
             for (int n = 0; n < pc.nsteps; ++n, ++gs) {
                 const int vs = gs % kVStages;
                 const int at = n * kStepBlocks;
-                if (at != 0 && (at & 31) == 0)
-                    ids = at + lane < pc.nblk ? block_id(p, pc.seq, b0 + at + lane, false) : -1;
+                if ((at & 31) == 0) {
+                    if (at != 0) ids = ahead;
+                    const int b = at + 32 + lane;
+                    ahead = b < pc.nblk ? block_id(p, pc.seq, b0 + b, false) : -1;
+                }
                 if (gs >= kVStages && !wait_all(br.v_empty(vs), ((gs / kVStages) - 1) & 1)) {
                     ok = false;
                     break;
@@ -659,8 +760,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
         }
     } else if (warp == 2) {
-        // ============================ score MMAs ============================
-        int gs = 0;
+        // ==================== query tiles and score MMAs ====================
+        int gs = 0, q_staged = 0;
         bool ok = true;
         for (int it = 0; ok; ++it) {
             const int rec = it & 1;
@@ -668,10 +769,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 ok = false;
                 break;
             }
-            const int done = pieces[rec].done, nsteps = pieces[rec].nsteps, nblk = pieces[rec].nblk;
+            const PieceHead pc = pieces[rec];
+            const int nsteps = pc.nsteps, nblk = pc.nblk;
             __syncwarp();
             if (lane == 0) mbar_arrive(br.piece_empty(rec));
-            if (done) break;
+            if (pc.done) break;
+            // the query tile, once the previous piece's last scores are done
+            if (it >= 1) ok = wait_all(br.q_empty(), (it - 1) & 1);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(br.q_full(), Gm::kQ);
+            __syncwarp();
+            if (lane < CH)
+                tensor_g2s_3d(sb + lane * (kRows * 128), &tp.tm_q, 128 * lane, pc.kvh * G,
+                              pc.q0 + pc.tile * (kRows >> logG), br.q_full());
+            q_staged = it + 1;
             ok = wait_all(br.q_full(), it & 1);
             for (int n = 0; n < nsteps && ok; ++n, ++gs) {
                 const int ks = gs % kKStages, b = gs & 1;
@@ -693,13 +804,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                                                  16, 1024, tc::kSwizzle128B),
                                    idesc, kk > 0);
                     tc::commit(br.s_full(b));
+                    mbar_arrive(br.s_full(b));  // passes the step's validity on
                     tc::commit(br.k_empty(ks));
                     if (n == nsteps - 1) tc::commit(br.q_empty());
                 }
                 __syncwarp();
             }
         }
-        if (!ok && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT, cta);
+        if (!ok) {
+            if (lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT, cta);
+            if (q_staged) mbar_wait_bounded(br.q_full(), (q_staged - 1) & 1);
+        }
     } else if (warp == kPVWarp) {
         // ============================= P V MMAs =============================
         constexpr uint32_t kIdescPV = tc::idesc_f16_f32(kRows, D, false, true);
@@ -711,64 +826,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 ok = false;
                 break;
             }
-            const Piece pc = pieces[rec];
+            const PieceHead pc = pieces[rec];
             __syncwarp();
             if (lane == 0) mbar_arrive(br.piece_empty(rec));
             if (pc.done) break;
-            const int ctx = pc.L - pc.Q;
             for (int n = 0; n < pc.nsteps && ok; ++n, ++gs) {
                 const int vs = gs % kVStages, b = gs & 1;
                 const int nb = min(kStepBlocks, pc.nblk - n * kStepBlocks);
-                // the previous piece's O and flags have been read
-                if (n == 0) {
-                    if (it > 0) ok = wait_all(br.o_free(), (it - 1) & 1);
-                    if (!ok) break;
-                    if (lane < kFlagWords) flags[lane] = 0;
-                    __syncwarp();
-                }
-                ok = wait_all(br.v_full(vs), (gs / kVStages) & 1);
+                // the previous piece's O has been read
+                if (n == 0 && it > 0) ok = wait_all(br.o_free(), (it - 1) & 1);
+                if (ok) ok = wait_all(br.v_full(vs), (gs / kVStages) & 1);
                 if (!ok) break;
                 const uint32_t v_s = sb + Gm::kOffV + vs * Gm::kV;
-                const int key0 = (pc.step0 + n) * kStepKeys;
-                if (key0 + nb * kBS > ctx) {
-                    // rows at and past the end: zeroed; drafted rows: their
-                    // non-finite elements zeroed and the row flagged
-                    uint8_t *vb = smem + Gm::kOffV + vs * Gm::kV;
-                    const int r0 = max(ctx - key0, 0);
-                    constexpr int kUnits = 8 * CH;  // 16-byte units of a row
-                    for (int i = r0 * kUnits + lane; i < nb * kBS * kUnits; i += 32) {
-                        const int t = i / kUnits, un = i % kUnits;
-                        uint4 *at = reinterpret_cast<uint4 *>(
-                            vb + (t >> 4) * Gm::kVBlock + (un >> 3) * (kBS * 128) + (t & 15) * 128 +
-                            (un & 7) * 16);
-                        const int key = key0 + t;
-                        if (key >= pc.L) {
-                            *at = make_uint4(0u, 0u, 0u, 0u);
-                        } else {
-                            uint4 x = *at;
-                            uint32_t *w = reinterpret_cast<uint32_t *>(&x);
-                            bool bad = false;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                if ((w[e] & 0x7C00u) == 0x7C00u) {
-                                    w[e] &= 0xFFFF0000u;
-                                    bad = true;
-                                }
-                                if ((w[e] & 0x7C000000u) == 0x7C000000u) {
-                                    w[e] &= 0x0000FFFFu;
-                                    bad = true;
-                                }
-                            }
-                            if (bad) {
-                                *at = x;
-                                atomicOr(&flags[(key - ctx) >> 5], 1u << ((key - ctx) & 31));
-                            }
-                        }
-                    }
-                    fence_proxy_async_smem();
-                }
-                __syncwarp();
-                if (n == pc.nsteps - 1 && lane == 0) mbar_arrive(br.scanned());
                 ok = wait_all(br.p_full(b), (gs >> 1) & 1);
                 if (!ok) break;
                 tc::fence_after_sync();
@@ -801,7 +870,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 ok = false;
                 break;
             }
-            const Piece pc = pieces[rec];
+            const PieceHead pc = pieces[rec];
             __syncwarp();
             if (lane == 0) mbar_arrive(br.piece_empty(rec));
             if (pc.done) break;
@@ -812,29 +881,35 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const int j = rr >> logG;
             const uint64_t *mask =
                 row_ok ? p.mask + static_cast<int64_t>(pc.q0 + j) * p.mask_words : nullptr;
+            // bring the row's mask near, for the step that needs it
+            if (row_ok) prefetch_l1(mask);
+            uint32_t *my_flags = flags + (it % 3) * kFlagWords;
             float m_used = -INFINITY, l = 0.f;  // l: this thread's keys only
 
             for (int n = 0; n < pc.nsteps; ++n, ++gs) {
                 const int sbuf = gs & 1;
-                const int at = n * kStepBlocks;
-                const int nb = min(kStepBlocks, pc.nblk - at);
                 const int key0 = (pc.step0 + n) * kStepKeys;
-                // the step's blocks in range, and this thread's visible keys:
-                // looked up while the scores are computed
-                const bool good = lane >= nb || block_id(p, pc.seq, pc.step0 * kStepBlocks + at + min(lane, nb - 1), false) >= 0;
-                const uint32_t blocks = __ballot_sync(0xffffffffu, good);
-                const bool fast = blocks == 0xffffffffu && key0 + kStepKeys <= ctx && sl2 >= 0.f;
-                uint64_t vis = ~0ull;
-                if (!fast && live) {
-                    vis = visible(mask, p.mask_words, key0 + kHalfKeys * h, ctx, pc.L);
-#pragma unroll
-                    for (int b = 0; b < 4; ++b)
-                        if (!((blocks >> (4 * h + b)) & 1u)) vis &= ~(0xFFFFull << (16 * b));
+                if (key0 + kStepKeys > ctx) {
+                    const int vs = gs % kVStages;
+                    if (!wait_all(br.v_full(vs), (gs / kVStages) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    clean_values<CH>(smem + Gm::kOffV + vs * Gm::kV, key0,
+                                     min(kStepBlocks, pc.nblk - n * kStepBlocks) * kBS, ctx, pc.L,
+                                     my_flags, threadIdx.x - 3 * 32);
+                    __syncwarp();
                 }
+                if (n == pc.nsteps - 1 && lane == 0) mbar_arrive(br.scanned());
                 if (!wait_all(br.s_full(sbuf), (gs >> 1) & 1)) {
                     ok = false;
                     break;
                 }
+                // the step's blocks that are in range: the key producer's word,
+                // one bit per copy (the ring is longer than it can be ahead:
+                // it stages at most kKStages steps past the scores, and these
+                // are at most two ahead of this warp)
+                const uint32_t copies = valid[gs % kValidRing];
                 if (!live) {
                     // (its rows of the weight buffer hold anything: they reach
                     // its rows of O alone; it keeps pace with the other warps,
@@ -857,7 +932,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(br.s_free(sbuf));
+                const bool fast = copies == 0xffffffffu && key0 + kStepKeys <= ctx && sl2 >= 0.f;
                 if (!fast) {
+                    uint64_t vis = visible(mask, p.mask_words, key0 + kHalfKeys * h, ctx, pc.L);
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                        if (!((copies >> (CH * (4 * h + b))) & 1u)) vis &= ~(0xFFFFull << (16 * b));
 #pragma unroll
                     for (int e = 0; e < kHalfKeys; ++e) {
                         const uint32_t w = e < 32 ? static_cast<uint32_t>(vis)
@@ -946,6 +1026,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 ok = false;
                 break;
             }
+            // the flags of the piece after the next one: every warp has read
+            // what they held for the previous piece, and none reaches that
+            // piece before this warp's arrivals for the next
+            if (warp == 3 && lane < kFlagWords) flags[(it + 2) % 3 * kFlagWords + lane] = 0;
+            __syncwarp();
             if (!live) {
                 if (lane == 0) mbar_arrive(br.o_free());
                 continue;
@@ -962,61 +1047,81 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
                 for (int d = 0; d < DH; ++d) o[d] = __uint_as_float(ob[d]);
             }
-            uint32_t flagged[kFlagWords];
-            bool any = false;
+            uint32_t any = 0;
 #pragma unroll
-            for (int w = 0; w < kFlagWords; ++w) {
-                flagged[w] = flags[w];
-                any = any || flagged[w] != 0;
+            for (int w = 0; w < kFlagWords; ++w) any |= my_flags[w];
+            if (any != 0 && row_ok) {
+                // the elements that were left out: a weight times an infinity
+                // or a NaN is that, whatever the (positive) weight
+                for (int node = 0; node < pc.Q; ++node) {
+                    if (!((my_flags[node >> 5] >> (node & 31)) & 1u) ||
+                        !((__ldg(mask + (node >> 6)) >> (node & 63)) & 1))
+                        continue;
+                    const int key = ctx + node;
+                    const int id = block_id(p, pc.seq, key / kBS, false);
+                    if (id < 0) continue;
+                    const __half *v = static_cast<const __half *>(p.v_cache) +
+                                      ((static_cast<int64_t>(id) * kBS + key % kBS) * Hk + pc.kvh) * D +
+                                      DH * h;
+#pragma unroll
+                    for (int d = 0; d < DH; ++d) {
+                        const float x = __half2float(v[d]);
+                        if (!isfinite(x)) o[d] += x;
+                    }
+                }
             }
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(br.o_free());
             l += __shfl_xor_sync(0xffffffffu, l, 16);  // the row's sum over both halves' keys
-            if (any && row_ok) {
-                // the elements that were left out: a weight times an infinity
-                // or a NaN is that, whatever the (positive) weight
-                for (int w = 0; w < kFlagWords; ++w)
-                    for (uint32_t bits = flagged[w]; bits; bits &= bits - 1) {
-                        const int node = 32 * w + __ffs(bits) - 1;
-                        if (!((__ldg(mask + node / 64) >> (node & 63)) & 1)) continue;
-                        const int key = ctx + node;
-                        const int id = block_id(p, pc.seq, key / kBS, false);
-                        if (id < 0) continue;
-                        const __half *v = static_cast<const __half *>(p.v_cache) +
-                                          ((static_cast<int64_t>(id) * kBS + key % kBS) * Hk + pc.kvh) * D +
-                                          DH * h;
-#pragma unroll
-                        for (int d = 0; d < DH; ++d) {
-                            const float x = __half2float(v[d]);
-                            if (!isfinite(x)) o[d] += x;
-                        }
-                    }
-            }
-            if (!row_ok) continue;
+            // a thread holds DH dims of one row: exchanged inside groups of
+            // lanes so that a warp's store covers whole lines of a few rows
+            // (stored as they lie, 32 lanes on 32 lines, an item's outputs
+            // took 3 us and its partial state 6)
+            const int r0 = quarter * 32 + wh * 16;
             if (pc.slot < 0) {
                 const float inv = l > 0.f ? 1.f / l : l;  // (no visible key: 0; NaN stays)
-                __half *dst = p.out + (static_cast<int64_t>(pc.q0 + j) * H + pc.kvh * G +
-                                       (rr & (G - 1))) * D + DH * h;
+                constexpr int NC = DH / 8;  // 16-byte pieces of a thread's fp16 dims
+                uint4 x[NC];
 #pragma unroll
-                for (int c = 0; c < DH / 16; ++c) {
-                    uint32_t x[8];
+                for (int c = 0; c < NC; ++c)
+                    x[c] = make_uint4(pack_half2(o[8 * c] * inv, o[8 * c + 1] * inv),
+                                      pack_half2(o[8 * c + 2] * inv, o[8 * c + 3] * inv),
+                                      pack_half2(o[8 * c + 4] * inv, o[8 * c + 5] * inv),
+                                      pack_half2(o[8 * c + 6] * inv, o[8 * c + 7] * inv));
+                lane_transpose<NC>(x, lane);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        x[e] = pack_half2(o[16 * c + 2 * e] * inv, o[16 * c + 2 * e + 1] * inv);
-                    *reinterpret_cast<uint4 *>(dst + 16 * c) = make_uint4(x[0], x[1], x[2], x[3]);
-                    *reinterpret_cast<uint4 *>(dst + 16 * c + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+                for (int c = 0; c < NC; ++c) {
+                    const int src = (lane & ~(NC - 1)) + c;  // the lane the row came from
+                    const int row = pc.tile * kRows + r0 + (src & 15);
+                    if (row < pc.Q * G)
+                        *reinterpret_cast<uint4 *>(
+                            p.out + (static_cast<int64_t>(pc.q0 + (row >> logG)) * H + pc.kvh * G +
+                                     (row & (G - 1))) * D +
+                            DH * (src >> 4) + 8 * (lane & (NC - 1))) = x[c];
                 }
             } else {
-                const int64_t row = static_cast<int64_t>(pc.slot) * kRows + r;
-                if (h == 0) tp.part_ml[row] = make_float2(m_used, l);
-                float *dst = tp.part_o + row * D + DH * h;
+                const int64_t row0 = static_cast<int64_t>(pc.slot) * kRows;
+                if (h == 0 && row_ok) tp.part_ml[row0 + r] = make_float2(m_used, l);
 #pragma unroll
-                for (int c = 0; c < DH / 8; ++c) {
-                    uint32_t x[8];
+                for (int k = 0; k < DH / 32; ++k) {
+                    uint4 x[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = __float_as_uint(o[8 * c + e]);
-                    store32(dst + 8 * c, x);
+                    for (int c = 0; c < 8; ++c)
+                        x[c] = make_uint4(__float_as_uint(o[32 * k + 4 * c]),
+                                          __float_as_uint(o[32 * k + 4 * c + 1]),
+                                          __float_as_uint(o[32 * k + 4 * c + 2]),
+                                          __float_as_uint(o[32 * k + 4 * c + 3]));
+                    lane_transpose<8>(x, lane);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const int src = (lane & ~7) + c;
+                        const int row = r0 + (src & 15);
+                        if (pc.tile * kRows + row < pc.Q * G)
+                            *reinterpret_cast<uint4 *>(tp.part_o + (row0 + row) * D +
+                                                       DH * (src >> 4) + 32 * k + 4 * (lane & 7)) =
+                                x[c];
+                    }
                 }
             }
         }
@@ -1034,46 +1139,41 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
 // Merges the partial states of the items that stretch borders cut: block
 // (b, y) takes rows kMergeRows y .. of the item that border b + 1 is the first
-// to cut.  D/8 threads per row, 8 dims each; the item's pieces are those of the
-// CTAs from b on whose stretch holds some of its steps.
+// to cut.  D/8 threads per row, 8 dims each.  The item's first piece is the
+// last one of CTA b (its second slot), the others the first ones of the CTAs
+// that follow.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads)
-    tree_merge_kernel(const __grid_constant__ TileParams tp, int ctas) {
+    tree_merge_kernel(const __grid_constant__ TileParams tp) {
     constexpr int kPerRow = D / 8;
     constexpr int kPass = kMergeThreads / kPerRow;  // rows at a time
     grid_dependency_wait();
-    const int c0 = blockIdx.x;  // the CTA that holds the item's first steps
+    const int c0 = blockIdx.x;
     const Border b = tp.borders[c0 + 1];
-    if (b.steps == 0) return;
+    if (b.pieces == 0) return;
     const TreeParams &p = tp.t;
     const int G = p.num_heads / p.num_kv_heads, logG = __ffs(G) - 1;
-    const int last = static_cast<int>(((b.item0 + b.steps + kItemUnits) * ctas - 1) / b.units);
     for (int rr = blockIdx.y * kMergeRows + threadIdx.x / kPerRow;
          rr < min(b.rows, static_cast<int>(blockIdx.y + 1) * kMergeRows); rr += kPass) {
         const int d0 = 8 * (threadIdx.x % kPerRow);
         float M = -INFINITY, den = 0.f, o[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = 0.f;
-        // pieces c0 .. last; the first one's state is in its CTA's second slot
-        for (int c = c0; c <= last; ++c) {
-            const int s0 = step_at(stretch(b.units, c, ctas) - b.item0, b.steps);
-            const int s1 = step_at(stretch(b.units, c + 1, ctas) - b.item0, b.steps);
-            if (s0 == s1) continue;
-            const int64_t row = static_cast<int64_t>(2 * c + (s0 == 0)) * kRows + rr;
+#pragma unroll 8
+        for (int i = 0; i < b.pieces; ++i) {
+            const int64_t row = static_cast<int64_t>(2 * (c0 + i) + (i == 0)) * kRows + rr;
             M = fmaxf(M, __ldcg(tp.part_ml + row).x);
         }
-        for (int c = c0; c <= last; ++c) {
-            const int s0 = step_at(stretch(b.units, c, ctas) - b.item0, b.steps);
-            const int s1 = step_at(stretch(b.units, c + 1, ctas) - b.item0, b.steps);
-            if (s0 == s1) continue;
-            const int64_t row = static_cast<int64_t>(2 * c + (s0 == 0)) * kRows + rr;
+#pragma unroll 4
+        for (int i = 0; i < b.pieces; ++i) {
+            const int64_t row = static_cast<int64_t>(2 * (c0 + i) + (i == 0)) * kRows + rr;
             const float2 ml = __ldcg(tp.part_ml + row);
+            const float4 x = __ldcg(reinterpret_cast<const float4 *>(tp.part_o + row * D + d0));
+            const float4 y = __ldcg(reinterpret_cast<const float4 *>(tp.part_o + row * D + d0) + 1);
             // (a piece without a visible finite score weighs nothing, but a NaN
             // in its sum or its O stays)
             const float w = ml.x == -INFINITY ? 1.f : ex2(ml.x - M);
             den = fmaf(ml.y, w, den);
-            const float4 x = __ldcg(reinterpret_cast<const float4 *>(tp.part_o + row * D + d0));
-            const float4 y = __ldcg(reinterpret_cast<const float4 *>(tp.part_o + row * D + d0) + 1);
             o[0] = fmaf(x.x, w, o[0]);
             o[1] = fmaf(x.y, w, o[1]);
             o[2] = fmaf(x.z, w, o[2]);
@@ -1143,12 +1243,11 @@ int launch_tiles(const TreeParams &t, int D, void *workspace, cudaStream_t strea
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_failure(e, "tree_tile_kernel launch");
     if (ctas == 1) return PKV_OK;
-    using MergeFn = void (*)(const TileParams, int);
-    const MergeFn merge = D == 128 ? tree_merge_kernel<128> : tree_merge_kernel<64>;
+    const Fn merge = D == 128 ? tree_merge_kernel<128> : tree_merge_kernel<64>;
     cfg.gridDim = dim3(static_cast<unsigned>(ctas - 1), kRows / kMergeRows);
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, merge, p, ctas);
+    e = cudaLaunchKernelEx(&cfg, merge, p);
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? PKV_OK : cuda_failure(e, "tree_merge_kernel launch");
 }
@@ -1181,7 +1280,7 @@ int tree_attention(void *out, const void *q, const void *k_cache, const void *v_
     if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
         !aligned(k_scale, 16) || !aligned(v_scale, 16) || !aligned(block_tables, 4) ||
         !aligned(seq_lens, 4) || !aligned(query_start, 4) || !aligned(tree_mask, 8) ||
-        !aligned(workspace, 32))
+        !aligned(workspace, 16))
         return PKV_ERR_ALIGNMENT;
     const size_t need = pkv_tree_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim,
                                                  num_query_tokens, max_query_len, max_seq_len);
