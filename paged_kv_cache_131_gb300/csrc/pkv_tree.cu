@@ -1,13 +1,12 @@
 // pkv_tree.cu -- attention of a tree of drafted tokens per sequence over the
-// paged cache (fp16 or FP8).
+// paged cache (fp16 or FP8), on the fifth-generation tensor cores.
 //
 // Sequence i holds L tokens, the last Q of them drafted; query row r sees the
 // context 0 .. L-Q-1 and the drafted tokens whose mask bit is set:
 //     out = sum_vis 2^(s_j - m) V_j / sum_vis 2^(s_j - m),
-//     s_j = scale log2(e) q . K_j,  m the running maximum.
+//     s_j = scale log2(e) q . K_j,  m any reference near the largest s_j.
 //
-// fp16 caches: tree_tile_kernel, on the fifth-generation tensor cores.  The
-// rows of a (sequence, KV head) -- drafted token j, head g of the group:
+// The rows of a (sequence, KV head) -- drafted token j, head g of the group:
 // row j*G + g -- are cut into tiles of 128 (the MMA's M), the cache into steps
 // of 128 keys.  The work is the list of (sequence, KV head, tile) items, each
 // its steps plus a start-up cost; one persistent CTA per SM takes an equal
@@ -15,34 +14,42 @@
 // GPU as well as a batch does.  An item cut by a stretch's border leaves fp32
 // partial states (m, l, O) in the workspace, and a second small kernel, whose
 // CTAs start as the first one's leave, merges them.  Bound: HBM while a tile's
-// 128-key step (64 KB of keys and values) costs less than its bytes, i.e. to
-// about 128 rows per KV head; the tensor pipe and the exponentials above.
+// 128-key step (64 KB of fp16 keys and values) costs less than its bytes, i.e.
+// to about 128 rows per KV head; the step's chain of MMAs and softmax above.
 //
 // Per CTA, warp-specialised, every hand-off an mbarrier with a bounded wait:
-//  * warp 0 walks the stretch, publishes its pieces and stages their keys
-//    (tensor copies of 16 rows x 128 bytes, a 3-step ring); warp 1 stages the
-//    values (a 3-step ring);
+//  * warp 0 walks the stretch, publishes its pieces and stages their keys, one
+//    tensor copy per block, in a ring; warp 1 stages the values likewise;
 //  * warp 2 stages a piece's query tile and issues S = Q K^T into one of two
 //    score buffers, so the scores of the next step are computed while the
-//    softmax works on this one;
-//  * warps 3-10, two threads per row: the softmax of the chunk kernel (running
-//    reference maximum that moves by more than 2^8 only, fp16 weights back to
-//    tensor memory), with the tree's mask;
-//  * warp 11 issues O += P V.  Value rows behind the sequence's end hold
-//    anything and are zeroed first (by the softmax warps); drafted rows may be
-//    masked for some query rows, and 0 x NaN is NaN, so their non-finite
-//    elements are zeroed too and added, where visible, when the piece's O is
-//    read out.
+//    softmax works on this one; warp 3 issues O += P V;
+//  * warps 4-11, two threads per row: the softmax.  The reference m moves only
+//    when the maximum grows by more than 2^8 (weights stay <= 256, O is
+//    rescaled in tensor memory first); weights are rounded to fp16 for the MMA
+//    (the normaliser sums them unrounded: the rounding errors are independent
+//    and at most 2^-12 of a weight's step each), with the tree's mask;
+//  * FP8: the rings hold codes, and warps 12-15 turn them into fp16 tiles
+//    (exact) for the MMAs.  A key's scale multiplies its score and its value's
+//    scale the weight, both in fp32; m then also covers the logarithm of the
+//    largest value scale of a step, so the scaled weights stay in fp16's range
+//    whatever the scales are.
+// Value rows behind the sequence's end hold anything and are zeroed before the
+// MMA (by the softmax warps, FP8: as they are converted); drafted rows may be
+// masked for some query rows, and 0 x NaN is NaN, so their non-finite elements
+// are zeroed too and added, where visible, when the piece's O is read out.
 // Rows of a tile past the last drafted one cost no softmax work: a warp whose
 // 16 rows are all past it only passes the barriers on.
 //
-// FP8 caches: tree_rows_kernel, one warp per (query row, head).
+// The kernel's code is kept small (rolled loops where they run once per item):
+// at 88 KB it missed the instruction cache in 27% of its requests, and a step
+// of a short item cost 2.7x what it does in a long one.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -57,9 +64,37 @@ namespace tree {
 namespace {
 
 constexpr int kBS = 16;
-constexpr int kThreads = 128;
+constexpr int kRows = 128;                    // query rows per tile: the MMA's M
+constexpr int kStepBlocks = 8;                // blocks per step
+constexpr int kStepKeys = kStepBlocks * kBS;  // 128 keys: the score MMA's N
+// softmax: warp 4 + 4 wh + q takes rows (tensor-memory lanes) 32 q + 16 wh ..
+// + 15, two threads per row: lanes 16 h + i take keys 64 h .. of a step and
+// the head dimensions (D/2) h .. of O
+constexpr int kSoftmaxWarp = 4;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kHalfKeys = kStepKeys / 2;
+constexpr int kConvertWarp = kSoftmaxWarp + kSoftmaxWarps;
+constexpr int kConvertWarps = 4;
+// tensor memory: O in columns [0, head_dim), two score buffers of 128 columns,
+// two weight buffers (fp16 pairs) of 64
+constexpr int kTmemCols = 512;
+constexpr int kTmemO = 0;
+constexpr int kTmemS = 128;
+constexpr int kTmemP = 384;
+constexpr float kRescaleLog2 = 8.f;  // move the reference past 2^8
+constexpr int kFlagWords = PKV_MAX_TREE_NODES / 32;
+constexpr int kValidRing = 8;  // steps whose blocks' validity is kept (see the softmax)
+constexpr int kScaleRing = 3;  // steps whose scales are kept (see the converters)
+// Units of an item: its steps and kItemUnits for its start-up.
+constexpr int kItemUnits = 1;
+// merge: threads and rows of a block
+constexpr int kMergeThreads = 256;
+constexpr int kMergeRows = 16;
 
 struct TreeParams {
+    CUtensorMap tm_k;
+    CUtensorMap tm_v;
+    CUtensorMap tm_q;  // query rows: 128 bytes of each row of a 128-row tile
     __half *out;
     const __half *q;
     const void *k_cache;
@@ -71,7 +106,8 @@ struct TreeParams {
     const int32_t *query_start;
     const uint64_t *mask;
     int32_t mask_words;
-    float scale_log2;
+    float scale_log2;     // |scale| log2(e), > 0
+    int32_t negate;       // the scale is negative: the MMA negates the scores
     int32_t num_heads;
     int32_t num_kv_heads;
     int32_t num_seqs;
@@ -81,108 +117,10 @@ struct TreeParams {
     int32_t max_seq_len;
     int64_t num_blocks;
     ErrorRecord *err;
+    struct Border *borders;  // [CTAs]
+    float2 *part_ml;         // [2 CTAs][128] (m, l)
+    float4 *part_o;          // [2 CTAs][D / 4][128] four dims each
 };
-
-template <int D>
-__device__ __forceinline__ void load_dims(const void *cache, const float *scale, int64_t row,
-                                          int lane, float (&x)[D / 32]) {
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-        const int64_t at = row * D + lane + 32 * i;
-        __nv_fp8_e4m3 c;
-        c.__x = static_cast<const uint8_t *>(cache)[at];
-        x[i] = static_cast<float>(c) * scale[row];
-    }
-}
-
-template <int D>
-__global__ void __launch_bounds__(kThreads) tree_rows_kernel(const __grid_constant__ TreeParams p) {
-    grid_dependency_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
-    const int H = p.num_heads, Hk = p.num_kv_heads;
-    if (w >= static_cast<int64_t>(p.num_query_tokens) * H) return;
-    const int r = static_cast<int>(w / H), h = static_cast<int>(w % H), kvh = h / (H / Hk);
-    int lo = 0, hi = p.num_seqs - 1;  // the last sequence that starts at or before r
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.query_start[mid] <= r) lo = mid;
-        else hi = mid - 1;
-    }
-    const int q0 = p.query_start[lo], q1 = p.query_start[lo + 1];
-    if (r < q0 || r >= q1) return;
-    const int Q = q1 - q0, L = p.seq_lens[lo];
-    if (L < 0 || L > p.max_seq_len || L > p.max_blocks * kBS || Q > L || Q > p.max_query_len ||
-        q0 < 0 || q1 > p.num_query_tokens) {
-        if (lane == 0) record_error(p.err, PKV_DEVERR_SEQ_LEN, lo);
-        return;
-    }
-    float q[D / 32], o[D / 32];
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-        q[i] = __half2float(p.q[w * D + lane + 32 * i]);
-        o[i] = 0.f;
-    }
-    float m = -INFINITY, l = 0.f;
-    for (int j = 0; j < L; ++j) {
-        if (j >= L - Q) {
-            const int b = j - (L - Q);
-            if (!((p.mask[static_cast<int64_t>(r) * p.mask_words + b / 64] >> (b % 64)) & 1))
-                continue;
-        }
-        const int64_t entry = static_cast<int64_t>(lo) * p.max_blocks + j / kBS;
-        const int64_t id = p.block_tables[entry];
-        if (id < 0 || id >= p.num_blocks) {
-            if (lane == 0) record_error(p.err, PKV_DEVERR_BLOCK_ID, entry);
-            continue;
-        }
-        const int64_t row = (id * kBS + j % kBS) * Hk + kvh;
-        float x[D / 32], s = 0.f;
-        load_dims<D>(p.k_cache, p.k_scale, row, lane, x);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) s = fmaf(q[i], x[i], s);
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        s *= p.scale_log2;
-        if (s == -INFINITY) continue;
-        const float mn = fmaxf(m, s), a = exp2f(m - mn), pr = exp2f(s - mn);
-        load_dims<D>(p.v_cache, p.v_scale, row, lane, x);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) o[i] = fmaf(o[i], a, pr * x[i]);
-        l = fmaf(l, a, pr);
-        m = mn;
-    }
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-        p.out[w * D + lane + 32 * i] = __float2half_rn(l == 0.f ? 0.f : o[i] / l);
-}
-
-// ---------------------------------------------------------------------------
-// The tensor-core kernel.
-
-constexpr int kRows = 128;                    // query rows per tile: the MMA's M
-constexpr int kStepBlocks = 8;                // blocks per step
-constexpr int kStepKeys = kStepBlocks * kBS;  // 128 keys: the score MMA's N
-constexpr int kKStages = 3;                   // key ring depth (steps)
-constexpr int kVStages = 3;                   // value ring depth (steps)
-// softmax: warp 3 + 4 wh + q takes rows (tensor-memory lanes) 32 q + 16 wh ..
-// + 15, two threads per row: lanes 16 h + i take keys 64 h .. of a step and
-// the head dimensions (D/2) h .. of O
-constexpr int kSoftmaxWarps = 8;
-constexpr int kHalfKeys = kStepKeys / 2;
-constexpr int kPVWarp = 3 + kSoftmaxWarps;
-constexpr int kTileThreads = (4 + kSoftmaxWarps) * 32;
-// tensor memory: O in columns [0, head_dim), two score buffers of 128 columns,
-// two weight buffers (fp16 pairs) of 64
-constexpr int kTmemCols = 512;
-constexpr int kTmemO = 0;
-constexpr int kTmemS = 128;
-constexpr int kTmemP = 384;
-constexpr float kRescaleLog2 = 8.f;  // move the reference past 2^8
-constexpr int kFlagWords = PKV_MAX_TREE_NODES / 32;
-// merge: threads per row, rows per block
-constexpr int kMergeThreads = 128;
-constexpr int kMergeRows = 8;
 
 // What a stretch's first border says about the item it falls into.
 struct Border {
@@ -191,16 +129,6 @@ struct Border {
     int32_t rows;    // query rows of the tile
     int32_t q0;      // first query token of the tile
     int32_t kvh;
-};
-
-struct TileParams {
-    CUtensorMap tm_k;  // keys: 128 bytes of 16 rows per copy
-    CUtensorMap tm_v;  // values: a head's chunks of 16 rows per copy
-    CUtensorMap tm_q;  // query rows: 128 bytes of each row of a 128-row tile
-    TreeParams t;
-    Border *borders;  // [CTAs]
-    float2 *part_ml;  // [2 CTAs][128] (m, l)
-    float *part_o;    // [2 CTAs][128][D]
 };
 
 // A piece as warp 0 hands it to the other warps: steps [step0, step0 + nsteps)
@@ -213,32 +141,41 @@ struct PieceHead {
 struct Piece : PieceHead {
     int ids[32];  // of the piece's first blocks (-1: none, or out of range)
 };
-constexpr int kValidRing = 8;  // steps whose blocks' validity is kept (see the softmax)
 
-template <int D>
+template <int D, bool FP8>
 struct Geo {
+    static constexpr int kThreads = (kConvertWarp + (FP8 ? kConvertWarps : 0)) * 32;
     static constexpr int kChunks = D / 64;                // 128-byte chunks of a head row
     static constexpr int kQ = kChunks * kRows * 128;      // [chunk][row][128 B]
-    static constexpr int kK = kChunks * kStepKeys * 128;  // [chunk][key][128 B]
-    static constexpr int kVBlock = kChunks * kBS * 128;   // [chunk][token][128 B]
+    // fp16 tiles, as the MMAs read them: keys [8 rows][chunk][row][128 B],
+    // values [block][chunk][token][128 B]
+    static constexpr int kK = kChunks * kStepKeys * 128;
+    static constexpr int kVBlock = kChunks * kBS * 128;
     static constexpr int kV = kStepBlocks * kVBlock;
+    // the rings the copies fill: fp16 tiles, or codes [block][token][D]
+    static constexpr int kKStages = 3;
+    static constexpr int kVStages = FP8 ? 2 : 3;
+    static constexpr int kBlockBytes = kBS * D * (FP8 ? 1 : 2);
+    static constexpr int kStage = kStepBlocks * kBlockBytes;
     static constexpr int kOffK = kQ;
-    static constexpr int kOffV = kOffK + kKStages * kK;
-    static constexpr int kOffBar = kOffV + kVStages * kV;
-    static constexpr int kBars = 4 + 2 + 2 * kKStages + 2 * kVStages + 4 + 4 + 2;
+    static constexpr int kOffV = kOffK + kKStages * kStage;
+    // FP8: one fp16 key tile and two value tiles, and the scales
+    static constexpr int kOffK16 = kOffV + kVStages * kStage;
+    static constexpr int kOffV16 = kOffK16 + (FP8 ? kK : 0);
+    static constexpr int kOffScale = kOffV16 + (FP8 ? 2 * kV : 0);  // [ring][k, v][128]
+    static constexpr int kOffBar = kOffScale + (FP8 ? kScaleRing * 2 * kStepKeys * 4 : 0);
+    static constexpr int kBars = 4 + 2 + 2 * kKStages + 2 * kVStages + 8 + 1 + 3;
     static constexpr int kOffPiece = kOffBar + kBars * 8;
     static constexpr int kOffFlags = kOffPiece + 2 * static_cast<int>(sizeof(Piece));
     static constexpr int kOffValid = kOffFlags + 3 * kFlagWords * 4;  // (see the softmax)
-    static constexpr int kOffMisc = kOffValid + kValidRing * 4;
-    static constexpr int kOffScan = kOffMisc + 16;  // the prologue's words
-    static constexpr int kBytes = kOffScan + (kTileThreads / 32 + 4) * 8;
+    static constexpr int kOffTop = kOffValid + kValidRing * 4;  // [ring][4] largest value scale
+    static constexpr int kOffMisc = kOffTop + kScaleRing * kConvertWarps * 4;
+    static constexpr int kOffScan = (kOffMisc + 4 + 7) / 8 * 8;  // the prologue's words
+    static constexpr int kBytes = kOffScan + (kThreads / 32 + 4) * 8;
 };
 
-int tile_smem_bytes(int D) {
-    return dec::kTileAlign + (D == 128 ? Geo<128>::kBytes : Geo<64>::kBytes);
-}
-
 // mbarrier addresses (shared space) by role
+template <int KS, int VS>
 struct Bars {
     uint32_t b;
     __device__ uint32_t piece_full(int s) const { return b + 8 * s; }
@@ -246,26 +183,70 @@ struct Bars {
     __device__ uint32_t q_full() const { return b + 8 * 4; }
     __device__ uint32_t q_empty() const { return b + 8 * 5; }
     __device__ uint32_t k_full(int s) const { return b + 8 * (6 + s); }
-    __device__ uint32_t k_empty(int s) const { return b + 8 * (6 + kKStages + s); }
-    static constexpr int kV0 = 6 + 2 * kKStages;
+    __device__ uint32_t k_empty(int s) const { return b + 8 * (6 + KS + s); }
+    static constexpr int kV0 = 6 + 2 * KS;
     __device__ uint32_t v_full(int s) const { return b + 8 * (kV0 + s); }
-    __device__ uint32_t v_empty(int s) const { return b + 8 * (kV0 + kVStages + s); }
-    static constexpr int kS0 = kV0 + 2 * kVStages;
+    __device__ uint32_t v_empty(int s) const { return b + 8 * (kV0 + VS + s); }
+    static constexpr int kS0 = kV0 + 2 * VS;
     __device__ uint32_t s_full(int s) const { return b + 8 * (kS0 + s); }
     __device__ uint32_t s_free(int s) const { return b + 8 * (kS0 + 2 + s); }
     __device__ uint32_t p_full(int s) const { return b + 8 * (kS0 + 4 + s); }
     __device__ uint32_t pv_done(int s) const { return b + 8 * (kS0 + 6 + s); }
     __device__ uint32_t o_free() const { return b + 8 * (kS0 + 8); }
-    __device__ uint32_t scanned() const { return b + 8 * (kS0 + 9); }
+    __device__ uint32_t k16_full() const { return b + 8 * (kS0 + 9); }
+    __device__ uint32_t v16_full(int s) const { return b + 8 * (kS0 + 10 + s); }
 };
 
-// arrivals that free a piece record: the value producer, the two MMA warps and
-// every softmax warp
-constexpr int kPieceReaders = 3 + kSoftmaxWarps;
+// Wait for phase `parity` of an mbarrier, giving up after about two seconds:
+// one small loop (the timer is read every 64th time round).
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .u32 n, k;\n\t.reg .u64 t, t0;\n\t"
+        "mov.u32 %0, 1;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\t"
+        "mov.u64 t0, %%globaltimer;\n\t"
+        "mov.u32 n, 0;\n\t"
+        "AGAIN:\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\t"
+        "add.u32 n, n, 1;\n\t"
+        "and.b32 k, n, 63;\n\t"
+        "setp.ne.u32 p, k, 0;\n\t"
+        "@p bra AGAIN;\n\t"
+        "mov.u64 t, %%globaltimer;\n\t"
+        "sub.u64 t, t, t0;\n\t"
+        "setp.lt.u64 p, t, 2000000000;\n\t"
+        "@p bra AGAIN;\n\t"
+        "mov.u32 %0, 0;\n\t"
+        "DONE:\n\t}"
+        : "=&r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 
-// Every lane waits (bounded); false if any lane gave up.
+// Every lane waits; false if any lane gave up.
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+    return __all_sync(0xffffffffu, wait_bounded(bar, parity));
+}
+
+__device__ __forceinline__ void tensor_g2s_2d(uint32_t dst, const void *tmap, int c0, int c1,
+                                              uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(tmap), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tensor_g2s_4d(uint32_t dst, const void *tmap, int c0, int c1,
+                                              int c2, int c3, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -274,8 +255,8 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Packed fp32 pairs (one instruction for two lanes' worth of fma or add) and
-// the three-input maximum.
+// Packed fp32 pairs (one instruction for two lanes' worth of fma, mul or add)
+// and the three-input maximum.
 __device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
@@ -291,6 +272,11 @@ __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -301,16 +287,18 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
+__device__ __forceinline__ uint32_t pack_scaled(uint32_t a, uint32_t b, float f) {
+    return pack_half2(__uint_as_float(a) * f, __uint_as_float(b) * f);
+}
 
-// Transposes N x N 16-byte elements held by groups of N lanes (N = 4 or 8):
-// afterwards element c of lane t of a group is element t of the group's lane c.
-template <int N>
-__device__ __forceinline__ void lane_transpose(uint4 (&x)[N], int lane) {
+// Transposes 4 x 4 16-byte elements held by groups of four lanes: afterwards
+// element c of lane t of a group is element t of the group's lane c.
+__device__ __forceinline__ void lane_transpose4(uint4 (&x)[4], int lane) {
 #pragma unroll
-    for (int m = 1; m < N; m <<= 1) {
+    for (int m = 1; m < 4; m <<= 1) {
         const bool up = lane & m;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < 4; ++i) {
             if (i & m) continue;
             uint4 &lo = x[i], &hi = x[i | m];
             uint4 s = up ? lo : hi;
@@ -327,9 +315,6 @@ __device__ __forceinline__ void lane_transpose(uint4 (&x)[N], int lane) {
 __device__ __forceinline__ void prefetch_l1(const void *p) {
     asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
 }
-
-// Units of an item: its steps and kItemUnits for its start-up.
-constexpr int kItemUnits = 1;
 
 // The step a place `x` units into an item falls on.
 __device__ __forceinline__ int step_at(int64_t x, int steps) {
@@ -373,9 +358,9 @@ __device__ __forceinline__ int64_t seq_units(const SeqGeo &sg, int Hk) {
 
 // Sum over the CTA of v, and the exclusive prefix of this thread's (every
 // thread calls; `sh` holds one word per warp).
+template <int kWarps>
 __device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t *sh, int64_t &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    constexpr int kWarps = kTileThreads / 32;
     int64_t x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -386,7 +371,7 @@ __device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t *sh, int64_t &tot
     __syncthreads();
     int64_t before = 0;
     total = 0;
-#pragma unroll
+#pragma unroll 1
     for (int w = 0; w < kWarps; ++w) {
         const int64_t y = sh[w];
         if (w < warp) before += y;
@@ -417,60 +402,6 @@ __device__ __forceinline__ uint64_t visible(const uint64_t *mask, int words, int
     return n >= 64 ? m : n <= 0 ? 0ull : m & ((1ull << n) - 1);
 }
 
-// Byte offset of 16-byte unit i (row-major) of a staged value tile.
-template <int CH>
-__device__ __forceinline__ int v_unit(int i) {
-    const int t = i / (8 * CH), u = i % (8 * CH);
-    return (t >> 4) * (CH * kBS * 128) + (u >> 3) * (kBS * 128) + (t & 15) * 128 + (u & 7) * 16;
-}
-
-// The fp16 pair w with infinities and NaN zeroed.
-__device__ __forceinline__ uint32_t finite_halves(uint32_t w) {
-    if ((w & 0x7C00u) == 0x7C00u) w &= 0xFFFF0000u;
-    if ((w & 0x7C000000u) == 0x7C000000u) w &= 0x0000FFFFu;
-    return w;
-}
-
-// The value tile `vb` of a step that reaches past the context: rows at and past
-// the sequence's end hold anything and are zeroed; of the drafted rows (key ctx
-// on) the non-finite elements are zeroed and the row flagged.  `keys` of the
-// step's keys, the first of them key0, are staged; thread i of kScanners.  A
-// unit is 16 bytes, kScan of them in flight per thread.
-constexpr int kScanners = kSoftmaxWarps * 32;
-template <int CH>
-__device__ __forceinline__ void clean_values(uint8_t *vb, int key0, int keys, int ctx, int L,
-                                             uint32_t *flags, int thread) {
-    constexpr int kUnits = 8 * CH;  // units of a row
-    constexpr int kScan = 4;
-    const int end = keys * kUnits;
-    for (int i0 = max(ctx - key0, 0) * kUnits + thread; i0 < end; i0 += kScanners * kScan) {
-        uint4 x[kScan];
-#pragma unroll
-        for (int k = 0; k < kScan; ++k)
-            x[k] = *reinterpret_cast<const uint4 *>(vb + v_unit<CH>(min(i0 + kScanners * k, end - 1)));
-#pragma unroll
-        for (int k = 0; k < kScan; ++k) {
-            const int i = i0 + kScanners * k;
-            const int key = key0 + i / kUnits;
-            // all ones in an exponent carry into its sign's place
-            const uint32_t bad = (((x[k].x & 0x7C007C00u) + 0x04000400u) |
-                                  ((x[k].y & 0x7C007C00u) + 0x04000400u) |
-                                  ((x[k].z & 0x7C007C00u) + 0x04000400u) |
-                                  ((x[k].w & 0x7C007C00u) + 0x04000400u)) & 0x80008000u;
-            if (i >= end || (bad == 0 && key < L)) continue;
-            uint4 *at = reinterpret_cast<uint4 *>(vb + v_unit<CH>(i));
-            if (key >= L) {
-                *at = make_uint4(0u, 0u, 0u, 0u);
-            } else {
-                *at = make_uint4(finite_halves(x[k].x), finite_halves(x[k].y),
-                                 finite_halves(x[k].z), finite_halves(x[k].w));
-                atomicOr(&flags[(key - ctx) >> 5], 1u << ((key - ctx) & 31));
-            }
-        }
-    }
-    fence_proxy_async_smem();
-}
-
 // Block id of entry b of a sequence, or -1 when out of range (recorded when
 // `report`).
 __device__ __forceinline__ int block_id(const TreeParams &p, int seq, int b, bool report) {
@@ -481,54 +412,249 @@ __device__ __forceinline__ int block_id(const TreeParams &p, int seq, int b, boo
     return -1;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kTileThreads, 1)
-    tree_tile_kernel(const __grid_constant__ TileParams tp) {
-    using Gm = Geo<D>;
+// Walks a CTA's stretch.
+struct Walk {
+    int64_t u, u1;  // the next unit, the stretch's end
+    SeqGeo sg;
+    int seq, n, item, x;  // the item (of n units) that u falls into, and u's place in it
+};
+
+// The next piece of the stretch (done: none is left), and lane l's id of its
+// block l.  Out of line: called at two places, once per piece.
+__device__ __noinline__ PieceHead next_piece(const TreeParams &p, Walk &w, int cta, int &id) {
+    const int lane = threadIdx.x & 31;
+    const int Hk = p.num_kv_heads, G = p.num_heads / Hk;
+    PieceHead pc;
+    pc.done = 1;
+    id = -1;
+    while (w.u < w.u1) {
+        if (w.x == w.n) {  // the next item
+            w.x = 0;
+            if (++w.item == Hk * w.sg.tiles) {  // of the next sequence with rows
+                w.item = 0;
+                do ++w.seq;
+                while (w.seq < p.num_seqs && !seq_geo(p, w.seq, G, false, w.sg));
+                if (w.seq >= p.num_seqs) return pc;  // (not reached: u1 is inside the list)
+                w.n = w.sg.steps + kItemUnits;
+            }
+        }
+        const int take = static_cast<int>(min(w.u1 - w.u, static_cast<int64_t>(w.n - w.x)));
+        const int s0 = step_at(w.x, w.sg.steps), s1 = step_at(w.x + take, w.sg.steps);
+        w.u += take;
+        w.x += take;
+        if (s1 == s0) continue;
+        pc.seq = w.seq;
+        pc.kvh = w.item / w.sg.tiles;
+        pc.tile = w.item - pc.kvh * w.sg.tiles;
+        pc.step0 = s0;
+        pc.nsteps = s1 - s0;
+        pc.nblk = min((w.sg.L + kBS - 1) / kBS - s0 * kStepBlocks, pc.nsteps * kStepBlocks);
+        pc.L = w.sg.L;
+        pc.Q = w.sg.Q;
+        pc.q0 = w.sg.q0;
+        pc.slot = s0 == 0 && s1 == w.sg.steps ? -1 : 2 * cta + (s0 == 0);
+        pc.done = 0;
+        if (lane < pc.nblk) id = block_id(p, w.seq, s0 * kStepBlocks + lane, true);
+        break;
+    }
+    return pc;
+}
+
+// The fp16 pair w with infinities and NaN zeroed.
+__device__ __forceinline__ uint32_t finite_halves(uint32_t w) {
+    if ((w & 0x7C00u) == 0x7C00u) w &= 0xFFFF0000u;
+    if ((w & 0x7C000000u) == 0x7C000000u) w &= 0x0000FFFFu;
+    return w;
+}
+// Non-zero if one of eight fp16 is infinite or NaN: all ones in an exponent
+// carry into its sign's place.
+__device__ __forceinline__ uint32_t any_non_finite(const uint4 &x) {
+    return (((x.x & 0x7C007C00u) + 0x04000400u) | ((x.y & 0x7C007C00u) + 0x04000400u) |
+            ((x.z & 0x7C007C00u) + 0x04000400u) | ((x.w & 0x7C007C00u) + 0x04000400u)) &
+           0x80008000u;
+}
+// A staged unit of eight values of row `key`: zero at and past the sequence's
+// end; of a drafted row its finite elements, and the row flagged.
+__device__ __forceinline__ uint4 clean_unit(uint4 x, int key, int ctx, int L, uint32_t *flags) {
+    if (key >= L) return make_uint4(0u, 0u, 0u, 0u);
+    if (key >= ctx && any_non_finite(x) != 0) {
+        x = make_uint4(finite_halves(x.x), finite_halves(x.y), finite_halves(x.z),
+                       finite_halves(x.w));
+        atomicOr(&flags[(key - ctx) >> 5], 1u << ((key - ctx) & 31));
+    }
+    return x;
+}
+
+// Byte offset of 16-byte unit i (row-major) of a staged fp16 value tile whose
+// order inside a row does not matter (the swizzle only permutes it).
+template <int CH>
+__device__ __forceinline__ int v_unit(int i) {
+    const int t = i / (8 * CH), u = i % (8 * CH);
+    return (t >> 4) * (CH * kBS * 128) + (u >> 3) * (kBS * 128) + (t & 15) * 128 + (u & 7) * 16;
+}
+
+// Cleans the value tile `vb` of a step that reaches past the context: its
+// first `keys` keys, the first of them key0.  The softmax threads share it,
+// kScan units in flight each.
+template <int CH>
+__device__ __noinline__ void clean_values(uint8_t *vb, int key0, int keys, int ctx, int L,
+                                          uint32_t *flags) {
+    constexpr int kUnits = 8 * CH;  // units of a row
+    constexpr int kThreads = kSoftmaxWarps * 32;
+    constexpr int kScan = 4;
+    const int end = keys * kUnits;
+    const int thread = threadIdx.x - kSoftmaxWarp * 32;
+#pragma unroll 1
+    for (int i0 = max(ctx - key0, 0) * kUnits + thread; i0 < end; i0 += kThreads * kScan) {
+        uint4 x[kScan];
+#pragma unroll
+        for (int k = 0; k < kScan; ++k)
+            x[k] = *reinterpret_cast<const uint4 *>(vb + v_unit<CH>(min(i0 + kThreads * k, end - 1)));
+#pragma unroll
+        for (int k = 0; k < kScan; ++k) {
+            const int i = i0 + kThreads * k;
+            const int key = key0 + i / kUnits;
+            if (i < end && (key >= L || any_non_finite(x[k]) != 0))
+                *reinterpret_cast<uint4 *>(vb + v_unit<CH>(i)) =
+                    clean_unit(x[k], key, ctx, L, flags);
+        }
+    }
+    fence_proxy_async_smem();
+}
+
+// The elements that were left out of a row's O (fp32 bits of dims d0 .. d0 +
+// 31), where the row sees them: a weight times an infinity or a NaN is that,
+// whatever the (positive) weight.
+template <int D, bool FP8>
+__device__ __forceinline__ void add_non_finite(const TreeParams &p, const PieceHead &pc,
+                                               const uint32_t *flags, const uint64_t *mask, int d0,
+                                               uint32_t (&o)[32]) {
+#pragma unroll 1
+    for (int node = 0; node < pc.Q; ++node) {
+        if (!((flags[node >> 5] >> (node & 31)) & 1u) ||
+            !((__ldg(mask + (node >> 6)) >> (node & 63)) & 1))
+            continue;
+        const int key = pc.L - pc.Q + node;
+        const int id = block_id(p, pc.seq, key / kBS, false);
+        if (id < 0) continue;
+        const int64_t at =
+            ((static_cast<int64_t>(id) * kBS + key % kBS) * p.num_kv_heads + pc.kvh) * D + d0;
+#pragma unroll
+        for (int d = 0; d < 32; ++d) {
+            float x;
+            if constexpr (FP8) {
+                const uint8_t c = static_cast<const uint8_t *>(p.v_cache)[at + d];
+                x = (c & 0x7Fu) == 0x7Fu ? NAN : 0.f;
+            } else {
+                x = __half2float(static_cast<const __half *>(p.v_cache)[at + d]);
+            }
+            if (!isfinite(x)) o[d] = __float_as_uint(__uint_as_float(o[d]) + x);
+        }
+    }
+}
+
+// Sixteen E4M3 codes as fp16 (exact; the NaN code becomes a NaN).
+__device__ __forceinline__ void codes_to_half(const uint4 &c, uint4 &lo, uint4 &hi) {
+    const uint32_t in[4] = {c.x, c.y, c.z, c.w};
+    uint32_t out[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+            : "=r"(out[2 * i]), "=r"(out[2 * i + 1])
+            : "r"(in[i]));
+    }
+    lo = make_uint4(out[0], out[1], out[2], out[3]);
+    hi = make_uint4(out[4], out[5], out[6], out[7]);
+}
+
+// A step's codes (staged [block][token][D bytes], swizzled as D asks) as the
+// fp16 key (V = false) or value tile, by the 128 converter threads.  Eight
+// lanes take half a row each of two neighbouring rows, opposite halves, so
+// that their reads and their writes fall on eight different 16-byte columns.
+template <int D, bool V>
+__device__ __forceinline__ void convert_tile(const uint8_t *codes, uint8_t *tile, int blocks,
+                                             int key0, int ctx, int L, uint32_t *flags) {
+    constexpr int CH = D / 64;
+    constexpr int kGroups = kConvertWarps * 4;  // groups of eight lanes
+    const int tid = threadIdx.x - kConvertWarp * 32;
+    const int p = tid & 7;
+    const bool tail = V && key0 + kStepKeys > ctx;
+#pragma unroll 4
+    for (int g = tid >> 3; g < blocks * (kBS / 2) * CH; g += kGroups) {
+        const int rp = g / CH, sel = g % CH;
+        const int t = 2 * rp + (p >> 2);
+        const int u = CH == 2 ? (p & 3) | (((p >> 2) ^ sel) << 2) : p & 3;
+        const int su = D == 128 ? u ^ (t & 7) : u ^ ((t >> 1) & 3);
+        uint4 lo, hi;
+        codes_to_half(*reinterpret_cast<const uint4 *>(codes + t * D + su * 16), lo, hi);
+        if (tail) {
+            lo = clean_unit(lo, key0 + t, ctx, L, flags);
+            hi = clean_unit(hi, key0 + t, ctx, L, flags);
+        }
+        const int c = u >> 2, x = 2 * (u & 3);
+        uint8_t *row = tile + (V ? (t >> 4) * (CH * kBS * 128) + c * (kBS * 128) + (t & 15) * 128
+                                 : (t >> 3) * (CH * 1024) + c * 1024 + (t & 7) * 128);
+        *reinterpret_cast<uint4 *>(row + ((x ^ (t & 7)) * 16)) = lo;
+        *reinterpret_cast<uint4 *>(row + (((x + 1) ^ (t & 7)) * 16)) = hi;
+    }
+    fence_proxy_async_smem();
+}
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
+    tree_tile_kernel(const __grid_constant__ TreeParams p) {
+    using Gm = Geo<D, FP8>;
     constexpr int CH = Gm::kChunks;
+    constexpr int KS = Gm::kKStages, VS = Gm::kVStages;
     constexpr int DH = D / 2;  // the head dimensions (of O) each softmax thread owns
-    const TreeParams &p = tp.t;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((dec::kTileAlign - (smem_u32(smem_raw) & (dec::kTileAlign - 1))) &
                                 (dec::kTileAlign - 1));
     const uint32_t sb = smem_u32(smem);
-    const Bars br{sb + Gm::kOffBar};
+    const Bars<KS, VS> br{sb + Gm::kOffBar};
     Piece *pieces = reinterpret_cast<Piece *>(smem + Gm::kOffPiece);
     uint32_t *flags = reinterpret_cast<uint32_t *>(smem + Gm::kOffFlags);
     volatile uint32_t *valid = reinterpret_cast<volatile uint32_t *>(smem + Gm::kOffValid);
     volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(smem + Gm::kOffMisc);
     int64_t *scan = reinterpret_cast<int64_t *>(smem + Gm::kOffScan);
-    volatile int64_t *start = scan + kTileThreads / 32;  // sequence, its first unit, L | Q, q0
+    volatile int64_t *start = scan + Gm::kThreads / 32;  // sequence, its first unit, L | Q, q0
+    volatile float *scales = reinterpret_cast<volatile float *>(smem + Gm::kOffScale);
+    volatile float *tops = reinterpret_cast<volatile float *>(smem + Gm::kOffTop);
 
     const int Hk = p.num_kv_heads, H = p.num_heads;
     const int G = H / Hk, logG = __ffs(G) - 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cta = blockIdx.x, ctas = gridDim.x;
     if (threadIdx.x == 0) {
+        // readers of a piece record: the value producer, the two MMA warps,
+        // every softmax warp and every converter
+        constexpr int kPieceReaders = 3 + kSoftmaxWarps + (FP8 ? kConvertWarps : 0);
         for (int s = 0; s < 2; ++s) {
             mbar_init(br.piece_full(s), 1);
             mbar_init(br.piece_empty(s), kPieceReaders);
             mbar_init(br.s_full(s), 2);
             mbar_init(br.s_free(s), kSoftmaxWarps);
             mbar_init(br.p_full(s), kSoftmaxWarps);
-            mbar_init(br.pv_done(s), 1);
+            mbar_init(br.pv_done(s), 2);
+            mbar_init(br.v16_full(s), kConvertWarps);
         }
         mbar_init(br.q_full(), 1);
         mbar_init(br.q_empty(), 1);
-        for (int s = 0; s < kKStages; ++s) {
+        for (int s = 0; s < KS; ++s) {
             mbar_init(br.k_full(s), 1);
-            mbar_init(br.k_empty(s), 1);
+            mbar_init(br.k_empty(s), FP8 ? kConvertWarps : 1);
         }
-        for (int s = 0; s < kVStages; ++s) {
+        for (int s = 0; s < VS; ++s) {
             mbar_init(br.v_full(s), 1);
-            mbar_init(br.v_empty(s), 1);
+            mbar_init(br.v_empty(s), FP8 ? kConvertWarps : 1);
         }
         mbar_init(br.o_free(), kSoftmaxWarps);
-        mbar_init(br.scanned(), kSoftmaxWarps);
+        mbar_init(br.k16_full(), kConvertWarps);
         fence_mbarrier_init();
-        prefetch_tensormap(&tp.tm_k);
-        prefetch_tensormap(&tp.tm_v);
-        prefetch_tensormap(&tp.tm_q);
+        prefetch_tensormap(&p.tm_k);
+        prefetch_tensormap(&p.tm_v);
+        prefetch_tensormap(&p.tm_q);
     }
     if (threadIdx.x < 3 * kFlagWords) flags[threadIdx.x] = 0;
     if (warp == 2) {
@@ -539,287 +665,317 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     grid_launch_dependents();  // the merge: it waits for this grid
 
     // ---- the list's length, and where this CTA's stretch starts: the thread
-    // that holds the sequence its first unit falls into says so (with more
-    // sequences than threads, in a second pass)
+    // that holds the sequence its first unit falls into says so.  (With more
+    // sequences than threads the list is gone through twice.)
     int64_t units = 0;
-    const bool one_pass = p.num_seqs <= kTileThreads;
-    for (int s0 = 0; s0 < p.num_seqs; s0 += kTileThreads) {
-        const int s = s0 + threadIdx.x;
-        SeqGeo sg;
-        const bool has = s < p.num_seqs && seq_geo(p, s, G, cta == 0, sg);
-        int64_t total;
-        const int64_t w = has ? seq_units(sg, Hk) : 0;
-        const int64_t before = cta_scan(w, scan, total);
-        units += total;
-        if (one_pass && total > 0) {
-            const int64_t u0 = stretch(total, cta, static_cast<int>(min(static_cast<int64_t>(ctas), total)));
-            if (w > 0 && before <= u0 && u0 < before + w) {
-                start[0] = s;
-                start[1] = before;
-                start[2] = static_cast<int64_t>(sg.L) << 32 | static_cast<unsigned>(sg.Q);
-                start[3] = sg.q0;
-            }
-        }
-    }
-    const int busy = static_cast<int>(min(static_cast<int64_t>(ctas), units));  // CTAs with a stretch
-    const int64_t u0 = busy ? stretch(units, cta, busy) : 0;
-    const int64_t u1 = busy ? stretch(units, cta + 1, busy) : 0;
-    if (!one_pass && cta < busy) {
+    int busy = 0;  // CTAs with a stretch
+    int64_t u0 = 0, u1 = 0;
+#pragma unroll 1
+    for (int pass = p.num_seqs <= Gm::kThreads ? 1 : 0; pass < 2; ++pass) {
         int64_t run = 0;
-        for (int s0 = 0; s0 < p.num_seqs; s0 += kTileThreads) {
+#pragma unroll 1
+        for (int s0 = 0; s0 < p.num_seqs; s0 += Gm::kThreads) {
             const int s = s0 + threadIdx.x;
             SeqGeo sg;
-            const bool has = s < p.num_seqs && seq_geo(p, s, G, false, sg);
+            const bool has =
+                s < p.num_seqs && seq_geo(p, s, G, cta == 0 && run == 0 && units == 0, sg);
             int64_t total;
             const int64_t w = has ? seq_units(sg, Hk) : 0;
-            const int64_t before = run + cta_scan(w, scan, total);
-            if (w > 0 && before <= u0 && u0 < before + w) {
-                start[0] = s;
-                start[1] = before;
-                start[2] = static_cast<int64_t>(sg.L) << 32 | static_cast<unsigned>(sg.Q);
-                start[3] = sg.q0;
-            }
+            const int64_t before = run + cta_scan<Gm::kThreads / 32>(w, scan, total);
             run += total;
+            if (pass == 1) {
+                if (p.num_seqs <= Gm::kThreads) units = total;
+                busy = static_cast<int>(min(static_cast<int64_t>(ctas), units));
+                if (busy != 0) {
+                    u0 = stretch(units, cta, busy);
+                    u1 = stretch(units, cta + 1, busy);
+                }
+                if (cta < busy && w > 0 && before <= u0 && u0 < before + w) {
+                    start[0] = s;
+                    start[1] = before;
+                    start[2] = static_cast<int64_t>(sg.L) << 32 | static_cast<unsigned>(sg.Q);
+                    start[3] = sg.q0;
+                }
+            }
         }
+        if (pass == 0) units = run;
     }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = misc[0];
-    if (cta >= busy) {
-        if (threadIdx.x == 0) tp.borders[cta].pieces = 0;
-    } else if (warp == 0) {
-        // ===================== pieces, query tiles and keys =====================
-        int seq = static_cast<int>(start[0]);
-        int64_t first = start[1];  // the sequence's first unit
-        int64_t u = u0;
-        SeqGeo sg = make_geo(static_cast<int>(start[2] >> 32), static_cast<int>(start[2]),
-                             static_cast<int>(start[3]), G);
-        // the place of the stretch's start in its item, kept from piece to piece
-        int n = sg.steps + kItemUnits;
-        int item = static_cast<int>((u - first) / n);
-        int x = static_cast<int>(u - first - static_cast<int64_t>(item) * n);
-        // the border at u0, for the merge (every CTA writes one, whether or not
-        // its stretch holds a step)
-        if (lane == 0) {
-            Border border;
-            const int64_t a = u0 - x;
-            const int tile = item % sg.tiles;
-            const bool cuts = cta > 0 && step_at(x, sg.steps) > 0 &&
-                              step_at(stretch(units, cta - 1, busy) - a, sg.steps) == 0;
-            // pieces: the CTA before this one, and those up to the item's last unit
-            border.pieces =
-                cuts ? static_cast<int>(((a + n) * busy - 1) / units) - (cta - 1) + 1 : 0;
-            border.rows = min(kRows, sg.Q * G - tile * kRows);
-            border.q0 = sg.q0 + tile * (kRows >> logG);
-            border.kvh = item / sg.tiles;
-            tp.borders[cta] = border;
-        }
-        __syncwarp();
-        // The next piece of the stretch, and the ids of its first blocks.
-        auto next_piece = [&](PieceHead &pc, int &ids) {
-            pc.done = 1;
-            ids = -1;
-            while (u < u1) {
-                if (x == n) {  // the next item
-                    x = 0;
-                    if (++item == Hk * sg.tiles) {  // of the next sequence with rows
-                        item = 0;
-                        do ++seq;
-                        while (seq < p.num_seqs && !seq_geo(p, seq, G, false, sg));
-                        if (seq >= p.num_seqs) return;  // (not reached: u1 is inside the list)
-                        n = sg.steps + kItemUnits;
+    const bool busy_cta = cta < busy;
+    if (!busy_cta && threadIdx.x == 0) p.borders[cta].pieces = 0;
+
+    if (warp < kSoftmaxWarp) {
+        if (!busy_cta) {
+        } else if (warp == 0) {
+            // ========================= pieces and keys =========================
+            Walk w;
+            w.seq = static_cast<int>(start[0]);
+            const int64_t first = start[1];  // the sequence's first unit
+            w.u = u0;
+            w.u1 = u1;
+            w.sg = make_geo(static_cast<int>(start[2] >> 32), static_cast<int>(start[2]),
+                            static_cast<int>(start[3]), G);
+            w.n = w.sg.steps + kItemUnits;
+            w.item = static_cast<int>((u0 - first) / w.n);
+            w.x = static_cast<int>(u0 - first - static_cast<int64_t>(w.item) * w.n);
+            // the border at u0, for the merge (every CTA writes one, whether or
+            // not its stretch holds a step)
+            if (lane == 0) {
+                Border border;
+                const int64_t a = u0 - w.x;  // the item's first unit
+                const int tile = w.item % w.sg.tiles;
+                const bool cuts = cta > 0 && step_at(w.x, w.sg.steps) > 0 &&
+                                  step_at(stretch(units, cta - 1, busy) - a, w.sg.steps) == 0;
+                // pieces: the CTA before this one, and those up to the item's last unit
+                border.pieces =
+                    cuts ? static_cast<int>(((a + w.n) * busy - 1) / units) - (cta - 1) + 1 : 0;
+                border.rows = min(kRows, w.sg.Q * G - tile * kRows);
+                border.q0 = w.sg.q0 + tile * (kRows >> logG);
+                border.kvh = w.item / w.sg.tiles;
+                p.borders[cta] = border;
+            }
+            __syncwarp();
+            int cur_ids;
+            PieceHead cur = next_piece(p, w, cta, cur_ids);
+            int gs = 0;  // steps staged
+            bool ok = true;
+#pragma unroll 1
+            for (int it = 0; ok; ++it) {
+                const int rec = it & 1;
+                if (it >= 2 && !wait_all(br.piece_empty(rec), ((it >> 1) - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                pieces[rec].ids[lane] = cur_ids;
+                if (lane == 0) static_cast<PieceHead &>(pieces[rec]) = cur;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(br.piece_full(rec));
+                if (cur.done) break;
+                // the ids of 32 blocks at a time, one per lane, the next ones --
+                // of this piece or the next -- looked up a window ahead
+                const int b0 = cur.step0 * kStepBlocks;
+                PieceHead nxt;
+                int nxt_ids = -1, ids = cur_ids, ahead = -1;
+#pragma unroll 1
+                for (int n = 0; n < cur.nsteps; ++n, ++gs) {
+                    const int ks = gs % KS;
+                    const int at = n * kStepBlocks;
+                    if ((at & 31) == 0) {
+                        if (at != 0) ids = ahead;
+                        const int b = at + 32 + lane;
+                        ahead = b < cur.nblk ? block_id(p, cur.seq, b0 + b, true) : -1;
+                    }
+                    if (gs >= KS && !wait_all(br.k_empty(ks), ((gs / KS) - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const int nb = min(kStepBlocks, cur.nblk - at);
+                    // lane l: block l of the step (a bad block reads rows before
+                    // the cache: zeros)
+                    const int id = __shfl_sync(0xffffffffu, ids, (at & 31) + (lane & 7));
+                    const uint32_t good = __ballot_sync(0xffffffffu, id >= 0 || lane >= nb);
+                    if (lane == 0) {
+                        valid[gs % kValidRing] = good;
+                        mbar_arrive_expect_tx(br.k_full(ks), nb * Gm::kBlockBytes);
+                    }
+                    __syncwarp();
+                    if (lane < nb) {
+                        const uint32_t dst =
+                            sb + Gm::kOffK + ks * Gm::kStage + lane * Gm::kBlockBytes;
+                        if constexpr (FP8)
+                            tensor_g2s_2d(dst, &p.tm_k, cur.kvh * D, id >= 0 ? id * kBS : -kBS,
+                                          br.k_full(ks));
+                        else
+                            tensor_g2s_4d(dst, &p.tm_k, 0, 0, cur.kvh * CH, id >= 0 ? 2 * id : -2,
+                                          br.k_full(ks));
+                    }
+                    // (when the ring is full: the look-ups wait for memory)
+                    if (n == min(KS, cur.nsteps) - 1) nxt = next_piece(p, w, cta, nxt_ids);
+                }
+                cur = nxt;
+                cur_ids = nxt_ids;
+            }
+            if (!ok) {
+                if (lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT, cta);
+                // let the last copies land before the CTA can exit
+#pragma unroll 1
+                for (int s = 0; s < KS && s < gs; ++s) {
+                    const int last = gs - 1 - ((gs - 1 - s) % KS);
+                    wait_bounded(br.k_full(s), (last / KS) & 1);
+                }
+            }
+        } else if (warp == 1) {
+            // ============================== values ==============================
+            int gs = 0;
+            bool ok = true;
+#pragma unroll 1
+            for (int it = 0; ok; ++it) {
+                const int rec = it & 1;
+                if (!wait_all(br.piece_full(rec), (it >> 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                const PieceHead pc = pieces[rec];
+                int ids = pieces[rec].ids[lane], ahead = -1;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(br.piece_empty(rec));
+                if (pc.done) break;
+                const int b0 = pc.step0 * kStepBlocks;
+#pragma unroll 1
+                for (int n = 0; n < pc.nsteps; ++n, ++gs) {
+                    const int vs = gs % VS;
+                    const int at = n * kStepBlocks;
+                    if ((at & 31) == 0) {
+                        if (at != 0) ids = ahead;
+                        const int b = at + 32 + lane;
+                        ahead = b < pc.nblk ? block_id(p, pc.seq, b0 + b, false) : -1;
+                    }
+                    if (gs >= VS && !wait_all(br.v_empty(vs), ((gs / VS) - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const int nb = min(kStepBlocks, pc.nblk - at);
+                    if (lane == 0) mbar_arrive_expect_tx(br.v_full(vs), nb * Gm::kBlockBytes);
+                    __syncwarp();
+                    const int id = __shfl_sync(0xffffffffu, ids, (at & 31) + (lane & 7));
+                    if (lane < nb) {
+                        const uint32_t dst =
+                            sb + Gm::kOffV + vs * Gm::kStage + lane * Gm::kBlockBytes;
+                        if constexpr (FP8)
+                            tensor_g2s_2d(dst, &p.tm_v, pc.kvh * D, id >= 0 ? id * kBS : -kBS,
+                                          br.v_full(vs));
+                        else
+                            tensor_g2s_3d(dst, &p.tm_v, 0, id >= 0 ? id * kBS : -kBS, pc.kvh * CH,
+                                          br.v_full(vs));
                     }
                 }
-                const int take = static_cast<int>(min(u1 - u, static_cast<int64_t>(n - x)));
-                const int s0 = step_at(x, sg.steps), s1 = step_at(x + take, sg.steps);
-                u += take;
-                x += take;
-                if (s1 == s0) continue;
-                pc.seq = seq;
-                pc.kvh = item / sg.tiles;
-                pc.tile = item - pc.kvh * sg.tiles;
-                pc.step0 = s0;
-                pc.nsteps = s1 - s0;
-                pc.nblk = min((sg.L + kBS - 1) / kBS - s0 * kStepBlocks, pc.nsteps * kStepBlocks);
-                pc.L = sg.L;
-                pc.Q = sg.Q;
-                pc.q0 = sg.q0;
-                pc.slot = s0 == 0 && s1 == sg.steps ? -1 : 2 * cta + (s0 == 0);
-                pc.done = 0;
-                if (lane < pc.nblk) ids = block_id(p, seq, s0 * kStepBlocks + lane, true);
-                return;
             }
-        };
-        PieceHead cur;
-        int cur_ids;
-        next_piece(cur, cur_ids);
-        int gs = 0;  // steps staged
-        bool ok = true;
-        for (int it = 0; ok; ++it) {
-            const int rec = it & 1;
-            if (it >= 2 && !wait_all(br.piece_empty(rec), ((it >> 1) - 1) & 1)) {
-                ok = false;
-                break;
-            }
-            pieces[rec].ids[lane] = cur_ids;
-            if (lane == 0) static_cast<PieceHead &>(pieces[rec]) = cur;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(br.piece_full(rec));
-            if (cur.done) break;
-            // its keys: the ids of 32 blocks at a time, one per lane, the next
-            // ones -- of this piece or the next -- looked up a window ahead
-            const int b0 = cur.step0 * kStepBlocks;
-            PieceHead nxt;
-            int nxt_ids = -1, ids = cur_ids, ahead = -1;
-            for (int n = 0; n < cur.nsteps; ++n, ++gs) {
-                const int ks = gs % kKStages;
-                const int at = n * kStepBlocks;
-                if ((at & 31) == 0) {
-                    if (at != 0) ids = ahead;
-                    const int b = at + 32 + lane;
-                    ahead = b < cur.nblk ? block_id(p, cur.seq, b0 + b, true) : -1;
+            if (!ok) {
+                if (lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT, cta);
+#pragma unroll 1
+                for (int s = 0; s < VS && s < gs; ++s) {
+                    const int last = gs - 1 - ((gs - 1 - s) % VS);
+                    wait_bounded(br.v_full(s), (last / VS) & 1);
                 }
-                if (gs >= kKStages && !wait_all(br.k_empty(ks), ((gs / kKStages) - 1) & 1)) {
+            }
+        } else if (warp == 2) {
+            // ==================== query tiles and score MMAs ====================
+            int gs = 0, q_staged = 0;
+            bool ok = true;
+#pragma unroll 1
+            for (int it = 0; ok; ++it) {
+                const int rec = it & 1;
+                if (!wait_all(br.piece_full(rec), (it >> 1) & 1)) {
                     ok = false;
                     break;
                 }
-                const int nb = min(kStepBlocks, cur.nblk - at);
-                // lane l: block l / CH of the step, chunk l % CH (a bad block
-                // reads rows before the cache: zeros)
-                const int b = min(lane / CH, kStepBlocks - 1), c = lane % CH;
-                const int id = __shfl_sync(0xffffffffu, ids, (at & 31) + b);
-                const uint32_t good = __ballot_sync(0xffffffffu, id >= 0 || lane >= nb * CH);
-                if (lane == 0) {
-                    valid[gs % kValidRing] = good;
-                    mbar_arrive_expect_tx(br.k_full(ks), nb * CH * kBS * 128);
-                }
+                const PieceHead pc = pieces[rec];
                 __syncwarp();
-                if (lane < nb * CH)
-                    tensor_g2s_3d(sb + Gm::kOffK + ks * Gm::kK + c * (kStepKeys * 128) +
-                                      b * (kBS * 128),
-                                  &tp.tm_k, 0, id >= 0 ? id * kBS : -kBS, cur.kvh * CH + c,
-                                  br.k_full(ks));
-                // (when the ring is full: the look-ups wait for memory)
-                if (n == min(kKStages, cur.nsteps) - 1) next_piece(nxt, nxt_ids);
-            }
-            cur = nxt;
-            cur_ids = nxt_ids;
-        }
-        if (!ok) {
-            if (lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT, cta);
-            // let the last copies land before the CTA can exit
-            for (int s = 0; s < kKStages && s < gs; ++s) {
-                const int last = gs - 1 - ((gs - 1 - s) % kKStages);
-                mbar_wait_bounded(br.k_full(s), (last / kKStages) & 1);
-            }
-        }
-    } else if (warp == 1) {
-        // ================================ values ================================
-        int gs = 0;
-        bool ok = true;
-        for (int it = 0; ok; ++it) {
-            const int rec = it & 1;
-            if (!wait_all(br.piece_full(rec), (it >> 1) & 1)) {
-                ok = false;
-                break;
-            }
-            const PieceHead pc = pieces[rec];
-            int ids = pieces[rec].ids[lane];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(br.piece_empty(rec));
-            if (pc.done) break;
-            const int b0 = pc.step0 * kStepBlocks;
-            int ahead = -1;
-            for (int n = 0; n < pc.nsteps; ++n, ++gs) {
-                const int vs = gs % kVStages;
-                const int at = n * kStepBlocks;
-                if ((at & 31) == 0) {
-                    if (at != 0) ids = ahead;
-                    const int b = at + 32 + lane;
-                    ahead = b < pc.nblk ? block_id(p, pc.seq, b0 + b, false) : -1;
-                }
-                if (gs >= kVStages && !wait_all(br.v_empty(vs), ((gs / kVStages) - 1) & 1)) {
-                    ok = false;
-                    break;
-                }
-                const int nb = min(kStepBlocks, pc.nblk - at);
-                if (lane == 0) mbar_arrive_expect_tx(br.v_full(vs), nb * Gm::kVBlock);
-                __syncwarp();
-                const int id = __shfl_sync(0xffffffffu, ids, (at & 31) + min(lane, kStepBlocks - 1));
-                if (lane < nb)
-                    tensor_g2s_3d(sb + Gm::kOffV + vs * Gm::kV + lane * Gm::kVBlock, &tp.tm_v, 0,
-                                  id >= 0 ? id * kBS : -kBS, pc.kvh * CH, br.v_full(vs));
-            }
-        }
-        if (!ok) {
-            if (lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT, cta);
-            for (int s = 0; s < kVStages && s < gs; ++s) {
-                const int last = gs - 1 - ((gs - 1 - s) % kVStages);
-                mbar_wait_bounded(br.v_full(s), (last / kVStages) & 1);
-            }
-        }
-    } else if (warp == 2) {
-        // ==================== query tiles and score MMAs ====================
-        int gs = 0, q_staged = 0;
-        bool ok = true;
-        for (int it = 0; ok; ++it) {
-            const int rec = it & 1;
-            if (!wait_all(br.piece_full(rec), (it >> 1) & 1)) {
-                ok = false;
-                break;
-            }
-            const PieceHead pc = pieces[rec];
-            const int nsteps = pc.nsteps, nblk = pc.nblk;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(br.piece_empty(rec));
-            if (pc.done) break;
-            // the query tile, once the previous piece's last scores are done
-            if (it >= 1) ok = wait_all(br.q_empty(), (it - 1) & 1);
-            if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(br.q_full(), Gm::kQ);
-            __syncwarp();
-            if (lane < CH)
-                tensor_g2s_3d(sb + lane * (kRows * 128), &tp.tm_q, 128 * lane, pc.kvh * G,
-                              pc.q0 + pc.tile * (kRows >> logG), br.q_full());
-            q_staged = it + 1;
-            ok = wait_all(br.q_full(), it & 1);
-            for (int n = 0; n < nsteps && ok; ++n, ++gs) {
-                const int ks = gs % kKStages, b = gs & 1;
-                ok = wait_all(br.k_full(ks), (gs / kKStages) & 1);
-                // the softmax has read the scores of two steps back
-                if (ok && gs >= 2) ok = wait_all(br.s_free(b), ((gs >> 1) - 1) & 1);
+                if (lane == 0) mbar_arrive(br.piece_empty(rec));
+                if (pc.done) break;
+                // the query tile, once the previous piece's last scores are done
+                if (it >= 1) ok = wait_all(br.q_empty(), (it - 1) & 1);
                 if (!ok) break;
-                tc::fence_after_sync();
-                if (lane == 0) {
-                    const int nb = min(kStepBlocks, nblk - n * kStepBlocks);
-                    const uint32_t idesc = tc::idesc_f16_f32(kRows, nb * kBS, false, false);
-                    const uint32_t k_s = sb + Gm::kOffK + ks * Gm::kK;
+                if (lane == 0) mbar_arrive_expect_tx(br.q_full(), Gm::kQ);
+                __syncwarp();
+                if (lane < CH)
+                    tensor_g2s_3d(sb + lane * (kRows * 128), &p.tm_q, 128 * lane, pc.kvh * G,
+                                  pc.q0 + pc.tile * (kRows >> logG), br.q_full());
+                q_staged = it + 1;
+                ok = wait_all(br.q_full(), it & 1);
+#pragma unroll 1
+                for (int n = 0; n < pc.nsteps && ok; ++n, ++gs) {
+                    const int ks = gs % KS, b = gs & 1;
+                    ok = FP8 ? wait_all(br.k16_full(), gs & 1)
+                             : wait_all(br.k_full(ks), (gs / KS) & 1);
+                    // the softmax has read the scores of two steps back
+                    if (ok && gs >= 2) ok = wait_all(br.s_free(b), ((gs >> 1) - 1) & 1);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    if (lane == 0) {
+                        const int nb = min(kStepBlocks, pc.nblk - n * kStepBlocks);
+                        // (bit 13: A is negated)
+                        const uint32_t idesc = tc::idesc_f16_f32(kRows, nb * kBS, false, false) |
+                                               (static_cast<uint32_t>(p.negate) << 13);
+                        const uint32_t k_s =
+                            sb + (FP8 ? Gm::kOffK16 : Gm::kOffK + ks * Gm::kStage);
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        tc::mma_ss(tmem + kTmemS + 128 * b,
-                                   tc::smem_desc(sb + (kk >> 2) * (kRows * 128) + (kk & 3) * 32, 16,
-                                                 1024, tc::kSwizzle128B),
-                                   tc::smem_desc(k_s + (kk >> 2) * (kStepKeys * 128) + (kk & 3) * 32,
-                                                 16, 1024, tc::kSwizzle128B),
-                                   idesc, kk > 0);
-                    tc::commit(br.s_full(b));
-                    mbar_arrive(br.s_full(b));  // passes the step's validity on
-                    tc::commit(br.k_empty(ks));
-                    if (n == nsteps - 1) tc::commit(br.q_empty());
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            tc::mma_ss(tmem + kTmemS + 128 * b,
+                                       tc::smem_desc(sb + (kk >> 2) * (kRows * 128) + (kk & 3) * 32,
+                                                     16, 1024, tc::kSwizzle128B),
+                                       tc::smem_desc(k_s + (kk >> 2) * 1024 + (kk & 3) * 32, 16,
+                                                     CH * 1024, tc::kSwizzle128B),
+                                       idesc, kk > 0);
+                        tc::commit(br.s_full(b));
+                        mbar_arrive(br.s_full(b));  // passes the step's validity and scales on
+                        if (!FP8) tc::commit(br.k_empty(ks));
+                        if (n == pc.nsteps - 1) tc::commit(br.q_empty());
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
+            if (!ok) {
+                if (lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT, cta);
+                if (q_staged) wait_bounded(br.q_full(), (q_staged - 1) & 1);
+            }
+        } else {
+            // ============================= P V MMAs =============================
+            constexpr uint32_t kIdescPV = tc::idesc_f16_f32(kRows, D, false, true);
+            int gs = 0;
+            bool ok = true;
+#pragma unroll 1
+            for (int it = 0; ok; ++it) {
+                const int rec = it & 1;
+                if (!wait_all(br.piece_full(rec), (it >> 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                const PieceHead pc = pieces[rec];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(br.piece_empty(rec));
+                if (pc.done) break;
+#pragma unroll 1
+                for (int n = 0; n < pc.nsteps && ok; ++n, ++gs) {
+                    const int vs = gs % VS, b = gs & 1;
+                    const int nb = min(kStepBlocks, pc.nblk - n * kStepBlocks);
+                    // the previous piece's O has been read
+                    if (n == 0 && it > 0) ok = wait_all(br.o_free(), (it - 1) & 1);
+                    if (ok)
+                        ok = FP8 ? wait_all(br.v16_full(b), (gs >> 1) & 1)
+                                 : wait_all(br.v_full(vs), (gs / VS) & 1);
+                    if (ok) ok = wait_all(br.p_full(b), (gs >> 1) & 1);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    if (lane == 0) {
+                        const uint32_t v_s =
+                            sb + (FP8 ? Gm::kOffV16 + b * Gm::kV : Gm::kOffV + vs * Gm::kStage);
+#pragma unroll 1
+                        for (int k = 0; k < nb; ++k)
+                            tc::mma_ts(tmem + kTmemO, tmem + kTmemP + 64 * b + 8 * k,
+                                       tc::smem_desc(v_s + k * Gm::kVBlock, kBS * 128, 1024,
+                                                     tc::kSwizzle128B),
+                                       kIdescPV, (n > 0 || k > 0) ? 1u : 0u);
+                        tc::commit(br.pv_done(b));
+                        mbar_arrive(br.pv_done(b));  // passes the piece's flags on
+                        if (!FP8) tc::commit(br.v_empty(vs));
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!ok && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT, cta);
         }
-        if (!ok) {
-            if (lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT, cta);
-            if (q_staged) mbar_wait_bounded(br.q_full(), (q_staged - 1) & 1);
-        }
-    } else if (warp == kPVWarp) {
-        // ============================= P V MMAs =============================
-        constexpr uint32_t kIdescPV = tc::idesc_f16_f32(kRows, D, false, true);
+    } else if (FP8 && warp >= kConvertWarp) {
+        // ========================= codes to fp16 tiles =========================
+        // Thread i also looks up key i's scales: its block id two steps ahead,
+        // the scales one step ahead.
+        const int tid = threadIdx.x - kConvertWarp * 32;
         int gs = 0;
-        bool ok = true;
+        bool ok = busy_cta;
+#pragma unroll 1
         for (int it = 0; ok; ++it) {
             const int rec = it & 1;
             if (!wait_all(br.piece_full(rec), (it >> 1) & 1)) {
@@ -827,43 +983,88 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 break;
             }
             const PieceHead pc = pieces[rec];
+            const int b_key = tid / kBS;  // block of this thread's key in a step
+            const int id0 = pieces[rec].ids[b_key], id1 = pieces[rec].ids[kStepBlocks + b_key];
             __syncwarp();
             if (lane == 0) mbar_arrive(br.piece_empty(rec));
             if (pc.done) break;
+            const int ctx = pc.L - pc.Q;
+            uint32_t *my_flags = flags + (it % 3) * kFlagWords;
+            const int64_t off = static_cast<int64_t>(tid % kBS) * Hk + pc.kvh;
+            // the scales of key tid of step n, whose block is id; 0: no such key
+            auto scale_of = [&](const float *scale, int id, int n) {
+                return id >= 0 && (pc.step0 + n) * kStepKeys + tid < pc.L
+                           ? __ldg(scale + static_cast<int64_t>(id) * kBS * Hk + off)
+                           : 0.f;
+            };
+            float ks = scale_of(p.k_scale, id0, 0), vs = scale_of(p.v_scale, id0, 0);
+            int id_next = pc.nsteps > 1 ? id1 : -1;
+#pragma unroll 1
             for (int n = 0; n < pc.nsteps && ok; ++n, ++gs) {
-                const int vs = gs % kVStages, b = gs & 1;
+                const int b = gs & 1, kst = gs % KS, vst = gs % VS;
                 const int nb = min(kStepBlocks, pc.nblk - n * kStepBlocks);
-                // the previous piece's O has been read
-                if (n == 0 && it > 0) ok = wait_all(br.o_free(), (it - 1) & 1);
-                if (ok) ok = wait_all(br.v_full(vs), (gs / kVStages) & 1);
+                const int key0 = (pc.step0 + n) * kStepKeys;
+                const float ks1 = scale_of(p.k_scale, id_next, n + 1);
+                const float vs1 = scale_of(p.v_scale, id_next, n + 1);
+                const int b2 = (n + 2) * kStepBlocks + b_key;
+                id_next = b2 < pc.nblk ? block_id(p, pc.seq, pc.step0 * kStepBlocks + b2, false) : -1;
+                // keys, once the scores of the step before are done with the
+                // tile.  (The softmax is then past the scales kScaleRing steps
+                // back: the values of the step before were not converted until
+                // the P V of three steps back was done.)
+                ok = wait_all(br.k_full(kst), (gs / KS) & 1);
+                if (ok && gs >= 1) ok = wait_all(br.s_full(b ^ 1), ((gs - 1) >> 1) & 1);
                 if (!ok) break;
-                const uint32_t v_s = sb + Gm::kOffV + vs * Gm::kV;
-                ok = wait_all(br.p_full(b), (gs >> 1) & 1);
-                if (!ok) break;
-                tc::fence_after_sync();
-                if (lane == 0) {
-                    for (int k = 0; k < nb; ++k)
-                        tc::mma_ts(tmem + kTmemO, tmem + kTmemP + 64 * b + 8 * k,
-                                   tc::smem_desc(v_s + k * Gm::kVBlock, kBS * 128, 1024,
-                                                 tc::kSwizzle128B),
-                                   kIdescPV, (n > 0 || k > 0) ? 1u : 0u);
-                    tc::commit(br.pv_done(b));
-                    tc::commit(br.v_empty(vs));
+                {
+                    const int ring = gs % kScaleRing;
+                    scales[ring * 2 * kStepKeys + tid] = ks;
+                    scales[ring * 2 * kStepKeys + kStepKeys + tid] = vs;
+                    // (the bits of non-negative floats order as they do)
+                    const uint32_t top = __reduce_max_sync(
+                        0xffffffffu, isfinite(vs) ? __float_as_uint(fabsf(vs)) : 0u);
+                    if (lane == 0) tops[ring * kConvertWarps + warp - kConvertWarp] = __uint_as_float(top);
                 }
+                convert_tile<D, false>(smem + Gm::kOffK + kst * Gm::kStage, smem + Gm::kOffK16, nb,
+                                       key0, ctx, pc.L, nullptr);
                 __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(br.k16_full());
+                    mbar_arrive(br.k_empty(kst));
+                }
+                // values, once the P V of two steps back is done with the tile
+                ok = wait_all(br.v_full(vst), (gs / VS) & 1);
+                if (ok && gs >= 2) ok = wait_all(br.pv_done(b), ((gs >> 1) - 1) & 1);
+                if (!ok) break;
+                if (n == 0) {
+                    // this piece's flags: last read three pieces back, before
+                    // the P V just waited for began its piece
+                    if (tid < kFlagWords) my_flags[tid] = 0;
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                }
+                convert_tile<D, true>(smem + Gm::kOffV + vst * Gm::kStage,
+                                      smem + Gm::kOffV16 + b * Gm::kV, nb, key0, ctx, pc.L,
+                                      my_flags);
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(br.v16_full(b));
+                    mbar_arrive(br.v_empty(vst));
+                }
+                ks = ks1;
+                vs = vs1;
             }
         }
-        if (!ok && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT, cta);
+        if (!ok && busy_cta && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT, cta);
     } else {
         // =============================== softmax ===============================
-        const int wh = (warp - 3) >> 2;
+        const int wh = (warp - kSoftmaxWarp) >> 2;
         const int quarter = warp & 3;
         const int h = lane >> 4;
         const int r = quarter * 32 + wh * 16 + (lane & 15);
         const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32 + wh * 16) << 16);
         const float sl2 = p.scale_log2;
         int gs = 0;
-        bool ok = true;
+        bool ok = busy_cta;
+#pragma unroll 1
         for (int it = 0; ok; ++it) {
             const int rec = it & 1;
             if (!wait_all(br.piece_full(rec), (it >> 1) & 1)) {
@@ -878,38 +1079,38 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const int rr = pc.tile * kRows + r;
             const bool row_ok = rr < pc.Q * G;
             const bool live = __any_sync(0xffffffffu, row_ok);
-            const int j = rr >> logG;
             const uint64_t *mask =
-                row_ok ? p.mask + static_cast<int64_t>(pc.q0 + j) * p.mask_words : nullptr;
+                row_ok ? p.mask + static_cast<int64_t>(pc.q0 + (rr >> logG)) * p.mask_words
+                       : nullptr;
             // bring the row's mask near, for the step that needs it
             if (row_ok) prefetch_l1(mask);
             uint32_t *my_flags = flags + (it % 3) * kFlagWords;
             float m_used = -INFINITY, l = 0.f;  // l: this thread's keys only
 
+#pragma unroll 1
             for (int n = 0; n < pc.nsteps; ++n, ++gs) {
                 const int sbuf = gs & 1;
                 const int key0 = (pc.step0 + n) * kStepKeys;
-                if (key0 + kStepKeys > ctx) {
-                    const int vs = gs % kVStages;
-                    if (!wait_all(br.v_full(vs), (gs / kVStages) & 1)) {
-                        ok = false;
-                        break;
+                const bool tail = key0 + kStepKeys > ctx;
+                uint64_t vis = ~0ull;
+                if (tail) {
+                    if constexpr (!FP8) {
+                        const int vs = gs % VS;
+                        if (!wait_all(br.v_full(vs), (gs / VS) & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        clean_values<CH>(smem + Gm::kOffV + vs * Gm::kStage, key0,
+                                         min(kStepBlocks, pc.nblk - n * kStepBlocks) * kBS, ctx,
+                                         pc.L, my_flags);
+                        __syncwarp();
                     }
-                    clean_values<CH>(smem + Gm::kOffV + vs * Gm::kV, key0,
-                                     min(kStepBlocks, pc.nblk - n * kStepBlocks) * kBS, ctx, pc.L,
-                                     my_flags, threadIdx.x - 3 * 32);
-                    __syncwarp();
+                    vis = visible(mask, p.mask_words, key0 + kHalfKeys * h, ctx, pc.L);
                 }
-                if (n == pc.nsteps - 1 && lane == 0) mbar_arrive(br.scanned());
                 if (!wait_all(br.s_full(sbuf), (gs >> 1) & 1)) {
                     ok = false;
                     break;
                 }
-                // the step's blocks that are in range: the key producer's word,
-                // one bit per copy (the ring is longer than it can be ahead:
-                // it stages at most kKStages steps past the scores, and these
-                // are at most two ahead of this warp)
-                const uint32_t copies = valid[gs % kValidRing];
                 if (!live) {
                     // (its rows of the weight buffer hold anything: they reach
                     // its rows of O alone; it keeps pace with the other warps,
@@ -928,24 +1129,43 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 for (int c = 0; c < kHalfKeys / 32; ++c)
                     tc::ld32_halves<kHalfKeys>(tl + kTmemS + 128 * sbuf + 32 * c,
                                                *reinterpret_cast<uint32_t(*)[32]>(sx + 32 * c));
+                // the step's blocks that are in range: the key producer's word
+                // (the ring is longer than it can be ahead: it stages at most
+                // three steps past the scores, and these are at most two ahead
+                // of this warp)
+                const uint32_t blocks = valid[gs % kValidRing];
                 tc::wait_ld();
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(br.s_free(sbuf));
-                const bool fast = copies == 0xffffffffu && key0 + kStepKeys <= ctx && sl2 >= 0.f;
-                if (!fast) {
-                    uint64_t vis = visible(mask, p.mask_words, key0 + kHalfKeys * h, ctx, pc.L);
+                const volatile float *sc = scales + (gs % kScaleRing) * 2 * kStepKeys + kHalfKeys * h;
+                float top2 = 0.f;  // log2 of the step's largest value scale
+                if constexpr (FP8) {
+                    const volatile float *t = tops + (gs % kScaleRing) * kConvertWarps;
+                    top2 = __log2f(fmaxf(fmax3(t[0], t[1], t[2]), fmaxf(t[3], 0x1p-100f)));
+#pragma unroll
+                    for (int e = 0; e < kHalfKeys; e += 4) {
+                        const float4 k4 = *const_cast<const float4 *>(
+                            reinterpret_cast<const volatile float4 *>(sc + e));
+                        const float2 a = f32x2_split(mul_f32x2(
+                            f32x2(__uint_as_float(sx[e]), __uint_as_float(sx[e + 1])), f32x2(k4.x, k4.y)));
+                        const float2 b = f32x2_split(mul_f32x2(
+                            f32x2(__uint_as_float(sx[e + 2]), __uint_as_float(sx[e + 3])), f32x2(k4.z, k4.w)));
+                        sx[e] = __float_as_uint(a.x);
+                        sx[e + 1] = __float_as_uint(a.y);
+                        sx[e + 2] = __float_as_uint(b.x);
+                        sx[e + 3] = __float_as_uint(b.y);
+                    }
+                }
+                const bool masked = tail || blocks != 0xffffffffu;
+                if (masked) {
 #pragma unroll
                     for (int b = 0; b < 4; ++b)
-                        if (!((copies >> (CH * (4 * h + b))) & 1u)) vis &= ~(0xFFFFull << (16 * b));
+                        if (!((blocks >> (4 * h + b)) & 1u)) vis &= ~(0xFFFFull << (16 * b));
+                    const uint32_t v0 = static_cast<uint32_t>(vis), v1 = static_cast<uint32_t>(vis >> 32);
 #pragma unroll
-                    for (int e = 0; e < kHalfKeys; ++e) {
-                        const uint32_t w = e < 32 ? static_cast<uint32_t>(vis)
-                                                  : static_cast<uint32_t>(vis >> 32);
-                        sx[e] = (w >> (e & 31)) & 1u
-                                    ? __float_as_uint(__uint_as_float(sx[e]) * sl2)
-                                    : __float_as_uint(-INFINITY);
-                    }
+                    for (int e = 0; e < kHalfKeys; ++e)
+                        if (!((e < 32 ? v0 : v1) & (1u << (e & 31)))) sx[e] = 0xFF800000u;  // -inf
                 }
                 float mr[8];
 #pragma unroll
@@ -954,12 +1174,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 for (int e = 0; e < kHalfKeys / 2; ++e)
                     mr[e & 7] = fmax3(mr[e & 7], __uint_as_float(sx[2 * e]),
                                       __uint_as_float(sx[2 * e + 1]));
-                float mx = fmax3(fmax3(mr[0], mr[1], mr[2]), fmax3(mr[3], mr[4], mr[5]),
-                                 fmaxf(mr[6], mr[7]));
-                if (fast) mx *= sl2;
+                const float mx = fmax3(fmax3(mr[0], mr[1], mr[2]), fmax3(mr[3], mr[4], mr[5]),
+                                       fmaxf(mr[6], mr[7]));
                 // the row's other half: the thread 16 lanes away
                 const float mo = __shfl_xor_sync(0xffffffffu, mx, 16);
-                const float m_new = fmaxf(m_used, fmaxf(mx, mo));
+                const float m_new = fmaxf(m_used, fmaf(fmaxf(mx, mo), sl2, top2));
                 const bool raise = m_new > m_used + kRescaleLog2;
                 // O holds this piece's earlier steps relative to m_used: rescale
                 // this thread's columns before the reference moves (the
@@ -972,7 +1191,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     }
                     tc::fence_after_sync();
                     const float alpha = resc ? ex2(m_used - m_new) : 1.f;
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < DH / 32; ++c) {
                         uint32_t x[32];
                         tc::ld32_halves<DH>(tl + kTmemO + 32 * c, x);
@@ -987,9 +1206,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
                 if (raise) m_used = m_new;
                 const float ms = m_used == -INFINITY ? 0.f : m_used;
-                // weights 2^(s * scale - m) (2^(t - m) for masked steps), fp16
-                // pairs; the P V of two steps back is done with this buffer
-                const float a = fast ? sl2 : 1.f;
+                // weights 2^(s - m), fp16 pairs; the P V of two steps back is
+                // done with this buffer
                 if (gs >= 2) {
                     if (!wait_all(br.pv_done(sbuf), ((gs >> 1) - 1) & 1)) {
                         ok = false;
@@ -997,15 +1215,26 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     }
                     tc::fence_after_sync();
                 }
-                const uint64_t a2 = f32x2(a, a), nms2 = f32x2(-ms, -ms);
+                const uint64_t a2 = f32x2(sl2, sl2), nms2 = f32x2(-ms, -ms);
                 uint64_t l2[4] = {0ull, 0ull, 0ull, 0ull};
                 uint32_t x[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
                     const float2 t = f32x2_split(fma_f32x2(
                         f32x2(__uint_as_float(sx[2 * e]), __uint_as_float(sx[2 * e + 1])), a2, nms2));
-                    const float p0 = ex2(t.x), p1 = ex2(t.y);
+                    float p0 = ex2(t.x), p1 = ex2(t.y);
                     l2[e & 3] = add_f32x2(l2[e & 3], f32x2(p0, p1));
+                    if constexpr (FP8) {
+                        const float2 v = *const_cast<const float2 *>(
+                            reinterpret_cast<const volatile float2 *>(sc + kStepKeys + 2 * e));
+                        const float2 w = f32x2_split(mul_f32x2(f32x2(p0, p1), f32x2(v.x, v.y)));
+                        p0 = w.x;
+                        p1 = w.y;
+                        if (masked) {  // (a masked key's scale may be anything)
+                            if (sx[2 * e] == 0xFF800000u) p0 = 0.f;
+                            if (sx[2 * e + 1] == 0xFF800000u) p1 = 0.f;
+                        }
+                    }
                     x[e] = pack_half2(p0, p1);
                 }
                 tc::st32_halves<32>(tl + kTmemP + 64 * sbuf, x);
@@ -1021,111 +1250,74 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
             // ---- the piece's output: O / l, or the partial state (m, l, O),
             // this thread's head dimensions
-            if (!wait_all(br.pv_done((gs - 1) & 1), ((gs - 1) >> 1) & 1) ||
-                !wait_all(br.scanned(), it & 1)) {
+            if (!wait_all(br.pv_done((gs - 1) & 1), ((gs - 1) >> 1) & 1)) {
                 ok = false;
                 break;
             }
-            // the flags of the piece after the next one: every warp has read
-            // what they held for the previous piece, and none reaches that
-            // piece before this warp's arrivals for the next
-            if (warp == 3 && lane < kFlagWords) flags[(it + 2) % 3 * kFlagWords + lane] = 0;
+            // fp16: the flags of the piece after the next one -- every warp has
+            // read what they held for the previous piece (it has since handed
+            // over this piece's weights), and none sets them before this warp
+            // has handed over the next piece's
+            if (!FP8 && warp == kSoftmaxWarp && lane < kFlagWords)
+                flags[(it + 2) % 3 * kFlagWords + lane] = 0;
             __syncwarp();
-            if (!live) {
-                if (lane == 0) mbar_arrive(br.o_free());
-                continue;
-            }
-            tc::fence_after_sync();
-            float o[DH];
-            {
-                uint32_t ob[DH];
+            if (live) {
+                tc::fence_after_sync();
+                uint32_t any = 0;
 #pragma unroll
-                for (int c = 0; c < DH / 32; ++c)
-                    tc::ld32_halves<DH>(tl + kTmemO + 32 * c,
-                                        *reinterpret_cast<uint32_t(*)[32]>(ob + 32 * c));
-                tc::wait_ld();
+                for (int w = 0; w < kFlagWords; ++w) any |= my_flags[w];
+                l += __shfl_xor_sync(0xffffffffu, l, 16);  // the row's sum over both halves' keys
+                const bool whole = pc.slot < 0;
+                const float inv = l > 0.f ? 1.f / l : l;  // (nothing visible: 0; NaN stays)
+                if (!whole && h == 0 && row_ok)
+                    p.part_ml[static_cast<int64_t>(pc.slot) * kRows + r] = make_float2(m_used, l);
+#pragma unroll 1
+                for (int k = 0; k < DH / 32; ++k) {  // 32 dims at a time
+                    uint32_t o[32];
+                    tc::ld32_halves<DH>(tl + kTmemO + 32 * k, o);
+                    tc::wait_ld();
+                    if (any != 0 && row_ok)
+                        add_non_finite<D, FP8>(p, pc, my_flags, mask, DH * h + 32 * k, o);
+                    if (whole) {
+                        // exchanged inside groups of four lanes, so that a store
+                        // of the warp covers 64 bytes of eight rows (16 bytes of
+                        // 32 rows each: 3 us for an item's outputs)
+                        uint4 x[4];
 #pragma unroll
-                for (int d = 0; d < DH; ++d) o[d] = __uint_as_float(ob[d]);
-            }
-            uint32_t any = 0;
+                        for (int c = 0; c < 4; ++c)
+                            x[c] = make_uint4(pack_scaled(o[8 * c], o[8 * c + 1], inv),
+                                              pack_scaled(o[8 * c + 2], o[8 * c + 3], inv),
+                                              pack_scaled(o[8 * c + 4], o[8 * c + 5], inv),
+                                              pack_scaled(o[8 * c + 6], o[8 * c + 7], inv));
+                        lane_transpose4(x, lane);
 #pragma unroll
-            for (int w = 0; w < kFlagWords; ++w) any |= my_flags[w];
-            if (any != 0 && row_ok) {
-                // the elements that were left out: a weight times an infinity
-                // or a NaN is that, whatever the (positive) weight
-                for (int node = 0; node < pc.Q; ++node) {
-                    if (!((my_flags[node >> 5] >> (node & 31)) & 1u) ||
-                        !((__ldg(mask + (node >> 6)) >> (node & 63)) & 1))
-                        continue;
-                    const int key = ctx + node;
-                    const int id = block_id(p, pc.seq, key / kBS, false);
-                    if (id < 0) continue;
-                    const __half *v = static_cast<const __half *>(p.v_cache) +
-                                      ((static_cast<int64_t>(id) * kBS + key % kBS) * Hk + pc.kvh) * D +
-                                      DH * h;
-#pragma unroll
-                    for (int d = 0; d < DH; ++d) {
-                        const float x = __half2float(v[d]);
-                        if (!isfinite(x)) o[d] += x;
-                    }
-                }
-            }
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(br.o_free());
-            l += __shfl_xor_sync(0xffffffffu, l, 16);  // the row's sum over both halves' keys
-            // a thread holds DH dims of one row: exchanged inside groups of
-            // lanes so that a warp's store covers whole lines of a few rows
-            // (stored as they lie, 32 lanes on 32 lines, an item's outputs
-            // took 3 us and its partial state 6)
-            const int r0 = quarter * 32 + wh * 16;
-            if (pc.slot < 0) {
-                const float inv = l > 0.f ? 1.f / l : l;  // (no visible key: 0; NaN stays)
-                constexpr int NC = DH / 8;  // 16-byte pieces of a thread's fp16 dims
-                uint4 x[NC];
-#pragma unroll
-                for (int c = 0; c < NC; ++c)
-                    x[c] = make_uint4(pack_half2(o[8 * c] * inv, o[8 * c + 1] * inv),
-                                      pack_half2(o[8 * c + 2] * inv, o[8 * c + 3] * inv),
-                                      pack_half2(o[8 * c + 4] * inv, o[8 * c + 5] * inv),
-                                      pack_half2(o[8 * c + 6] * inv, o[8 * c + 7] * inv));
-                lane_transpose<NC>(x, lane);
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const int src = (lane & ~(NC - 1)) + c;  // the lane the row came from
-                    const int row = pc.tile * kRows + r0 + (src & 15);
-                    if (row < pc.Q * G)
-                        *reinterpret_cast<uint4 *>(
-                            p.out + (static_cast<int64_t>(pc.q0 + (row >> logG)) * H + pc.kvh * G +
+                        for (int c = 0; c < 4; ++c) {
+                            const int src = (lane & ~3) + c;  // the lane the row came from
+                            const int row = pc.tile * kRows + quarter * 32 + wh * 16 + (src & 15);
+                            if (row < pc.Q * G)
+                                *reinterpret_cast<uint4 *>(
+                                    p.out +
+                                    (static_cast<int64_t>(pc.q0 + (row >> logG)) * H + pc.kvh * G +
                                      (row & (G - 1))) * D +
-                            DH * (src >> 4) + 8 * (lane & (NC - 1))) = x[c];
-                }
-            } else {
-                const int64_t row0 = static_cast<int64_t>(pc.slot) * kRows;
-                if (h == 0 && row_ok) tp.part_ml[row0 + r] = make_float2(m_used, l);
+                                    DH * (src >> 4) + 32 * k + 8 * (lane & 3)) = x[c];
+                        }
+                    } else if (row_ok) {
+                        // the rows of a half-warp side by side
+                        uint4 *dst = reinterpret_cast<uint4 *>(p.part_o) +
+                                     (static_cast<int64_t>(pc.slot) * (D / 4) +
+                                      (DH * h + 32 * k) / 4) * kRows + r;
 #pragma unroll
-                for (int k = 0; k < DH / 32; ++k) {
-                    uint4 x[8];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        x[c] = make_uint4(__float_as_uint(o[32 * k + 4 * c]),
-                                          __float_as_uint(o[32 * k + 4 * c + 1]),
-                                          __float_as_uint(o[32 * k + 4 * c + 2]),
-                                          __float_as_uint(o[32 * k + 4 * c + 3]));
-                    lane_transpose<8>(x, lane);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const int src = (lane & ~7) + c;
-                        const int row = r0 + (src & 15);
-                        if (pc.tile * kRows + row < pc.Q * G)
-                            *reinterpret_cast<uint4 *>(tp.part_o + (row0 + row) * D +
-                                                       DH * (src >> 4) + 32 * k + 4 * (lane & 7)) =
-                                x[c];
+                        for (int c = 0; c < 8; ++c)
+                            dst[c * kRows] =
+                                make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
                     }
                 }
+                tc::fence_before_sync();
+                __syncwarp();
             }
+            if (lane == 0) mbar_arrive(br.o_free());
         }
-        if (!ok && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT, cta);
+        if (!ok && busy_cta && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT, cta);
     }
 
     // every role is done: hand the tensor memory back
@@ -1139,56 +1331,66 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
 // Merges the partial states of the items that stretch borders cut: block
 // (b, y) takes rows kMergeRows y .. of the item that border b + 1 is the first
-// to cut.  D/8 threads per row, 8 dims each.  The item's first piece is the
-// last one of CTA b (its second slot), the others the first ones of the CTAs
-// that follow.
+// to cut.  The item's first piece is the last one of CTA b (its second slot),
+// the others the first ones of the CTAs that follow.  A thread takes one row
+// and D/4 / 16 groups of four dims, rows side by side as the states lie; the
+// result is turned round in shared memory for whole rows of output.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads)
-    tree_merge_kernel(const __grid_constant__ TileParams tp) {
-    constexpr int kPerRow = D / 8;
-    constexpr int kPass = kMergeThreads / kPerRow;  // rows at a time
+    tree_merge_kernel(const __grid_constant__ TreeParams p) {
+    constexpr int kGroups = kMergeThreads / kMergeRows;  // threads per row
+    constexpr int NQ = D / 4 / kGroups;                  // groups of four dims per thread
+    __shared__ uint2 turned[kMergeRows][D / 4 + 1];
     grid_dependency_wait();
     const int c0 = blockIdx.x;
-    const Border b = tp.borders[c0 + 1];
-    if (b.pieces == 0) return;
-    const TreeParams &p = tp.t;
+    const Border b = p.borders[c0 + 1];
+    const int row0 = blockIdx.y * kMergeRows;
+    if (b.pieces == 0 || row0 >= b.rows) return;
     const int G = p.num_heads / p.num_kv_heads, logG = __ffs(G) - 1;
-    for (int rr = blockIdx.y * kMergeRows + threadIdx.x / kPerRow;
-         rr < min(b.rows, static_cast<int>(blockIdx.y + 1) * kMergeRows); rr += kPass) {
-        const int d0 = 8 * (threadIdx.x % kPerRow);
-        float M = -INFINITY, den = 0.f, o[8];
+    const int rl = threadIdx.x % kMergeRows, g = threadIdx.x / kMergeRows;
+    const int rr = min(row0 + rl, b.rows - 1);
+    const float2 *ml0 = p.part_ml + static_cast<int64_t>(2 * c0) * kRows + rr;
+    const float4 *o0 = p.part_o + static_cast<int64_t>(2 * c0) * (D / 4) * kRows + rr;
+    float M = -INFINITY, den = 0.f, o[4 * NQ];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = 0.f;
+    for (int e = 0; e < 4 * NQ; ++e) o[e] = 0.f;
 #pragma unroll 8
-        for (int i = 0; i < b.pieces; ++i) {
-            const int64_t row = static_cast<int64_t>(2 * (c0 + i) + (i == 0)) * kRows + rr;
-            M = fmaxf(M, __ldcg(tp.part_ml + row).x);
-        }
+    for (int i = 0; i < b.pieces; ++i) {
+        const int slot = 2 * i + (i == 0);
+        M = fmaxf(M, __ldcg(ml0 + static_cast<int64_t>(slot) * kRows).x);
+    }
 #pragma unroll 4
-        for (int i = 0; i < b.pieces; ++i) {
-            const int64_t row = static_cast<int64_t>(2 * (c0 + i) + (i == 0)) * kRows + rr;
-            const float2 ml = __ldcg(tp.part_ml + row);
-            const float4 x = __ldcg(reinterpret_cast<const float4 *>(tp.part_o + row * D + d0));
-            const float4 y = __ldcg(reinterpret_cast<const float4 *>(tp.part_o + row * D + d0) + 1);
-            // (a piece without a visible finite score weighs nothing, but a NaN
-            // in its sum or its O stays)
-            const float w = ml.x == -INFINITY ? 1.f : ex2(ml.x - M);
-            den = fmaf(ml.y, w, den);
-            o[0] = fmaf(x.x, w, o[0]);
-            o[1] = fmaf(x.y, w, o[1]);
-            o[2] = fmaf(x.z, w, o[2]);
-            o[3] = fmaf(x.w, w, o[3]);
-            o[4] = fmaf(y.x, w, o[4]);
-            o[5] = fmaf(y.y, w, o[5]);
-            o[6] = fmaf(y.z, w, o[6]);
-            o[7] = fmaf(y.w, w, o[7]);
+    for (int i = 0; i < b.pieces; ++i) {
+        const int slot = 2 * i + (i == 0);
+        const float2 ml = __ldcg(ml0 + static_cast<int64_t>(slot) * kRows);
+        float4 x[NQ];
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+            x[q] = __ldcg(o0 + (static_cast<int64_t>(slot) * (D / 4) + g + kGroups * q) * kRows);
+        // (a piece without a visible finite score weighs nothing, but a NaN in
+        // its sum or its O stays)
+        const float w = ml.x == -INFINITY ? 1.f : ex2(ml.x - M);
+        den = fmaf(ml.y, w, den);
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+            o[4 * q] = fmaf(x[q].x, w, o[4 * q]);
+            o[4 * q + 1] = fmaf(x[q].y, w, o[4 * q + 1]);
+            o[4 * q + 2] = fmaf(x[q].z, w, o[4 * q + 2]);
+            o[4 * q + 3] = fmaf(x[q].w, w, o[4 * q + 3]);
         }
-        const float inv = den > 0.f ? 1.f / den : den;
-        __half *dst = p.out + (static_cast<int64_t>(b.q0 + (rr >> logG)) * p.num_heads + b.kvh * G +
-                               (rr & (G - 1))) * D + d0;
-        *reinterpret_cast<uint4 *>(dst) =
-            make_uint4(pack_half2(o[0] * inv, o[1] * inv), pack_half2(o[2] * inv, o[3] * inv),
-                       pack_half2(o[4] * inv, o[5] * inv), pack_half2(o[6] * inv, o[7] * inv));
+    }
+    const float inv = den > 0.f ? 1.f / den : den;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+        turned[rl][g + kGroups * q] = make_uint2(pack_half2(o[4 * q] * inv, o[4 * q + 1] * inv),
+                                                 pack_half2(o[4 * q + 2] * inv, o[4 * q + 3] * inv));
+    __syncthreads();
+    for (int i = threadIdx.x; i < kMergeRows * (D / 4); i += kMergeThreads) {
+        const int row = row0 + i / (D / 4);
+        if (row >= b.rows) break;
+        __half *dst = p.out + (static_cast<int64_t>(b.q0 + (row >> logG)) * p.num_heads +
+                               b.kvh * G + (row & (G - 1))) * D;
+        reinterpret_cast<uint2 *>(dst)[i % (D / 4)] = turned[i / (D / 4)][i % (D / 4)];
     }
 }
 
@@ -1205,36 +1407,93 @@ Scratch scratch(int ctas, int D) {
     return z;
 }
 
-// The tensor-core kernel and its merge, on `stream`.
-int launch_tiles(const TreeParams &t, int D, void *workspace, cudaStream_t stream) {
-    TileParams p{};
-    p.t = t;
-    const int Hk = t.num_kv_heads;
-    const int row_bytes = Hk * D * 2;
-    int st = dec::make_kv_tensor_map(&p.tm_k, t.k_cache, t.num_blocks, row_bytes, 1);
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                 const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// A tensor map over bytes; returns a PKV status.
+int encode(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims,
+           const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle swizzle) {
+    // the driver's encoder, found once through the runtime
+    static const EncodeTiled fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                             cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return static_cast<EncodeTiled>(nullptr);
+        return reinterpret_cast<EncodeTiled>(f);
+    }();
+    if (fn == nullptr) {
+        set_last_error("cuTensorMapEncodeTiled is not available from the driver");
+        return PKV_ERR_CUDA;
+    }
+    const cuuint32_t ones[4] = {1u, 1u, 1u, 1u};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<cuuint32_t>(rank),
+                          const_cast<void *>(base), dims, strides, box, ones,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        set_last_error("cuTensorMapEncodeTiled failed (tree attention)");
+        return PKV_ERR_CUDA;
+    }
+    return PKV_OK;
+}
+
+// fp16 keys [NB * 16][row_bytes] as {128 bytes, 8 rows, chunks, 8-row groups}:
+// one copy brings a head's chunks of a block, each 8 rows x 128 bytes -- the
+// unit of the MMA's swizzled operand -- on its own, in a uniform order.
+int make_key_map(CUtensorMap *map, const void *cache, int64_t num_blocks, int row_bytes, int D) {
+    const cuuint64_t row = static_cast<cuuint64_t>(row_bytes);
+    const cuuint64_t dims[4] = {128, 8, row / 128, static_cast<cuuint64_t>(num_blocks) * 2};
+    const cuuint64_t strides[3] = {row, 128, 8 * row};
+    const cuuint32_t box[4] = {128, 8, static_cast<cuuint32_t>(D / 64), 2};
+    return encode(map, cache, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Codes [NB * 16][row_bytes] by 16 rows of one head.
+int make_code_map(CUtensorMap *map, const void *cache, int64_t num_blocks, int row_bytes, int D) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes),
+                                static_cast<cuuint64_t>(num_blocks) * kBS};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(D), kBS};
+    return encode(map, cache, 2, dims, strides, box,
+                  D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+// The tile kernel and its merge, on `stream`.
+template <int D, bool FP8>
+int launch(TreeParams &p, void *workspace, cudaStream_t stream) {
+    using Gm = Geo<D, FP8>;
+    const int Hk = p.num_kv_heads;
+    const int row_bytes = Hk * D * (FP8 ? 1 : 2);
+    int st = FP8 ? make_code_map(&p.tm_k, p.k_cache, p.num_blocks, row_bytes, D)
+                 : make_key_map(&p.tm_k, p.k_cache, p.num_blocks, row_bytes, D);
     if (st == PKV_OK)
-        st = dec::make_kv_tensor_map(&p.tm_v, t.v_cache, t.num_blocks, row_bytes, D * 2 / 128);
+        st = FP8 ? make_code_map(&p.tm_v, p.v_cache, p.num_blocks, row_bytes, D)
+                 : dec::make_kv_tensor_map(&p.tm_v, p.v_cache, p.num_blocks, row_bytes, D / 64);
     if (st == PKV_OK)
-        st = dec::make_q_tensor_map(&p.tm_q, t.q, t.num_query_tokens, t.num_heads, D,
-                                    t.num_heads / Hk);
+        st = dec::make_q_tensor_map(&p.tm_q, p.q, p.num_query_tokens, p.num_heads, D,
+                                    p.num_heads / Hk);
     if (st != PKV_OK) return st;
     const int ctas = sm_count();
     const Scratch z = scratch(ctas, D);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.borders = reinterpret_cast<Border *>(ws);
     p.part_ml = reinterpret_cast<float2 *>(ws + z.borders);
-    p.part_o = reinterpret_cast<float *>(ws + z.borders + z.ml);
-    using Fn = void (*)(const TileParams);
-    const Fn fn = D == 128 ? tree_tile_kernel<128> : tree_tile_kernel<64>;
-    const int smem = tile_smem_bytes(D);
-    st = prepare_kernel(reinterpret_cast<const void *>(fn), kTileThreads, smem, nullptr);
+    p.part_o = reinterpret_cast<float4 *>(ws + z.borders + z.ml);
+    using Fn = void (*)(const TreeParams);
+    const Fn fn = tree_tile_kernel<D, FP8>;
+    const int smem = dec::kTileAlign + Gm::kBytes;
+    st = prepare_kernel(reinterpret_cast<const void *>(fn), Gm::kThreads, smem, nullptr);
     if (st != PKV_OK) return st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(kTileThreads);
+    cfg.blockDim = dim3(Gm::kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -1243,11 +1502,10 @@ int launch_tiles(const TreeParams &t, int D, void *workspace, cudaStream_t strea
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_failure(e, "tree_tile_kernel launch");
     if (ctas == 1) return PKV_OK;
-    const Fn merge = D == 128 ? tree_merge_kernel<128> : tree_merge_kernel<64>;
     cfg.gridDim = dim3(static_cast<unsigned>(ctas - 1), kRows / kMergeRows);
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, merge, p);
+    e = cudaLaunchKernelEx(&cfg, static_cast<Fn>(tree_merge_kernel<D>), p);
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? PKV_OK : cuda_failure(e, "tree_merge_kernel launch");
 }
@@ -1297,7 +1555,10 @@ int tree_attention(void *out, const void *q, const void *k_cache, const void *v_
     p.query_start = query_start;
     p.mask = tree_mask;
     p.mask_words = mask_words;
-    p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    // (a scale of zero weighs every finite score alike: so does one this small)
+    const double sl2 = static_cast<double>(scale) * 1.4426950408889634;
+    p.scale_log2 = static_cast<float>(std::max(std::abs(sl2), 1e-37));
+    p.negate = scale < 0.f;
     p.num_heads = num_heads;
     p.num_kv_heads = num_kv_heads;
     p.num_seqs = num_seqs;
@@ -1308,23 +1569,10 @@ int tree_attention(void *out, const void *q, const void *k_cache, const void *v_
     p.num_blocks = num_blocks;
     p.err = device_error_record();
     if (p.err == nullptr) return PKV_ERR_CUDA;
-    if (!fp8)
-        return launch_tiles(p, head_dim, workspace, reinterpret_cast<cudaStream_t>(stream));
-    using Fn = void (*)(const TreeParams);
-    const Fn fn = head_dim == 128 ? tree_rows_kernel<128> : tree_rows_kernel<64>;
-    const int64_t warps = static_cast<int64_t>(num_query_tokens) * num_heads;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((warps + 3) / 4));
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, fn, p);
-    if (e == cudaSuccess) e = cudaGetLastError();
-    return e == cudaSuccess ? PKV_OK : cuda_failure(e, "tree attention launch");
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (head_dim == 128)
+        return fp8 ? launch<128, true>(p, workspace, s) : launch<128, false>(p, workspace, s);
+    return fp8 ? launch<64, true>(p, workspace, s) : launch<64, false>(p, workspace, s);
 }
 
 }  // namespace
