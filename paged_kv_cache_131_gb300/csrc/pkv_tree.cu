@@ -8,10 +8,11 @@
 //
 // The rows of a (sequence, KV head) -- drafted token j, head g of the group:
 // row j*G + g -- are cut into tiles of 128 (the MMA's M), the cache into steps
-// of 128 keys.  The work is the list of (sequence, KV head, tile) items, each
+// of 128 keys.  The work is the list of (tile, sequence, KV head) items, each
 // its steps plus a start-up cost; one persistent CTA per SM takes an equal
 // contiguous stretch of the whole list, so a single long sequence fills the
-// GPU as well as a batch does.  An item cut by a stretch's border leaves fp32
+// GPU as well as a batch does, and the CTAs that work on different tiles of
+// the same keys do so at about the same time, out of L2.  An item cut by a stretch's border leaves fp32
 // partial states (m, l, O) in the workspace, and a second small kernel, whose
 // CTAs start as the first one's leave, merges them.  Bound: HBM while a tile's
 // 128-key step (64 KB of fp16 keys and values) costs less than its bytes, i.e.
@@ -114,6 +115,7 @@ struct TreeParams {
     int32_t max_blocks;
     int32_t num_query_tokens;
     int32_t max_query_len;
+    int32_t max_tiles;  // of a (sequence, KV head)
     int32_t max_seq_len;
     int64_t num_blocks;
     ErrorRecord *err;
@@ -352,8 +354,9 @@ __device__ __forceinline__ bool seq_geo(const TreeParams &p, int s, int G, bool 
     return Q > 0;
 }
 
-__device__ __forceinline__ int64_t seq_units(const SeqGeo &sg, int Hk) {
-    return static_cast<int64_t>(Hk) * sg.tiles * (sg.steps + kItemUnits);
+// Units of one tile of a sequence, all its KV heads.
+__device__ __forceinline__ int64_t tile_units(const SeqGeo &sg, int Hk) {
+    return static_cast<int64_t>(Hk) * (sg.steps + kItemUnits);
 }
 
 // Sum over the CTA of v, and the exclusive prefix of this thread's (every
@@ -416,7 +419,8 @@ __device__ __forceinline__ int block_id(const TreeParams &p, int seq, int b, boo
 struct Walk {
     int64_t u, u1;  // the next unit, the stretch's end
     SeqGeo sg;
-    int seq, n, item, x;  // the item (of n units) that u falls into, and u's place in it
+    int tile, seq, kvh;  // the item (of n units) that u falls into
+    int n, x;            // and u's place in it
 };
 
 // The next piece of the stretch (done: none is left), and lane l's id of its
@@ -430,11 +434,27 @@ __device__ __noinline__ PieceHead next_piece(const TreeParams &p, Walk &w, int c
     while (w.u < w.u1) {
         if (w.x == w.n) {  // the next item
             w.x = 0;
-            if (++w.item == Hk * w.sg.tiles) {  // of the next sequence with rows
-                w.item = 0;
-                do ++w.seq;
-                while (w.seq < p.num_seqs && !seq_geo(p, w.seq, G, false, w.sg));
-                if (w.seq >= p.num_seqs) return pc;  // (not reached: u1 is inside the list)
+            if (++w.kvh == Hk) {  // of the next sequence with such a tile
+                w.kvh = 0;
+                uint32_t found = 0;
+                for (int s0 = w.seq + 1; found == 0; s0 += 32) {
+                    if (s0 >= p.num_seqs) {
+                        s0 = 0;
+                        ++w.tile;
+                        if (w.tile >= p.max_tiles) return pc;  // (not reached: u1 is inside the list)
+                    }
+                    SeqGeo sg;
+                    const bool has = s0 + lane < p.num_seqs &&
+                                     seq_geo(p, s0 + lane, G, false, sg) && sg.tiles > w.tile;
+                    found = __ballot_sync(0xffffffffu, has);
+                    if (found != 0) {
+                        const int src = __ffs(found) - 1;
+                        w.seq = s0 + src;
+                        w.sg = make_geo(__shfl_sync(0xffffffffu, sg.L, src),
+                                        __shfl_sync(0xffffffffu, sg.Q, src),
+                                        __shfl_sync(0xffffffffu, sg.q0, src), G);
+                    }
+                }
                 w.n = w.sg.steps + kItemUnits;
             }
         }
@@ -444,8 +464,8 @@ __device__ __noinline__ PieceHead next_piece(const TreeParams &p, Walk &w, int c
         w.x += take;
         if (s1 == s0) continue;
         pc.seq = w.seq;
-        pc.kvh = w.item / w.sg.tiles;
-        pc.tile = w.item - pc.kvh * w.sg.tiles;
+        pc.kvh = w.kvh;
+        pc.tile = w.tile;
         pc.step0 = s0;
         pc.nsteps = s1 - s0;
         pc.nblk = min((w.sg.L + kBS - 1) / kBS - s0 * kStepBlocks, pc.nsteps * kStepBlocks);
@@ -543,8 +563,9 @@ __device__ __forceinline__ void add_non_finite(const TreeParams &p, const PieceH
         for (int d = 0; d < 32; ++d) {
             float x;
             if constexpr (FP8) {
-                const uint8_t c = static_cast<const uint8_t *>(p.v_cache)[at + d];
-                x = (c & 0x7Fu) == 0x7Fu ? NAN : 0.f;
+                __nv_fp8_e4m3 c;
+                c.__x = static_cast<const uint8_t *>(p.v_cache)[at + d];
+                x = static_cast<float>(c) * __ldg(p.v_scale + at / D);
             } else {
                 x = __half2float(static_cast<const __half *>(p.v_cache)[at + d]);
             }
@@ -571,32 +592,54 @@ __device__ __forceinline__ void codes_to_half(const uint4 &c, uint4 &lo, uint4 &
 // A step's codes (staged [block][token][D bytes], swizzled as D asks) as the
 // fp16 key (V = false) or value tile, by the 128 converter threads.  Eight
 // lanes take half a row each of two neighbouring rows, opposite halves, so
-// that their reads and their writes fall on eight different 16-byte columns.
+// that their reads and their writes fall on eight different 16-byte columns;
+// a thread's units are whole blocks apart, their places constants apart.
+// `clean`: the values of a step that reaches past the context.
 template <int D, bool V>
-__device__ __forceinline__ void convert_tile(const uint8_t *codes, uint8_t *tile, int blocks,
-                                             int key0, int ctx, int L, uint32_t *flags) {
+__device__ __forceinline__ void convert_tile(const uint8_t *codes, uint8_t *tile, int keys,
+                                             bool clean, int key0, int ctx, int L,
+                                             uint32_t *flags) {
     constexpr int CH = D / 64;
-    constexpr int kGroups = kConvertWarps * 4;  // groups of eight lanes
+    constexpr int kRowsApart = 32 / CH;                      // rows between a thread's units
+    constexpr int kUnits = kStepKeys / kRowsApart;           // per thread
+    constexpr int kTileApart = kRowsApart / kBS * CH * kBS * 128;
     const int tid = threadIdx.x - kConvertWarp * 32;
-    const int p = tid & 7;
-    const bool tail = V && key0 + kStepKeys > ctx;
-#pragma unroll 4
-    for (int g = tid >> 3; g < blocks * (kBS / 2) * CH; g += kGroups) {
-        const int rp = g / CH, sel = g % CH;
-        const int t = 2 * rp + (p >> 2);
-        const int u = CH == 2 ? (p & 3) | (((p >> 2) ^ sel) << 2) : p & 3;
-        const int su = D == 128 ? u ^ (t & 7) : u ^ ((t >> 1) & 3);
-        uint4 lo, hi;
-        codes_to_half(*reinterpret_cast<const uint4 *>(codes + t * D + su * 16), lo, hi);
-        if (tail) {
-            lo = clean_unit(lo, key0 + t, ctx, L, flags);
-            hi = clean_unit(hi, key0 + t, ctx, L, flags);
+    const int p = tid & 7, g = tid >> 3;
+    const int t = 2 * (g / CH) + (p >> 2);
+    const int u = CH == 2 ? (p & 3) | (((p >> 2) ^ (g & 1)) << 2) : p & 3;
+    const int su = D == 128 ? u ^ (t & 7) : u ^ ((t >> 1) & 3);
+    const uint8_t *src = codes + t * D + su * 16;
+    const int c = u >> 2, x = 2 * (u & 3);
+    uint8_t *row = tile + (V ? (t >> 4) * (CH * kBS * 128) + c * (kBS * 128) + (t & 15) * 128
+                             : (t >> 3) * (CH * 1024) + c * 1024 + (t & 7) * 128);
+    uint8_t *d0 = row + ((x ^ (t & 7)) * 16), *d1 = row + (((x + 1) ^ (t & 7)) * 16);
+    if (keys == kStepKeys && !clean) {
+#pragma unroll
+        for (int i0 = 0; i0 < kUnits; i0 += 4) {
+            uint4 in[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                in[i] = *reinterpret_cast<const uint4 *>(src + (i0 + i) * kRowsApart * D);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint4 lo, hi;
+                codes_to_half(in[i], lo, hi);
+                *reinterpret_cast<uint4 *>(d0 + (i0 + i) * kTileApart) = lo;
+                *reinterpret_cast<uint4 *>(d1 + (i0 + i) * kTileApart) = hi;
+            }
         }
-        const int c = u >> 2, x = 2 * (u & 3);
-        uint8_t *row = tile + (V ? (t >> 4) * (CH * kBS * 128) + c * (kBS * 128) + (t & 15) * 128
-                                 : (t >> 3) * (CH * 1024) + c * 1024 + (t & 7) * 128);
-        *reinterpret_cast<uint4 *>(row + ((x ^ (t & 7)) * 16)) = lo;
-        *reinterpret_cast<uint4 *>(row + (((x + 1) ^ (t & 7)) * 16)) = hi;
+    } else {
+#pragma unroll 1
+        for (int i = 0; i < kUnits && t + i * kRowsApart < keys; ++i) {
+            uint4 lo, hi;
+            codes_to_half(*reinterpret_cast<const uint4 *>(src + i * kRowsApart * D), lo, hi);
+            if (clean) {
+                lo = clean_unit(lo, key0 + t + i * kRowsApart, ctx, L, flags);
+                hi = clean_unit(hi, key0 + t + i * kRowsApart, ctx, L, flags);
+            }
+            *reinterpret_cast<uint4 *>(d0 + i * kTileApart) = lo;
+            *reinterpret_cast<uint4 *>(d1 + i * kTileApart) = hi;
+        }
     }
     fence_proxy_async_smem();
 }
@@ -618,9 +661,9 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
     volatile uint32_t *valid = reinterpret_cast<volatile uint32_t *>(smem + Gm::kOffValid);
     volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(smem + Gm::kOffMisc);
     int64_t *scan = reinterpret_cast<int64_t *>(smem + Gm::kOffScan);
-    volatile int64_t *start = scan + Gm::kThreads / 32;  // sequence, its first unit, L | Q, q0
-    volatile float *scales = reinterpret_cast<volatile float *>(smem + Gm::kOffScale);
-    volatile float *tops = reinterpret_cast<volatile float *>(smem + Gm::kOffTop);
+    volatile int64_t *start = scan + Gm::kThreads / 32;  // tile | sequence, its first unit, L | Q, q0
+    float *scales = reinterpret_cast<float *>(smem + Gm::kOffScale);
+    float *tops = reinterpret_cast<float *>(smem + Gm::kOffTop);
 
     const int Hk = p.num_kv_heads, H = p.num_heads;
     const int G = H / Hk, logG = __ffs(G) - 1;
@@ -665,40 +708,42 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
     grid_launch_dependents();  // the merge: it waits for this grid
 
     // ---- the list's length, and where this CTA's stretch starts: the thread
-    // that holds the sequence its first unit falls into says so.  (With more
-    // sequences than threads the list is gone through twice.)
-    int64_t units = 0;
-    int busy = 0;  // CTAs with a stretch
-    int64_t u0 = 0, u1 = 0;
+    // that holds the sequence its first unit falls into says so
+    const bool one_go = p.num_seqs <= Gm::kThreads;  // a thread per sequence
+    int64_t units = 0, before = 0;
+    SeqGeo sg{};
 #pragma unroll 1
-    for (int pass = p.num_seqs <= Gm::kThreads ? 1 : 0; pass < 2; ++pass) {
-        int64_t run = 0;
+    for (int s0 = 0; s0 < p.num_seqs; s0 += Gm::kThreads) {
+        const int s = s0 + threadIdx.x;
+        if (!(s < p.num_seqs && seq_geo(p, s, G, cta == 0, sg))) sg.tiles = 0;
+        int64_t total;
+        before = cta_scan<Gm::kThreads / 32>(sg.tiles * tile_units(sg, Hk), scan, total);
+        units += total;
+    }
+    const int busy = static_cast<int>(min(static_cast<int64_t>(ctas), units));  // CTAs with a stretch
+    const int64_t u0 = busy ? stretch(units, cta, busy) : 0;
+    const int64_t u1 = busy ? stretch(units, cta + 1, busy) : 0;
+    {
+        int64_t run = 0;  // units of the tiles and sequences gone through
+        const bool known = one_go && p.max_tiles == 1;  // the scan above found the places
 #pragma unroll 1
-        for (int s0 = 0; s0 < p.num_seqs; s0 += Gm::kThreads) {
-            const int s = s0 + threadIdx.x;
-            SeqGeo sg;
-            const bool has =
-                s < p.num_seqs && seq_geo(p, s, G, cta == 0 && run == 0 && units == 0, sg);
-            int64_t total;
-            const int64_t w = has ? seq_units(sg, Hk) : 0;
-            const int64_t before = run + cta_scan<Gm::kThreads / 32>(w, scan, total);
-            run += total;
-            if (pass == 1) {
-                if (p.num_seqs <= Gm::kThreads) units = total;
-                busy = static_cast<int>(min(static_cast<int64_t>(ctas), units));
-                if (busy != 0) {
-                    u0 = stretch(units, cta, busy);
-                    u1 = stretch(units, cta + 1, busy);
-                }
-                if (cta < busy && w > 0 && before <= u0 && u0 < before + w) {
-                    start[0] = s;
+        for (int tile = 0; tile < p.max_tiles && run <= u0 && cta < busy; ++tile) {
+#pragma unroll 1
+            for (int s0 = 0; s0 < p.num_seqs; s0 += Gm::kThreads) {
+                const int s = s0 + threadIdx.x;
+                if (!one_go && !(s < p.num_seqs && seq_geo(p, s, G, false, sg))) sg.tiles = 0;
+                const int64_t w = sg.tiles > tile ? tile_units(sg, Hk) : 0;
+                int64_t total = units;
+                if (!known) before = run + cta_scan<Gm::kThreads / 32>(w, scan, total);
+                if (w > 0 && before <= u0 && u0 < before + w) {
+                    start[0] = static_cast<int64_t>(tile) << 32 | s;
                     start[1] = before;
                     start[2] = static_cast<int64_t>(sg.L) << 32 | static_cast<unsigned>(sg.Q);
                     start[3] = sg.q0;
                 }
+                run += total;
             }
         }
-        if (pass == 0) units = run;
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -713,28 +758,28 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
             // ========================= pieces and keys =========================
             Walk w;
             w.seq = static_cast<int>(start[0]);
-            const int64_t first = start[1];  // the sequence's first unit
+            w.tile = static_cast<int>(start[0] >> 32);
+            const int64_t first = start[1];  // the first unit of the sequence's tile
             w.u = u0;
             w.u1 = u1;
             w.sg = make_geo(static_cast<int>(start[2] >> 32), static_cast<int>(start[2]),
                             static_cast<int>(start[3]), G);
             w.n = w.sg.steps + kItemUnits;
-            w.item = static_cast<int>((u0 - first) / w.n);
-            w.x = static_cast<int>(u0 - first - static_cast<int64_t>(w.item) * w.n);
+            w.kvh = static_cast<int>((u0 - first) / w.n);
+            w.x = static_cast<int>(u0 - first - static_cast<int64_t>(w.kvh) * w.n);
             // the border at u0, for the merge (every CTA writes one, whether or
             // not its stretch holds a step)
             if (lane == 0) {
                 Border border;
                 const int64_t a = u0 - w.x;  // the item's first unit
-                const int tile = w.item % w.sg.tiles;
                 const bool cuts = cta > 0 && step_at(w.x, w.sg.steps) > 0 &&
                                   step_at(stretch(units, cta - 1, busy) - a, w.sg.steps) == 0;
                 // pieces: the CTA before this one, and those up to the item's last unit
                 border.pieces =
                     cuts ? static_cast<int>(((a + w.n) * busy - 1) / units) - (cta - 1) + 1 : 0;
-                border.rows = min(kRows, w.sg.Q * G - tile * kRows);
-                border.q0 = w.sg.q0 + tile * (kRows >> logG);
-                border.kvh = w.item / w.sg.tiles;
+                border.rows = min(kRows, w.sg.Q * G - w.tile * kRows);
+                border.q0 = w.sg.q0 + w.tile * (kRows >> logG);
+                border.kvh = w.kvh;
                 p.borders[cta] = border;
             }
             __syncwarp();
@@ -1018,14 +1063,17 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                 {
                     const int ring = gs % kScaleRing;
                     scales[ring * 2 * kStepKeys + tid] = ks;
-                    scales[ring * 2 * kStepKeys + kStepKeys + tid] = vs;
+                    // (a drafted row's scale that is not finite counts as its
+                    // non-finite elements do: left out here, added at the end)
+                    const bool out = !isfinite(vs) && tid + key0 >= ctx;
+                    scales[ring * 2 * kStepKeys + kStepKeys + tid] = out ? 0.f : vs;
                     // (the bits of non-negative floats order as they do)
                     const uint32_t top = __reduce_max_sync(
                         0xffffffffu, isfinite(vs) ? __float_as_uint(fabsf(vs)) : 0u);
                     if (lane == 0) tops[ring * kConvertWarps + warp - kConvertWarp] = __uint_as_float(top);
                 }
-                convert_tile<D, false>(smem + Gm::kOffK + kst * Gm::kStage, smem + Gm::kOffK16, nb,
-                                       key0, ctx, pc.L, nullptr);
+                convert_tile<D, false>(smem + Gm::kOffK + kst * Gm::kStage, smem + Gm::kOffK16,
+                                       nb * kBS, false, key0, ctx, pc.L, nullptr);
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(br.k16_full());
@@ -1041,9 +1089,12 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                     if (tid < kFlagWords) my_flags[tid] = 0;
                     asm volatile("bar.sync 1, 128;" ::: "memory");
                 }
+                const bool tail = key0 + kStepKeys > ctx;
+                if (tail && tid + key0 >= ctx && !isfinite(vs))  // (its stored scale is 0)
+                    atomicOr(&my_flags[(tid + key0 - ctx) >> 5], 1u << ((tid + key0 - ctx) & 31));
                 convert_tile<D, true>(smem + Gm::kOffV + vst * Gm::kStage,
-                                      smem + Gm::kOffV16 + b * Gm::kV, nb, key0, ctx, pc.L,
-                                      my_flags);
+                                      smem + Gm::kOffV16 + b * Gm::kV, nb * kBS, tail, key0, ctx,
+                                      pc.L, my_flags);
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(br.v16_full(b));
@@ -1138,15 +1189,14 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(br.s_free(sbuf));
-                const volatile float *sc = scales + (gs % kScaleRing) * 2 * kStepKeys + kHalfKeys * h;
+                const float *sc = scales + (gs % kScaleRing) * 2 * kStepKeys + kHalfKeys * h;
                 float top2 = 0.f;  // log2 of the step's largest value scale
                 if constexpr (FP8) {
-                    const volatile float *t = tops + (gs % kScaleRing) * kConvertWarps;
+                    const float *t = tops + (gs % kScaleRing) * kConvertWarps;
                     top2 = __log2f(fmaxf(fmax3(t[0], t[1], t[2]), fmaxf(t[3], 0x1p-100f)));
 #pragma unroll
                     for (int e = 0; e < kHalfKeys; e += 4) {
-                        const float4 k4 = *const_cast<const float4 *>(
-                            reinterpret_cast<const volatile float4 *>(sc + e));
+                        const float4 k4 = *reinterpret_cast<const float4 *>(sc + e);
                         const float2 a = f32x2_split(mul_f32x2(
                             f32x2(__uint_as_float(sx[e]), __uint_as_float(sx[e + 1])), f32x2(k4.x, k4.y)));
                         const float2 b = f32x2_split(mul_f32x2(
@@ -1218,6 +1268,7 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                 const uint64_t a2 = f32x2(sl2, sl2), nms2 = f32x2(-ms, -ms);
                 uint64_t l2[4] = {0ull, 0ull, 0ull, 0ull};
                 uint32_t x[32];
+                float4 v4;  // FP8: the value scales of four keys
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
                     const float2 t = f32x2_split(fma_f32x2(
@@ -1225,15 +1276,11 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                     float p0 = ex2(t.x), p1 = ex2(t.y);
                     l2[e & 3] = add_f32x2(l2[e & 3], f32x2(p0, p1));
                     if constexpr (FP8) {
-                        const float2 v = *const_cast<const float2 *>(
-                            reinterpret_cast<const volatile float2 *>(sc + kStepKeys + 2 * e));
-                        const float2 w = f32x2_split(mul_f32x2(f32x2(p0, p1), f32x2(v.x, v.y)));
+                        if ((e & 1) == 0) v4 = *reinterpret_cast<const float4 *>(sc + kStepKeys + 2 * e);
+                        const float2 w = f32x2_split(mul_f32x2(
+                            f32x2(p0, p1), (e & 1) ? f32x2(v4.z, v4.w) : f32x2(v4.x, v4.y)));
                         p0 = w.x;
                         p1 = w.y;
-                        if (masked) {  // (a masked key's scale may be anything)
-                            if (sx[2 * e] == 0xFF800000u) p0 = 0.f;
-                            if (sx[2 * e + 1] == 0xFF800000u) p1 = 0.f;
-                        }
                     }
                     x[e] = pack_half2(p0, p1);
                 }
@@ -1565,6 +1612,7 @@ int tree_attention(void *out, const void *q, const void *k_cache, const void *v_
     p.max_blocks = max_blocks_per_seq;
     p.num_query_tokens = num_query_tokens;
     p.max_query_len = max_query_len;
+    p.max_tiles = (max_query_len * G + kRows - 1) / kRows;
     p.max_seq_len = max_seq_len;
     p.num_blocks = num_blocks;
     p.err = device_error_record();
