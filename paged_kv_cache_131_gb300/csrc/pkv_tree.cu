@@ -405,14 +405,33 @@ __device__ __forceinline__ uint64_t visible(const uint64_t *mask, int words, int
     return n >= 64 ? m : n <= 0 ? 0ull : m & ((1ull << n) - 1);
 }
 
-// Block id of entry b of a sequence, or -1 when out of range (recorded when
+// Loads that are issued where they stand (a plain one may sink to its use).
+__device__ __forceinline__ int load_early(const int32_t *p) {
+    int v;
+    asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ float load_early(const float *p) {
+    float v;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+
+// Entry b of a sequence's block table as it stands: looked up ahead of its use,
+// so that only checked_id, at the use, waits for it.
+__device__ __forceinline__ int table_entry(const TreeParams &p, int seq, int b) {
+    return load_early(p.block_tables + static_cast<int64_t>(seq) * p.max_blocks + b);
+}
+// The block id of entry b, or -1 when it is out of range (recorded when
 // `report`).
-__device__ __forceinline__ int block_id(const TreeParams &p, int seq, int b, bool report) {
-    const int64_t at = static_cast<int64_t>(seq) * p.max_blocks + b;
-    const int id = __ldg(p.block_tables + at);
+__device__ __forceinline__ int checked_id(const TreeParams &p, int id, int seq, int b, bool report) {
     if (id >= 0 && static_cast<int64_t>(id) < p.num_blocks) return id;
-    if (report) record_error(p.err, PKV_DEVERR_BLOCK_ID, at);
+    if (report)
+        record_error(p.err, PKV_DEVERR_BLOCK_ID, static_cast<int64_t>(seq) * p.max_blocks + b);
     return -1;
+}
+__device__ __forceinline__ int block_id(const TreeParams &p, int seq, int b, bool report) {
+    return checked_id(p, table_entry(p, seq, b), seq, b, report);
 }
 
 // Walks a CTA's stretch.
@@ -809,9 +828,10 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                     const int ks = gs % KS;
                     const int at = n * kStepBlocks;
                     if ((at & 31) == 0) {
-                        if (at != 0) ids = ahead;
+                        if (at != 0 && at + lane < cur.nblk)
+                            ids = checked_id(p, ahead, cur.seq, b0 + at + lane, true);
                         const int b = at + 32 + lane;
-                        ahead = b < cur.nblk ? block_id(p, cur.seq, b0 + b, true) : -1;
+                        if (b < cur.nblk) ahead = table_entry(p, cur.seq, b0 + b);
                     }
                     if (gs >= KS && !wait_all(br.k_empty(ks), ((gs / KS) - 1) & 1)) {
                         ok = false;
@@ -874,9 +894,10 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                     const int vs = gs % VS;
                     const int at = n * kStepBlocks;
                     if ((at & 31) == 0) {
-                        if (at != 0) ids = ahead;
+                        if (at != 0 && at + lane < pc.nblk)
+                            ids = checked_id(p, ahead, pc.seq, b0 + at + lane, false);
                         const int b = at + 32 + lane;
-                        ahead = b < pc.nblk ? block_id(p, pc.seq, b0 + b, false) : -1;
+                        if (b < pc.nblk) ahead = table_entry(p, pc.seq, b0 + b);
                     }
                     if (gs >= VS && !wait_all(br.v_empty(vs), ((gs / VS) - 1) & 1)) {
                         ok = false;
@@ -1039,20 +1060,16 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
             // the scales of key tid of step n, whose block is id; 0: no such key
             auto scale_of = [&](const float *scale, int id, int n) {
                 return id >= 0 && (pc.step0 + n) * kStepKeys + tid < pc.L
-                           ? __ldg(scale + static_cast<int64_t>(id) * kBS * Hk + off)
+                           ? load_early(scale + static_cast<int64_t>(id) * kBS * Hk + off)
                            : 0.f;
             };
             float ks = scale_of(p.k_scale, id0, 0), vs = scale_of(p.v_scale, id0, 0);
-            int id_next = pc.nsteps > 1 ? id1 : -1;
+            int entry = pc.nsteps > 1 ? id1 : -1;  // of this key's block of the next step
 #pragma unroll 1
             for (int n = 0; n < pc.nsteps && ok; ++n, ++gs) {
                 const int b = gs & 1, kst = gs % KS, vst = gs % VS;
                 const int nb = min(kStepBlocks, pc.nblk - n * kStepBlocks);
                 const int key0 = (pc.step0 + n) * kStepKeys;
-                const float ks1 = scale_of(p.k_scale, id_next, n + 1);
-                const float vs1 = scale_of(p.v_scale, id_next, n + 1);
-                const int b2 = (n + 2) * kStepBlocks + b_key;
-                id_next = b2 < pc.nblk ? block_id(p, pc.seq, pc.step0 * kStepBlocks + b2, false) : -1;
                 // keys, once the scores of the step before are done with the
                 // tile.  (The softmax is then past the scales kScaleRing steps
                 // back: the values of the step before were not converted until
@@ -1072,6 +1089,18 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                         0xffffffffu, isfinite(vs) ? __float_as_uint(fabsf(vs)) : 0u);
                     if (lane == 0) tops[ring * kConvertWarps + warp - kConvertWarp] = __uint_as_float(top);
                 }
+                const bool left_out = !isfinite(vs);
+                // the next step's scales, and the one's block after it (after
+                // this step's have been used: waiting for a load waits for the
+                // ones issued since)
+                {
+                    const int id_next = checked_id(p, entry, 0, 0, false);
+                    ks = scale_of(p.k_scale, id_next, n + 1);
+                    vs = scale_of(p.v_scale, id_next, n + 1);
+                    const int b2 = (n + 2) * kStepBlocks + b_key;
+                    entry = -1;
+                    if (b2 < pc.nblk) entry = table_entry(p, pc.seq, pc.step0 * kStepBlocks + b2);
+                }
                 convert_tile<D, false>(smem + Gm::kOffK + kst * Gm::kStage, smem + Gm::kOffK16,
                                        nb * kBS, false, key0, ctx, pc.L, nullptr);
                 __syncwarp();
@@ -1090,7 +1119,7 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                     asm volatile("bar.sync 1, 128;" ::: "memory");
                 }
                 const bool tail = key0 + kStepKeys > ctx;
-                if (tail && tid + key0 >= ctx && !isfinite(vs))  // (its stored scale is 0)
+                if (tail && tid + key0 >= ctx && left_out)  // (its stored scale is 0)
                     atomicOr(&my_flags[(tid + key0 - ctx) >> 5], 1u << ((tid + key0 - ctx) & 31));
                 convert_tile<D, true>(smem + Gm::kOffV + vst * Gm::kStage,
                                       smem + Gm::kOffV16 + b * Gm::kV, nb * kBS, tail, key0, ctx,
@@ -1100,8 +1129,6 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                     mbar_arrive(br.v16_full(b));
                     mbar_arrive(br.v_empty(vst));
                 }
-                ks = ks1;
-                vs = vs1;
             }
         }
         if (!ok && busy_cta && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT, cta);
