@@ -95,7 +95,8 @@ constexpr int kMergeRows = 16;
 struct TreeParams {
     CUtensorMap tm_k;
     CUtensorMap tm_v;
-    CUtensorMap tm_q;  // query rows: 128 bytes of each row of a 128-row tile
+    CUtensorMap tm_q;    // query rows: 128 bytes of each row of a 128-row tile
+    CUtensorMap tm_q16;  // the same of 16 rows
     __half *out;
     const __half *q;
     const void *k_cache;
@@ -333,6 +334,11 @@ __device__ __forceinline__ int64_t stretch(int64_t units, int c, int busy) {
 struct SeqGeo {
     int L, Q, q0, tiles, steps;
 };
+
+// Up to 64 rows are laid out as four groups of 16, one in each quarter of the
+// tile, so that every quarter of the SM has one softmax warp at work instead of
+// half of them two (FP8, 64 rows: 3200 -> 2500 cycles a step).
+__device__ __forceinline__ bool spread_rows(int rows) { return rows <= kRows / 2; }
 
 __device__ __forceinline__ SeqGeo make_geo(int L, int Q, int q0, int G) {
     return SeqGeo{L, Q, q0, (Q * G + kRows - 1) / kRows, (L + kStepKeys - 1) / kStepKeys};
@@ -663,6 +669,29 @@ __device__ __forceinline__ void convert_tile(const uint8_t *codes, uint8_t *tile
     fence_proxy_async_smem();
 }
 
+// The walk of a stretch from what the prologue left in `start`: tile | sequence,
+// the first unit of that sequence's tile, L | Q, q0.
+__device__ __forceinline__ Walk walk_from(const volatile int64_t *start, int64_t u0, int64_t u1,
+                                          int G) {
+    Walk w;
+    w.seq = static_cast<int>(start[0]);
+    w.tile = static_cast<int>(start[0] >> 32);
+    w.u = u0;
+    w.u1 = u1;
+    w.sg = make_geo(static_cast<int>(start[2] >> 32), static_cast<int>(start[2]),
+                    static_cast<int>(start[3]), G);
+    w.n = w.sg.steps + kItemUnits;
+    const int64_t in = u0 - start[1];  // units from the tile's first
+    if (in >> 31) {
+        w.kvh = static_cast<int>(in / w.n);
+        w.x = static_cast<int>(in - static_cast<int64_t>(w.kvh) * w.n);
+    } else {
+        w.kvh = static_cast<int>(in) / w.n;
+        w.x = static_cast<int>(in) - w.kvh * w.n;
+    }
+    return w;
+}
+
 template <int D, bool FP8>
 __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
     tree_tile_kernel(const __grid_constant__ TreeParams p) {
@@ -775,33 +804,7 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
         if (!busy_cta) {
         } else if (warp == 0) {
             // ========================= pieces and keys =========================
-            Walk w;
-            w.seq = static_cast<int>(start[0]);
-            w.tile = static_cast<int>(start[0] >> 32);
-            const int64_t first = start[1];  // the first unit of the sequence's tile
-            w.u = u0;
-            w.u1 = u1;
-            w.sg = make_geo(static_cast<int>(start[2] >> 32), static_cast<int>(start[2]),
-                            static_cast<int>(start[3]), G);
-            w.n = w.sg.steps + kItemUnits;
-            w.kvh = static_cast<int>((u0 - first) / w.n);
-            w.x = static_cast<int>(u0 - first - static_cast<int64_t>(w.kvh) * w.n);
-            // the border at u0, for the merge (every CTA writes one, whether or
-            // not its stretch holds a step)
-            if (lane == 0) {
-                Border border;
-                const int64_t a = u0 - w.x;  // the item's first unit
-                const bool cuts = cta > 0 && step_at(w.x, w.sg.steps) > 0 &&
-                                  step_at(stretch(units, cta - 1, busy) - a, w.sg.steps) == 0;
-                // pieces: the CTA before this one, and those up to the item's last unit
-                border.pieces =
-                    cuts ? static_cast<int>(((a + w.n) * busy - 1) / units) - (cta - 1) + 1 : 0;
-                border.rows = min(kRows, w.sg.Q * G - w.tile * kRows);
-                border.q0 = w.sg.q0 + w.tile * (kRows >> logG);
-                border.kvh = w.kvh;
-                p.borders[cta] = border;
-            }
-            __syncwarp();
+            Walk w = walk_from(start, u0, u1, G);
             int cur_ids;
             PieceHead cur = next_piece(p, w, cta, cur_ids);
             int gs = 0;  // steps staged
@@ -945,11 +948,18 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                 // the query tile, once the previous piece's last scores are done
                 if (it >= 1) ok = wait_all(br.q_empty(), (it - 1) & 1);
                 if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(br.q_full(), Gm::kQ);
+                if (lane == 0)
+                    mbar_arrive_expect_tx(br.q_full(), spread_rows(pc.Q * G) ? Gm::kQ / 2 : Gm::kQ);
                 __syncwarp();
-                if (lane < CH)
+                if (spread_rows(pc.Q * G)) {  // sixteen rows to each 32 of the tile
+                    const int c = lane >> 2, k = lane & 3;
+                    if (lane < 4 * CH)
+                        tensor_g2s_3d(sb + c * (kRows * 128) + k * (32 * 128), &p.tm_q16, 128 * c,
+                                      pc.kvh * G, pc.q0 + k * (16 >> logG), br.q_full());
+                } else if (lane < CH) {
                     tensor_g2s_3d(sb + lane * (kRows * 128), &p.tm_q, 128 * lane, pc.kvh * G,
                                   pc.q0 + pc.tile * (kRows >> logG), br.q_full());
+                }
                 q_staged = it + 1;
                 ok = wait_all(br.q_full(), it & 1);
 #pragma unroll 1
@@ -991,6 +1001,23 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
         } else {
             // ============================= P V MMAs =============================
             constexpr uint32_t kIdescPV = tc::idesc_f16_f32(kRows, D, false, true);
+            // the border at u0, for the merge (every CTA writes one, whether or
+            // not its stretch holds a step)
+            if (lane == 0) {
+                const Walk w = walk_from(start, u0, u1, G);
+                Border border;
+                const int64_t a = u0 - w.x;  // the item's first unit
+                const bool cuts = cta > 0 && step_at(w.x, w.sg.steps) > 0 &&
+                                  step_at(stretch(units, cta - 1, busy) - a, w.sg.steps) == 0;
+                // pieces: the CTA before this one, and those up to the item's last unit
+                border.pieces =
+                    cuts ? static_cast<int>(((a + w.n) * busy - 1) / units) - (cta - 1) + 1 : 0;
+                border.rows = min(kRows, w.sg.Q * G - w.tile * kRows);
+                border.q0 = w.sg.q0 + w.tile * (kRows >> logG);
+                border.kvh = w.kvh;
+                p.borders[cta] = border;
+            }
+            __syncwarp();
             int gs = 0;
             bool ok = true;
 #pragma unroll 1
@@ -1137,7 +1164,6 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
         const int wh = (warp - kSoftmaxWarp) >> 2;
         const int quarter = warp & 3;
         const int h = lane >> 4;
-        const int r = quarter * 32 + wh * 16 + (lane & 15);
         const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32 + wh * 16) << 16);
         const float sl2 = p.scale_log2;
         int gs = 0;
@@ -1154,6 +1180,11 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
             if (lane == 0) mbar_arrive(br.piece_empty(rec));
             if (pc.done) break;
             const int ctx = pc.L - pc.Q;
+            // the tile's row of this warp's first lane (past the tile: none)
+            const int r0 = !spread_rows(pc.Q * G) ? quarter * 32 + wh * 16
+                           : wh == 0              ? quarter * 16
+                                                  : kRows;
+            const int r = r0 + (lane & 15);
             const int rr = pc.tile * kRows + r;
             const bool row_ok = rr < pc.Q * G;
             const bool live = __any_sync(0xffffffffu, row_ok);
@@ -1367,7 +1398,7 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             const int src = (lane & ~3) + c;  // the lane the row came from
-                            const int row = pc.tile * kRows + quarter * 32 + wh * 16 + (src & 15);
+                            const int row = pc.tile * kRows + r0 + (src & 15);
                             if (row < pc.Q * G)
                                 *reinterpret_cast<uint4 *>(
                                     p.out +
@@ -1536,6 +1567,18 @@ int make_code_map(CUtensorMap *map, const void *cache, int64_t num_blocks, int r
                   D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
+// Query rows [Tq][heads][D] by 128 bytes of 16 rows: `group` heads of 16/group
+// tokens.
+int make_query_map(CUtensorMap *map, const void *q, int64_t tokens, int heads, int D, int group) {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(heads),
+                                static_cast<cuuint64_t>(tokens)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2,
+                                   static_cast<cuuint64_t>(heads) * D * 2};
+    const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(group),
+                               static_cast<cuuint32_t>(16 / group)};
+    return encode(map, q, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 // The tile kernel and its merge, on `stream`.
 template <int D, bool FP8>
 int launch(TreeParams &p, void *workspace, cudaStream_t stream) {
@@ -1550,6 +1593,8 @@ int launch(TreeParams &p, void *workspace, cudaStream_t stream) {
     if (st == PKV_OK)
         st = dec::make_q_tensor_map(&p.tm_q, p.q, p.num_query_tokens, p.num_heads, D,
                                     p.num_heads / Hk);
+    if (st == PKV_OK)
+        st = make_query_map(&p.tm_q16, p.q, p.num_query_tokens, p.num_heads, D, p.num_heads / Hk);
     if (st != PKV_OK) return st;
     const int ctas = sm_count();
     const Scratch z = scratch(ctas, D);
