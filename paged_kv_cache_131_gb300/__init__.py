@@ -353,83 +353,100 @@ def pkv_decode_attention_fp8(out, q, k_cache, v_cache, k_scale, v_scale, block_t
     return _check(st, "pkv_decode_attention_fp8") if check else st
 
 
-def _shape(t, name, want):
-    """Refuse a tensor whose shape is not ``want``."""
+# The speculative step's calls are short kernels in a latency-bound loop: their
+# tensors are checked with one pass of cheap attribute reads each, and the
+# stream is taken as a raw handle (a torch.cuda.Stream object costs 3 us).
+
+
+def _current(t, name):
+    """The current device's index, which ``t`` must be on."""
+    import torch
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    return dev
+
+
+def _arg(t, name, dtype, shape, dev):
+    """Device pointer of a contiguous tensor of this dtype and shape on device ``dev``."""
     if t is None:
         raise ValueError(f"{name} is missing")
-    if tuple(t.shape) != tuple(want):
-        raise ValueError(f"{name} must have shape {tuple(want)}, got {tuple(t.shape)}")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be a CUDA tensor of device {dev}, is on {t.device}")
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _on_current_device(**tensors):
-    """Refuse tensors that are not on the current CUDA device: the launch goes to
-    a stream of that device."""
-    import torch
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name} is on {t.device}, not on the current device")
+def _raw_stream(stream, dev):
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return getattr(stream, "cuda_stream", stream)
 
 
-def _token_rows(t, name):
-    """(device pointer, token stride in elements) of fp16 rows [T, heads, D] whose
-    heads are packed; tokens may be strided (a slice of a packed QKV row)."""
-    import torch
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.float16 or t.dim() != 3:
-        raise ValueError(f"{name} must be float16 [tokens, heads, head_dim]")
-    T, h, D = t.shape
-    if (D > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != D):
+def _token_rows(t, name, dtype, shape, dev):
+    """(device pointer, token stride in elements) of rows [T, heads, D] whose heads
+    are packed; tokens may be strided (a slice of a packed QKV row)."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _arg(t, name, dtype, shape, dev)
+    T, h, D = shape
+    st, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (h > 1 and sh != D):
         raise ValueError(f"{name}: a token's heads must be packed")
-    return t.data_ptr(), t.stride(0) if T > 1 else h * D
+    return t.data_ptr(), st if T > 1 else h * D
+
+
+def _workspace(workspace, dev):
+    """(device pointer, bytes) of a workspace tensor, or of none."""
+    if workspace is None:
+        return None, 0
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor of the call's device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _norm_rope_write(name, q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, scales,
                      cos_sin, q_weight, k_weight, eps, interleaved, block_size, num_blocks,
                      stream, check):
     import torch
+    f16, i64, f32 = torch.float16, torch.int64, torch.float32
+    dev = _current(q, "q")
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q must be [T, H, D], k [T, Hk, D]")
     T, H, D = q.shape
     Hk = k.shape[1]
-    kind = torch.float16 if scales is None else torch.uint8
-    _on_current_device(q_out=q_out, q=q, k=k, v=v, positions=positions, slot_mapping=slot_mapping,
-                       k_cache=k_cache, v_cache=v_cache, cos_sin=cos_sin, q_weight=q_weight,
-                       k_weight=k_weight)
-    _shape(q_out, "q_out", (T, H, D))
-    _shape(k, "k", (T, Hk, D))
-    _shape(v, "v", (T, Hk, D))
-    _shape(slot_mapping, "slot_mapping", (T,))
-    _shape(k_cache, "k_cache", (num_blocks, block_size, Hk, D))
-    _shape(v_cache, "v_cache", (num_blocks, block_size, Hk, D))
-    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _shape(w, n, (D,))
-    if cos_sin is None:
-        max_pos, rot = 0, 0
-    else:
+    qp, qs = _token_rows(q, "q", f16, (T, H, D), dev)
+    kp, ks = _token_rows(k, "k", f16, (T, Hk, D), dev)
+    vp, vs = _token_rows(v, "v", f16, (T, Hk, D), dev)
+    rot = max_pos = 0
+    table = pos = None
+    if cos_sin is not None:
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin must be [max_position, rot_dim]")
         max_pos, rot = cos_sin.shape
-        _shape(positions, "positions", (T,))
-    nr = pkv_norm_rope(_dev(q_weight, "q_weight", torch.float16),
-                       _dev(k_weight, "k_weight", torch.float16), eps,
-                       _dev(cos_sin, "cos_sin", torch.float32), max_pos, rot, int(interleaved))
-    qp, qs = _token_rows(q, "q")
-    kp, ks = _token_rows(k, "k")
-    vp, vs = _token_rows(v, "v")
-    args = [_dev(q_out, "q_out", torch.float16), qp, kp, vp, qs, ks, vs, ctypes.byref(nr),
-            _dev(positions, "positions", torch.int64) if rot else None,
-            _dev(slot_mapping, "slot_mapping", torch.int64), T, _dev(k_cache, "k_cache", kind),
-            _dev(v_cache, "v_cache", kind)]
+        table = _arg(cos_sin, "cos_sin", f32, (max_pos, rot), dev)
+        if rot:
+            pos = _arg(positions, "positions", i64, (T,), dev)
+    nr = pkv_norm_rope(
+        None if q_weight is None else _arg(q_weight, "q_weight", f16, (D,), dev),
+        None if k_weight is None else _arg(k_weight, "k_weight", f16, (D,), dev),
+        eps, table, max_pos, rot, bool(interleaved))
+    kind = f16 if scales is None else torch.uint8
+    rows = (num_blocks, block_size, Hk, D)
+    args = [_arg(q_out, "q_out", f16, (T, H, D), dev), qp, kp, vp, qs, ks, vs, ctypes.byref(nr),
+            pos, _arg(slot_mapping, "slot_mapping", i64, (T,), dev), T,
+            _arg(k_cache, "k_cache", kind, rows, dev), _arg(v_cache, "v_cache", kind, rows, dev)]
     if scales is not None:
-        _on_current_device(k_scale=scales[0], v_scale=scales[1])
-        for s, n in zip(scales, ("k_scale", "v_scale")):
-            _shape(s, n, (num_blocks, block_size, Hk))
-            args.append(_dev(s, n, torch.float32))
-    st = getattr(load(), name)(*args, H, Hk, D, block_size, num_blocks, _stream(stream))
+        args += [_arg(scales[0], "k_scale", f32, rows[:3], dev),
+                 _arg(scales[1], "v_scale", f32, rows[:3], dev)]
+    st = getattr(load(), name)(*args, H, Hk, D, block_size, num_blocks, _raw_stream(stream, dev))
     return _check(st, name) if check else st
 
 
@@ -466,22 +483,20 @@ def pkv_cache_read_fp8(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, b
     """Rows of E4M3 caches read back into fp16 k, v [T, Hk, D]: see pkv_cache_read_fp8
     in pagedkv.h (v, v_cache, v_scale may all be None)."""
     import torch
+    f16, f32, u8 = torch.float16, torch.float32, torch.uint8
+    dev = _current(k, "k")
     T, Hk, D = k.shape
-    _on_current_device(k=k, v=v, slot_mapping=slot_mapping, k_cache=k_cache, v_cache=v_cache,
-                       k_scale=k_scale, v_scale=v_scale)
-    _shape(slot_mapping, "slot_mapping", (T,))
-    for x, c, s, n in ((k, k_cache, k_scale, "k"), (v, v_cache, v_scale, "v")):
-        if x is None and c is None and s is None and n == "v":
-            continue
-        _shape(x, n, (T, Hk, D))
-        _shape(c, n + "_cache", (num_blocks, block_size, Hk, D))
-        _shape(s, n + "_scale", (num_blocks, block_size, Hk))
+    rows = (num_blocks, block_size, Hk, D)
+    ptrs = [_arg(k, "k", f16, (T, Hk, D), dev), _arg(k_cache, "k_cache", u8, rows, dev),
+            _arg(k_scale, "k_scale", f32, rows[:3], dev)]
+    if v is None and v_cache is None and v_scale is None:
+        ptrs += [None, None, None]
+    else:
+        ptrs += [_arg(v, "v", f16, (T, Hk, D), dev), _arg(v_cache, "v_cache", u8, rows, dev),
+                 _arg(v_scale, "v_scale", f32, rows[:3], dev)]
     st = load().pkv_cache_read_fp8(
-        _dev(k, "k", torch.float16), _dev(v, "v", torch.float16),
-        _dev(slot_mapping, "slot_mapping", torch.int64), T,
-        _dev(k_cache, "k_cache", torch.uint8), _dev(v_cache, "v_cache", torch.uint8),
-        _dev(k_scale, "k_scale", torch.float32), _dev(v_scale, "v_scale", torch.float32),
-        Hk, D, block_size, num_blocks, _stream(stream))
+        ptrs[0], ptrs[3], _arg(slot_mapping, "slot_mapping", torch.int64, (T,), dev), T, ptrs[1],
+        ptrs[4], ptrs[2], ptrs[5], Hk, D, block_size, num_blocks, _raw_stream(stream, dev))
     return _check(st, "pkv_cache_read_fp8") if check else st
 
 
@@ -489,36 +504,27 @@ def _tree_attention(name, out, q, k_cache, v_cache, scales, block_tables, seq_le
                     tree_mask, scale, num_heads, num_kv_heads, head_dim, block_size,
                     max_query_len, max_seq_len, num_blocks, workspace, stream, check):
     import torch
-    _on_current_device(out=out, q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-                       seq_lens=seq_lens, query_start=query_start, tree_mask=tree_mask,
-                       workspace=workspace)
-    if q.dim() != 3 or block_tables.dim() != 2 or tree_mask.dim() != 2:
-        raise ValueError("q must be [Tq, H, D], block_tables [S, MB], tree_mask [Tq, words]")
+    f16, f32, i32 = torch.float16, torch.float32, torch.int32
+    dev = _current(q, "q")
+    if block_tables.dim() != 2 or tree_mask.dim() != 2:
+        raise ValueError("block_tables must be [S, MB], tree_mask [Tq, words]")
     Tq, S = q.shape[0], seq_lens.numel()
-    _shape(q, "q", (Tq, num_heads, head_dim))
-    _shape(out, "out", (Tq, num_heads, head_dim))
-    _shape(query_start, "query_start", (S + 1,))
-    _shape(block_tables, "block_tables", (S, block_tables.shape[1]))
-    _shape(tree_mask, "tree_mask", (Tq, tree_mask.shape[1]))
-    kind = torch.float16 if scales is None else torch.uint8
-    args = [_dev(out, "out", torch.float16), _dev(q, "q", torch.float16)]
-    for c, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _shape(c, n, (num_blocks, block_size, num_kv_heads, head_dim))
-        args.append(_dev(c, n, kind))
+    MB, words = block_tables.shape[1], tree_mask.shape[1]
+    qshape = (Tq, num_heads, head_dim)
+    rows = (num_blocks, block_size, num_kv_heads, head_dim)
+    kind = f16 if scales is None else torch.uint8
+    args = [_arg(out, "out", f16, qshape, dev), _arg(q, "q", f16, qshape, dev),
+            _arg(k_cache, "k_cache", kind, rows, dev), _arg(v_cache, "v_cache", kind, rows, dev)]
     if scales is not None:
-        _on_current_device(k_scale=scales[0], v_scale=scales[1])
-        for s, n in zip(scales, ("k_scale", "v_scale")):
-            _shape(s, n, (num_blocks, block_size, num_kv_heads))
-            args.append(_dev(s, n, torch.float32))
-    ws_ptr, ws_bytes = None, 0
-    if workspace is not None:
-        ws_ptr, ws_bytes = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+        args += [_arg(scales[0], "k_scale", f32, rows[:3], dev),
+                 _arg(scales[1], "v_scale", f32, rows[:3], dev)]
     st = getattr(load(), name)(
-        *args, _dev(block_tables, "block_tables", torch.int32),
-        _dev(seq_lens, "seq_lens", torch.int32), _dev(query_start, "query_start", torch.int32),
-        _dev(tree_mask, "tree_mask", torch.int64), tree_mask.shape[1], float(scale), num_heads,
-        num_kv_heads, head_dim, block_size, S, block_tables.shape[1], Tq, int(max_query_len),
-        int(max_seq_len), int(num_blocks), ws_ptr, ws_bytes, _stream(stream))
+        *args, _arg(block_tables, "block_tables", i32, (S, MB), dev),
+        _arg(seq_lens, "seq_lens", i32, (S,), dev),
+        _arg(query_start, "query_start", i32, (S + 1,), dev),
+        _arg(tree_mask, "tree_mask", torch.int64, (Tq, words), dev), words, scale, num_heads,
+        num_kv_heads, head_dim, block_size, S, MB, Tq, max_query_len, max_seq_len, num_blocks,
+        *_workspace(workspace, dev), _raw_stream(stream, dev))
     return _check(st, name) if check else st
 
 
@@ -569,20 +575,21 @@ def pkv_tree_accept(caches, num_layers: int, path, ctx_lens, block_tables, block
     int32 [S]; block_tables: CUDA int32 [S, MB].
     """
     import torch
-    _on_current_device(path=path, ctx_lens=ctx_lens, block_tables=block_tables)
+    i32 = torch.int32
+    dev = _current(path, "path")
     if path.dim() != 2 or block_tables.dim() != 2:
         raise ValueError("path must be [S, max_depth], block_tables [S, MB]")
-    S = path.shape[0]
-    _shape(ctx_lens, "ctx_lens", (S,))
-    _shape(block_tables, "block_tables", (S, block_tables.shape[1]))
+    S, depth = path.shape
+    MB = block_tables.shape[1]
     arr = (pkv_cache_desc * max(1, len(caches)))()
     for i, (cache, view) in enumerate(caches):
-        _on_current_device(**{f"caches[{i}]": cache})
-        arr[i] = pkv_cache_desc(_dev(cache, f"caches[{i}]"), _as_view(view))
+        arr[i].cache = _arg(cache, f"caches[{i}]", cache.dtype, cache.shape, dev)
+        arr[i].view = _as_view(view)
     st = load().pkv_tree_accept(
-        arr, len(caches), num_layers, _dev(path, "path", torch.int32), path.shape[1],
-        _dev(ctx_lens, "ctx_lens", torch.int32), _dev(block_tables, "block_tables", torch.int32),
-        S, block_tables.shape[1], block_size, num_blocks, _stream(stream))
+        arr, len(caches), num_layers, _arg(path, "path", i32, (S, depth), dev), depth,
+        _arg(ctx_lens, "ctx_lens", i32, (S,), dev),
+        _arg(block_tables, "block_tables", i32, (S, MB), dev), S, MB, block_size, num_blocks,
+        _raw_stream(stream, dev))
     return _check(st, "pkv_tree_accept") if check else st
 
 

@@ -9,13 +9,16 @@
 // rounding in between).
 //
 // A row of D fp16 is held by D/8 lanes, 8 dims (one 16-byte load) each, so the
-// sums over a row are shuffles inside 8 or 16 lanes and a pair's other half is
-// at most one shuffle away.  A warp's job is kRows rows for each of its row
-// groups, all of one token: every load of the job is issued before the first
-// is used, and the token's cosines and sines are read once for all its rows.
+// sum over a row is shuffles inside 8 or 16 lanes.  A warp's job is kRows rows
+// for each of its row groups, all of one token and one kind (query, key or
+// value).  Every load of the job is issued before the first is used, the other
+// halves of the pairs among them (a second load of the same line instead of
+// shuffles), and before it is known whether the token is padding.  Weights
+// and rotation are two factors per dim, A = w cos and B = -+ w' sin, shared by
+// the job's rows: y = rsqrt(..) (x A + x' B).
 //
-// Bound: HBM -- every row read and written once.  The table's rows come from
-// L2 or, for a token's later jobs, L1.
+// Bound: HBM -- every row read and written once; the table's rows come from L2
+// or, for a token's later jobs, L1.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -49,8 +52,10 @@ struct NormRopeParams {
     const int64_t *positions;
     const int64_t *slot_mapping;
     int64_t num_slots;
-    int64_t num_jobs;
-    int32_t jobs_per_token;
+    uint32_t num_jobs;
+    uint32_t jobs_per_token;
+    int32_t query_jobs;  // the first of a token's jobs; then the keys', the values'
+    int32_t row_jobs;    // of the keys, and of the values
     int32_t num_heads;
     int32_t num_kv_heads;
     ErrorRecord *err;
@@ -66,9 +71,43 @@ __device__ __forceinline__ void unpack8(const uint4 &r, float (&x)[8]) {
     }
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-    return make_uint4(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]), pack_half2(x[4], x[5]),
-                      pack_half2(x[6], x[7]));
+// Packed fp32 pairs: one instruction for two dims.
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 f32x2_split(uint64_t r) {
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
+    return v;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ void unpack_pairs(const uint4 &r, uint64_t (&x)[4]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack_half2(w[i]);
+        x[i] = f32x2(f.x, f.y);
+    }
+}
+__device__ __forceinline__ uint4 pack_pairs(const uint64_t (&x)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = f32x2_split(x[i]);
+        w[i] = pack_half2(f.x, f.y);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -80,133 +119,173 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kThreads)
     norm_rope_write_kernel(const __grid_constant__ NormRopeParams p) {
-    constexpr int LPR = D / 8;     // lanes per row
-    constexpr int RG = 32 / LPR;   // row groups of a warp
-    constexpr int kJobRows = RG * kRows;
+    constexpr int LPR = D / 8;    // lanes per row
+    constexpr int RG = 32 / LPR;  // row groups of a warp
+    const uint32_t job = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    if (job >= p.num_jobs) return;
     const int lane = threadIdx.x & 31;
-    const int sl = lane % LPR, rg = lane / LPR;
-    const int d0 = 8 * sl;
-    const int H = p.num_heads, Hk = p.num_kv_heads;
-    const int rows = H + 2 * Hk;
+    const int d0 = 8 * (lane % LPR), rg = lane / LPR;
+    const uint32_t token = job / p.jobs_per_token;
+    const int64_t t = token;
+    int j = static_cast<int>(job - token * p.jobs_per_token);
+    int kind = 0;  // query, key, value
+    if (j >= p.query_jobs) {
+        j -= p.query_jobs;
+        kind = 1;
+        if (j >= p.row_jobs) {
+            j -= p.row_jobs;
+            kind = 2;
+        }
+    }
+    const int heads = kind == 0 ? p.num_heads : p.num_kv_heads;
+    const int h0 = j * (RG * kRows) + rg;
+    const __half *src = (kind == 0 ? p.src[0] : kind == 1 ? p.src[1] : p.src[2]) +
+                        t * (kind == 0 ? p.stride[0] : kind == 1 ? p.stride[1] : p.stride[2]);
     const int half = p.rot >> 1;
-    const bool rotates = d0 < p.rot;
-    const bool second = !p.interleaved && d0 >= half;  // the b half of its pairs
-    const int partner = p.interleaved || !rotates ? lane : second ? lane - half / 8 : lane + half / 8;
+    const bool rotates = kind < 2 && d0 < p.rot;
+    const bool halves = rotates && !p.interleaved;
+    const bool second = d0 >= half;  // the b half of its pairs
+    const int dp = second ? d0 - half : d0 + half;  // the other halves' dims
     grid_dependency_wait();  // the rows may come from the kernel just before
-    const int64_t nwarps = (static_cast<int64_t>(gridDim.x) * kThreads) >> 5;
-    for (int64_t job = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
-         job < p.num_jobs; job += nwarps) {
-        const int64_t t = job / p.jobs_per_token;
-        const int row0 = static_cast<int>(job - t * p.jobs_per_token) * kJobRows + rg;
-        const int64_t slot = p.slot_mapping[t];
-        const int64_t pos = p.rot ? p.positions[t] : 0;
-        if (slot < 0) continue;  // padding
-        const bool bad_slot = slot >= p.num_slots;
-        if (bad_slot || (p.rot && (pos < 0 || pos >= p.max_position))) {
-            if (lane == 0)
-                record_error(p.err, bad_slot ? PKV_DEVERR_SLOT : PKV_DEVERR_POSITION, t);
+    const int64_t slot = p.slot_mapping[t];
+    const int64_t pos = p.rot ? p.positions[t] : 0;
+    uint4 raw[kRows], other[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const __half *row = src + (h0 + i * RG) * D;
+        raw[i] = other[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (h0 + i * RG < heads) {
+            raw[i] = *reinterpret_cast<const uint4 *>(row + d0);
+            if (halves) other[i] = *reinterpret_cast<const uint4 *>(row + dp);
+        }
+    }
+    if (slot < 0) return;  // padding
+    const bool bad_slot = slot >= p.num_slots;
+    if (bad_slot || (p.rot && (pos < 0 || pos >= p.max_position))) {
+        if (lane == 0) record_error(p.err, bad_slot ? PKV_DEVERR_SLOT : PKV_DEVERR_POSITION, t);
+        return;
+    }
+    uint64_t A[4], B[4];  // the factors of dims 2i, 2i + 1
+    const __half *weight = kind == 0 ? p.weight[0] : p.weight[1];
+    if (kind < 2) {
+        float w[8], wp[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = wp[e] = 1.f;
+        if (weight != nullptr) {
+            unpack8(__ldg(reinterpret_cast<const uint4 *>(weight + d0)), w);
+            if (halves) unpack8(__ldg(reinterpret_cast<const uint4 *>(weight + dp)), wp);
+        }
+        float a[8], b[8];
+        if (!rotates) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                a[e] = w[e];
+                b[e] = 0.f;
+            }
+        } else {
+            const float4 *cs = reinterpret_cast<const float4 *>(p.table + pos * p.rot);
+            if (p.interleaved) {  // pairs d0/2 .. d0/2 + 3
+                const float4 c = __ldg(cs + d0 / 8), s = __ldg(cs + half / 4 + d0 / 8);
+                const float cv[4] = {c.x, c.y, c.z, c.w}, sv[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    a[2 * e] = w[2 * e] * cv[e];
+                    b[2 * e] = -w[2 * e + 1] * sv[e];
+                    a[2 * e + 1] = w[2 * e + 1] * cv[e];
+                    b[2 * e + 1] = w[2 * e] * sv[e];
+                }
+            } else {  // pairs d0 .. d0 + 7, or those of the other half
+                const int i0 = (second ? dp : d0) / 4;
+                const float4 c0 = __ldg(cs + i0), c1 = __ldg(cs + i0 + 1);
+                const float4 s0 = __ldg(cs + half / 4 + i0), s1 = __ldg(cs + half / 4 + i0 + 1);
+                const float cv[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+                const float sv[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    a[e] = w[e] * cv[e];
+                    b[e] = (second ? wp[e] : -wp[e]) * sv[e];
+                }
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            A[e] = f32x2(a[2 * e], a[2 * e + 1]);
+            B[e] = f32x2(b[2 * e], b[2 * e + 1]);
+        }
+    }
+    __syncwarp();  // (the queries may be rewritten in place)
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int h = h0 + i * RG;
+        const bool live = h < heads;
+        if (!FP8 && kind == 2) {  // values move as they are
+            if (live)
+                *reinterpret_cast<uint4 *>(static_cast<__half *>(p.cache[1]) +
+                                           (slot * heads + h) * D + d0) = raw[i];
             continue;
         }
-        uint4 raw[kRows];
+        uint64_t x[4];
+        unpack_pairs(raw[i], x);
+        if (kind < 2) {
+            uint64_t r2 = f32x2(1.f, 1.f);
+            if (weight != nullptr) {
+                uint64_t q2 = mul_f32x2(x[0], x[0]);
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int row = row0 + i * RG;
-            const int kind = row < H ? 0 : row < H + Hk ? 1 : 2;
-            const int h = row - (kind == 0 ? 0 : kind == 1 ? H : H + Hk);
-            if (row < rows)
-                raw[i] = *reinterpret_cast<const uint4 *>(p.src[kind] + t * p.stride[kind] +
-                                                          h * D + d0);
-        }
-        // this lane's cosines and sines: pairs d0 .. d0+7 (halves) or
-        // d0/2 .. d0/2 + 3 (interleaved)
-        float c[8], s[8];
-        if (rotates) {
-            const float *row = p.table + pos * p.rot;
-            const int i0 = p.interleaved ? d0 / 2 : second ? d0 - half : d0;
-            *reinterpret_cast<float4 *>(c) = __ldg(reinterpret_cast<const float4 *>(row + i0));
-            *reinterpret_cast<float4 *>(s) =
-                __ldg(reinterpret_cast<const float4 *>(row + half + i0));
-            if (!p.interleaved) {
-                *reinterpret_cast<float4 *>(c + 4) =
-                    __ldg(reinterpret_cast<const float4 *>(row + i0 + 4));
-                *reinterpret_cast<float4 *>(s + 4) =
-                    __ldg(reinterpret_cast<const float4 *>(row + half + i0 + 4));
-            }
-        }
+                for (int e = 1; e < 4; ++e) q2 = fma_f32x2(x[e], x[e], q2);
+                const float2 q = f32x2_split(q2);
+                float ss = q.x + q.y;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int row = row0 + i * RG;
-            const bool live = row < rows;
-            const int kind = row < H ? 0 : row < H + Hk ? 1 : 2;
-            const int h = row - (kind == 0 ? 0 : kind == 1 ? H : H + Hk);
-            float x[8];
-            if (live) {
-                unpack8(raw[i], x);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = 0.f;
-            }
-            const __half *w = kind < 2 ? p.weight[kind] : nullptr;
-            // (the shuffles run in every lane; rows of other kinds drop the sum)
-            float ss = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-            for (int o = LPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (w != nullptr) {
+                for (int o = LPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
                 const float r = rsqrtf(ss * (1.f / D) + p.eps);
-                float wf[8];
-                unpack8(__ldg(reinterpret_cast<const uint4 *>(w + d0)), wf);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = x[e] * r * wf[e];
+                r2 = f32x2(r, r);
             }
+            uint64_t y[4];
             if (p.interleaved) {
-                if (rotates && kind < 2) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float a = x[2 * e], b = x[2 * e + 1];
-                        x[2 * e] = a * c[e] - b * s[e];
-                        x[2 * e + 1] = b * c[e] + a * s[e];
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const float2 v = f32x2_split(x[e]);
+                    y[e] = f32x2(v.y, v.x);
                 }
-            } else if (p.rot) {
-                const float sign = second ? 1.f : -1.f;
-                float y[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(0xffffffffu, x[e], partner);
-                if (rotates && kind < 2) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = x[e] * c[e] + sign * y[e] * s[e];
-                }
+            } else {
+                unpack_pairs(other[i], y);
             }
-            if constexpr (FP8) {
-                float amax = 0.f;
+            // (a dim that is not rotated meets no other)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
+            for (int e = 0; e < 4; ++e) {
+                const uint64_t z = mul_f32x2(x[e], A[e]);
+                x[e] = mul_f32x2(rotates ? fma_f32x2(y[e], B[e], z) : z, r2);
+            }
+        }
+        if constexpr (FP8) {
+            if (kind > 0) {
+                float v[8], amax = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = f32x2_split(x[e]);
+                    v[2 * e] = f.x;
+                    v[2 * e + 1] = f.y;
+                    amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+                }
 #pragma unroll
                 for (int o = LPR / 2; o >= 1; o >>= 1)
                     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                if (live && kind > 0) {
-                    const float sc = amax / 448.f;  // 448: E4M3's largest finite value
-                    float y[8];
+                if (!live) continue;
+                const float sc = amax / 448.f;  // 448: E4M3's largest finite value
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = sc == 0.f ? 0.f : x[e] / sc;
-                    const int64_t at = slot * Hk + h;
-                    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.cache[kind - 1]) + at * D +
-                                               d0) =
-                        make_uint2(e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16),
-                                   e4m3x2(y[4], y[5]) | (e4m3x2(y[6], y[7]) << 16));
-                    if (sl == 0) p.scale[kind - 1][at] = sc;
-                    continue;
-                }
+                for (int e = 0; e < 8; ++e) v[e] = sc == 0.f ? 0.f : v[e] / sc;
+                const int64_t at = slot * heads + h;
+                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.cache[kind - 1]) + at * D +
+                                           d0) =
+                    make_uint2(e4m3x2(v[0], v[1]) | (e4m3x2(v[2], v[3]) << 16),
+                               e4m3x2(v[4], v[5]) | (e4m3x2(v[6], v[7]) << 16));
+                if (d0 == 0) p.scale[kind - 1][at] = sc;
+                continue;
             }
-            if (!live) continue;
-            __half *dst = kind == 0 ? p.q_out + (t * H + h) * D
-                                    : static_cast<__half *>(p.cache[kind - 1]) +
-                                          (slot * Hk + h) * D;
-            // values move as they are (their bits, not a round trip through fp32)
-            *reinterpret_cast<uint4 *>(dst + d0) = kind == 2 ? raw[i] : pack8(x);
         }
+        if (!live) continue;
+        __half *dst = kind == 0 ? p.q_out + (t * heads + h) * D
+                                : static_cast<__half *>(p.cache[0]) + (slot * heads + h) * D;
+        *reinterpret_cast<uint4 *>(dst + d0) = pack_pairs(x);
     }
 }
 
@@ -263,9 +342,11 @@ int norm_rope_write(void *q_out, const void *q, const void *k, const void *v, in
     p.num_heads = num_heads;
     p.num_kv_heads = num_kv_heads;
     const int job_rows = 32 / (head_dim / 8) * kRows;
-    p.jobs_per_token = (num_heads + 2 * num_kv_heads + job_rows - 1) / job_rows;
-    if (num_tokens > INT64_MAX / p.jobs_per_token) return PKV_ERR_INVALID;
-    p.num_jobs = num_tokens * p.jobs_per_token;
+    p.query_jobs = (num_heads + job_rows - 1) / job_rows;
+    p.row_jobs = (num_kv_heads + job_rows - 1) / job_rows;
+    p.jobs_per_token = static_cast<uint32_t>(p.query_jobs + 2 * p.row_jobs);
+    if (num_tokens > INT32_MAX / static_cast<int64_t>(p.jobs_per_token)) return PKV_ERR_UNSUPPORTED;
+    p.num_jobs = static_cast<uint32_t>(num_tokens) * p.jobs_per_token;
     p.err = device_error_record();
     if (p.err == nullptr) return PKV_ERR_CUDA;
     using Fn = void (*)(const NormRopeParams);
@@ -273,12 +354,11 @@ int norm_rope_write(void *q_out, const void *q, const void *k, const void *v, in
                                          : norm_rope_write_kernel<128, false>)
                                   : (fp8 ? norm_rope_write_kernel<64, true>
                                          : norm_rope_write_kernel<64, false>);
-    const int64_t want = (p.num_jobs + kThreads / 32 - 1) / (kThreads / 32);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(want, 1 << 20)));
+    cfg.gridDim = dim3((p.num_jobs + kThreads / 32 - 1) / (kThreads / 32));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
     cfg.attrs = attr;

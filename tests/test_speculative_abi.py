@@ -127,4 +127,5 @@ def test_the_binding_refuses_what_does_not_fit(lib):
     with pytest.raises(ValueError):
         pkv.pkv_tree_accept([], 1, i64.view(2, 2).int(), i64.int(), i64.view(2, 2).int(), 16, 1)
     with pytest.raises(ValueError):  # heads of a token apart
-        pkv._token_rows(torch.zeros(4, 2, 128, dtype=torch.float16)[..., ::2], "q")
+        pkv._token_rows(torch.zeros(4, 2, 128, dtype=torch.float16)[..., ::2], "q", torch.float16,
+                        (4, 2, 64), -1)
