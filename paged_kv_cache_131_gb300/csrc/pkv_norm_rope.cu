@@ -9,16 +9,20 @@
 // rounding in between).
 //
 // A row of D fp16 is held by D/8 lanes, 8 dims (one 16-byte load) each, so the
-// sum over a row is shuffles inside 8 or 16 lanes.  A warp's job is kRows rows
-// for each of its row groups, all of one token and one kind (query, key or
-// value).  Every load of the job is issued before the first is used, the other
-// halves of the pairs among them (a second load of the same line instead of
-// shuffles), and before it is known whether the token is padding.  Weights
-// and rotation are two factors per dim, A = w cos and B = -+ w' sin, shared by
-// the job's rows: y = rsqrt(..) (x A + x' B).
+// sum over a row, and the other halves of its pairs, are shuffles inside 8 or
+// 16 lanes.  A token's rows are cut into chunks of kRows rows per row group,
+// all of one kind (query, key or value); a warp's job is a run of chunks of
+// one token, the next chunk's rows loaded while this one's are worked on (the
+// first ones before it is known whether the token is padding).  Weights and
+// rotation are two factors per dim, A = w cos and B = -+ w' sin, made once per
+// job and kind: y = rsqrt(..) (x A + x' B).  Large calls get long jobs (fewer
+// factors made), small ones a chunk per warp.
 //
-// Bound: HBM -- every row read and written once; the table's rows come from L2
-// or, for a token's later jobs, L1.
+// Bound: HBM -- every row read and written once; the table's rows come from L2.
+// 32 query and 8 KV heads of 128 dims: 16384 tokens 75.5 us into fp16 caches
+// (5.45 TB/s), 85 us into FP8 ones (4.3 TB/s: the scales' divisions).  Chunks of
+// 4 rows: 77 and 90 us; 4 resident blocks instead of 3: 86 and 100 (spills); a
+// chunk per warp: 139 and 154 (the factors are then made per chunk).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -35,7 +39,9 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 4;  // rows per row group and job
+constexpr int kRows = 2;       // rows per row group and chunk
+constexpr int kMinBlocks = 3;  // resident blocks per SM
+constexpr int kJobStart = 4;   // a job's start-up, in chunks
 
 struct NormRopeParams {
     const __half *src[3];  // q, k, v
@@ -54,8 +60,10 @@ struct NormRopeParams {
     int64_t num_slots;
     uint32_t num_jobs;
     uint32_t jobs_per_token;
-    int32_t query_jobs;  // the first of a token's jobs; then the keys', the values'
-    int32_t row_jobs;    // of the keys, and of the values
+    int32_t job_chunks;    // chunks of a job
+    int32_t token_chunks;  // of a token: the queries', the keys', the values'
+    int32_t query_chunks;
+    int32_t row_chunks;    // of the keys, and of the values
     int32_t num_heads;
     int32_t num_kv_heads;
     ErrorRecord *err;
@@ -115,9 +123,76 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
         __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3));
 }
 
+// The factors of a lane's dims d0 .. d0 + 7 (their other halves': dp on) at
+// position pos, with this weight (or none).
+__device__ __forceinline__ void make_factors(const NormRopeParams &p, const __half *weight,
+                                             int64_t pos, int d0, int dp, bool rotates,
+                                             bool second, uint64_t (&A)[4], uint64_t (&B)[4]) {
+    const int half = p.rot >> 1;
+    float w[8], wp[8], a[8], b[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = wp[e] = 1.f;
+    if (weight != nullptr) {
+        unpack8(__ldg(reinterpret_cast<const uint4 *>(weight + d0)), w);
+        if (rotates && !p.interleaved)
+            unpack8(__ldg(reinterpret_cast<const uint4 *>(weight + dp)), wp);
+    }
+    if (!rotates) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            a[e] = w[e];
+            b[e] = 0.f;
+        }
+    } else {
+        const float4 *cs = reinterpret_cast<const float4 *>(p.table + pos * p.rot);
+        if (p.interleaved) {  // pairs d0/2 .. d0/2 + 3
+            const float4 c = __ldg(cs + d0 / 8), s = __ldg(cs + half / 4 + d0 / 8);
+            const float cv[4] = {c.x, c.y, c.z, c.w}, sv[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                a[2 * e] = w[2 * e] * cv[e];
+                b[2 * e] = -w[2 * e + 1] * sv[e];
+                a[2 * e + 1] = w[2 * e + 1] * cv[e];
+                b[2 * e + 1] = w[2 * e] * sv[e];
+            }
+        } else {  // pairs d0 .. d0 + 7, or those of the other half
+            const int i0 = (second ? dp : d0) / 4;
+            const float4 c0 = __ldg(cs + i0), c1 = __ldg(cs + i0 + 1);
+            const float4 s0 = __ldg(cs + half / 4 + i0), s1 = __ldg(cs + half / 4 + i0 + 1);
+            const float cv[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+            const float sv[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                a[e] = w[e] * cv[e];
+                b[e] = (second ? wp[e] : -wp[e]) * sv[e];
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        A[e] = f32x2(a[2 * e], a[2 * e + 1]);
+        B[e] = f32x2(b[2 * e], b[2 * e + 1]);
+    }
+}
+
+// A token's chunk: kind, first row of the warp's first row group.
+struct Chunk {
+    int kind;  // query, key, value; or none
+    int h0;
+};
+
+template <int D>
+__device__ __forceinline__ Chunk chunk_of(const NormRopeParams &p, int c) {
+    constexpr int kChunk = 256 / D * kRows;
+    if (c < p.query_chunks) return Chunk{0, c * kChunk};
+    c -= p.query_chunks;
+    if (c < p.row_chunks) return Chunk{1, c * kChunk};
+    return Chunk{2, (c - p.row_chunks) * kChunk};
+}
+
 // D: head_dim; FP8: quantised caches.
 template <int D, bool FP8>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kMinBlocks)
     norm_rope_write_kernel(const __grid_constant__ NormRopeParams p) {
     constexpr int LPR = D / 8;    // lanes per row
     constexpr int RG = 32 / LPR;  // row groups of a warp
@@ -127,38 +202,32 @@ __global__ void __launch_bounds__(kThreads)
     const int d0 = 8 * (lane % LPR), rg = lane / LPR;
     const uint32_t token = job / p.jobs_per_token;
     const int64_t t = token;
-    int j = static_cast<int>(job - token * p.jobs_per_token);
-    int kind = 0;  // query, key, value
-    if (j >= p.query_jobs) {
-        j -= p.query_jobs;
-        kind = 1;
-        if (j >= p.row_jobs) {
-            j -= p.row_jobs;
-            kind = 2;
-        }
-    }
-    const int heads = kind == 0 ? p.num_heads : p.num_kv_heads;
-    const int h0 = j * (RG * kRows) + rg;
-    const __half *src = (kind == 0 ? p.src[0] : kind == 1 ? p.src[1] : p.src[2]) +
-                        t * (kind == 0 ? p.stride[0] : kind == 1 ? p.stride[1] : p.stride[2]);
+    int c = static_cast<int>(job - token * p.jobs_per_token) * p.job_chunks;
+    const int c1 = min(c + p.job_chunks, p.token_chunks);
     const int half = p.rot >> 1;
-    const bool rotates = kind < 2 && d0 < p.rot;
-    const bool halves = rotates && !p.interleaved;
+    const bool rotates = d0 < p.rot;
     const bool second = d0 >= half;  // the b half of its pairs
     const int dp = second ? d0 - half : d0 + half;  // the other halves' dims
+    const int partner = rotates && !p.interleaved ? lane + (dp - d0) / 8 : lane;
+    auto load = [&](const Chunk &ch, uint4 (&r)[kRows]) {
+        const int heads = ch.kind == 0 ? p.num_heads : p.num_kv_heads;
+        const __half *src =
+            (ch.kind == 0 ? p.src[0] : ch.kind == 1 ? p.src[1] : p.src[2]) +
+            t * (ch.kind == 0 ? p.stride[0] : ch.kind == 1 ? p.stride[1] : p.stride[2]) +
+            (ch.h0 + rg) * D + d0;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            r[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (ch.h0 + rg + i * RG < heads)
+                r[i] = *reinterpret_cast<const uint4 *>(src + i * RG * D);
+        }
+    };
     grid_dependency_wait();  // the rows may come from the kernel just before
     const int64_t slot = p.slot_mapping[t];
     const int64_t pos = p.rot ? p.positions[t] : 0;
-    uint4 raw[kRows], other[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const __half *row = src + (h0 + i * RG) * D;
-        raw[i] = other[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (h0 + i * RG < heads) {
-            raw[i] = *reinterpret_cast<const uint4 *>(row + d0);
-            if (halves) other[i] = *reinterpret_cast<const uint4 *>(row + dp);
-        }
-    }
+    Chunk ch = chunk_of<D>(p, c);
+    uint4 next[kRows];
+    load(ch, next);
     if (slot < 0) return;  // padding
     const bool bad_slot = slot >= p.num_slots;
     if (bad_slot || (p.rot && (pos < 0 || pos >= p.max_position))) {
@@ -166,126 +235,120 @@ __global__ void __launch_bounds__(kThreads)
         return;
     }
     uint64_t A[4], B[4];  // the factors of dims 2i, 2i + 1
-    const __half *weight = kind == 0 ? p.weight[0] : p.weight[1];
-    if (kind < 2) {
-        float w[8], wp[8];
+    int made = -1;        // the kind they are for
+    const __half *weight = nullptr;
+    while (true) {
+        uint4 raw[kRows];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = wp[e] = 1.f;
-        if (weight != nullptr) {
-            unpack8(__ldg(reinterpret_cast<const uint4 *>(weight + d0)), w);
-            if (halves) unpack8(__ldg(reinterpret_cast<const uint4 *>(weight + dp)), wp);
+        for (int i = 0; i < kRows; ++i) raw[i] = next[i];
+        const int kind = ch.kind, h0 = ch.h0 + rg;
+        const int heads = kind == 0 ? p.num_heads : p.num_kv_heads;
+        const bool more = ++c < c1;
+        if (more) {
+            ch = chunk_of<D>(p, c);
+            load(ch, next);
         }
-        float a[8], b[8];
-        if (!rotates) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                a[e] = w[e];
-                b[e] = 0.f;
-            }
-        } else {
-            const float4 *cs = reinterpret_cast<const float4 *>(p.table + pos * p.rot);
-            if (p.interleaved) {  // pairs d0/2 .. d0/2 + 3
-                const float4 c = __ldg(cs + d0 / 8), s = __ldg(cs + half / 4 + d0 / 8);
-                const float cv[4] = {c.x, c.y, c.z, c.w}, sv[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    a[2 * e] = w[2 * e] * cv[e];
-                    b[2 * e] = -w[2 * e + 1] * sv[e];
-                    a[2 * e + 1] = w[2 * e + 1] * cv[e];
-                    b[2 * e + 1] = w[2 * e] * sv[e];
-                }
-            } else {  // pairs d0 .. d0 + 7, or those of the other half
-                const int i0 = (second ? dp : d0) / 4;
-                const float4 c0 = __ldg(cs + i0), c1 = __ldg(cs + i0 + 1);
-                const float4 s0 = __ldg(cs + half / 4 + i0), s1 = __ldg(cs + half / 4 + i0 + 1);
-                const float cv[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-                const float sv[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    a[e] = w[e] * cv[e];
-                    b[e] = (second ? wp[e] : -wp[e]) * sv[e];
-                }
-            }
+        if (kind < 2 && kind != made) {
+            made = kind;
+            weight = kind == 0 ? p.weight[0] : p.weight[1];
+            make_factors(p, weight, pos, d0, dp, rotates, second, A, B);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            A[e] = f32x2(a[2 * e], a[2 * e + 1]);
-            B[e] = f32x2(b[2 * e], b[2 * e + 1]);
-        }
-    }
-    __syncwarp();  // (the queries may be rewritten in place)
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int h = h0 + i * RG;
-        const bool live = h < heads;
-        if (!FP8 && kind == 2) {  // values move as they are
-            if (live)
-                *reinterpret_cast<uint4 *>(static_cast<__half *>(p.cache[1]) +
-                                           (slot * heads + h) * D + d0) = raw[i];
-            continue;
-        }
-        uint64_t x[4];
-        unpack_pairs(raw[i], x);
-        if (kind < 2) {
-            uint64_t r2 = f32x2(1.f, 1.f);
-            if (weight != nullptr) {
-                uint64_t q2 = mul_f32x2(x[0], x[0]);
-#pragma unroll
-                for (int e = 1; e < 4; ++e) q2 = fma_f32x2(x[e], x[e], q2);
-                const float2 q = f32x2_split(q2);
-                float ss = q.x + q.y;
-#pragma unroll
-                for (int o = LPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                const float r = rsqrtf(ss * (1.f / D) + p.eps);
-                r2 = f32x2(r, r);
-            }
-            uint64_t y[4];
-            if (p.interleaved) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 v = f32x2_split(x[e]);
-                    y[e] = f32x2(v.y, v.x);
-                }
-            } else {
-                unpack_pairs(other[i], y);
-            }
-            // (a dim that is not rotated meets no other)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint64_t z = mul_f32x2(x[e], A[e]);
-                x[e] = mul_f32x2(rotates ? fma_f32x2(y[e], B[e], z) : z, r2);
-            }
-        }
-        if constexpr (FP8) {
-            if (kind > 0) {
-                float v[8], amax = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 f = f32x2_split(x[e]);
-                    v[2 * e] = f.x;
-                    v[2 * e + 1] = f.y;
-                    amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-                }
-#pragma unroll
-                for (int o = LPR / 2; o >= 1; o >>= 1)
-                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                if (!live) continue;
-                const float sc = amax / 448.f;  // 448: E4M3's largest finite value
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = sc == 0.f ? 0.f : v[e] / sc;
-                const int64_t at = slot * heads + h;
-                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.cache[kind - 1]) + at * D +
-                                           d0) =
-                    make_uint2(e4m3x2(v[0], v[1]) | (e4m3x2(v[2], v[3]) << 16),
-                               e4m3x2(v[4], v[5]) | (e4m3x2(v[6], v[7]) << 16));
-                if (d0 == 0) p.scale[kind - 1][at] = sc;
+        for (int i = 0; i < kRows; ++i) {
+            const int h = h0 + i * RG;
+            const bool live = h < heads;
+            if (!FP8 && kind == 2) {  // values move as they are
+                if (live)
+                    *reinterpret_cast<uint4 *>(static_cast<__half *>(p.cache[1]) +
+                                               (slot * heads + h) * D + d0) = raw[i];
                 continue;
             }
+            uint64_t x[4];
+            unpack_pairs(raw[i], x);
+            if (kind < 2) {
+                uint64_t r2 = f32x2(1.f, 1.f);
+                if (weight != nullptr) {
+                    uint64_t q2 = mul_f32x2(x[0], x[0]);
+#pragma unroll
+                    for (int e = 1; e < 4; ++e) q2 = fma_f32x2(x[e], x[e], q2);
+                    const float2 q = f32x2_split(q2);
+                    float ss = q.x + q.y;
+#pragma unroll
+                    for (int o = LPR / 2; o >= 1; o >>= 1)
+                        ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                    const float r = rsqrtf(ss * (1.f / D) + p.eps);
+                    r2 = f32x2(r, r);
+                }
+                uint64_t y[4];
+                if (p.interleaved) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 v = f32x2_split(x[e]);
+                        y[e] = f32x2(v.y, v.x);
+                    }
+                } else {
+                    uint4 o;
+                    o.x = __shfl_sync(0xffffffffu, raw[i].x, partner);
+                    o.y = __shfl_sync(0xffffffffu, raw[i].y, partner);
+                    o.z = __shfl_sync(0xffffffffu, raw[i].z, partner);
+                    o.w = __shfl_sync(0xffffffffu, raw[i].w, partner);
+                    unpack_pairs(o, y);
+                }
+                // (a dim that is not rotated meets no other)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint64_t z = mul_f32x2(x[e], A[e]);
+                    x[e] = mul_f32x2(rotates ? fma_f32x2(y[e], B[e], z) : z, r2);
+                }
+            }
+            if constexpr (FP8) {
+                if (kind > 0) {
+                    float v[8], amax = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = f32x2_split(x[e]);
+                        v[2 * e] = f.x;
+                        v[2 * e + 1] = f.y;
+                        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+#pragma unroll
+                    for (int o = LPR / 2; o >= 1; o >>= 1)
+                        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                    if (!live) continue;
+                    const float sc = amax / 448.f;  // 448: E4M3's largest finite value
+                    if (sc > 0x1p-100f && sc < 0x1p100f) {
+                        // x / sc rounded to nearest from the rounded reciprocal
+                        // r and one correction, q + r (x - q sc) with q = x r
+                        // (Markstein 1990): three operations instead of a
+                        // division's.  (Where x - q sc underflows, the code is 0.)
+                        const float r = 1.f / sc;
+                        const uint64_t r2 = f32x2(r, r), ns2 = f32x2(-sc, -sc);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint64_t q = mul_f32x2(x[e], r2);
+                            const float2 f = f32x2_split(fma_f32x2(fma_f32x2(q, ns2, x[e]), r2, q));
+                            v[2 * e] = f.x;
+                            v[2 * e + 1] = f.y;
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = sc == 0.f ? 0.f : v[e] / sc;
+                    }
+                    const int64_t at = slot * heads + h;
+                    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.cache[kind - 1]) +
+                                               at * D + d0) =
+                        make_uint2(e4m3x2(v[0], v[1]) | (e4m3x2(v[2], v[3]) << 16),
+                                   e4m3x2(v[4], v[5]) | (e4m3x2(v[6], v[7]) << 16));
+                    if (d0 == 0) p.scale[kind - 1][at] = sc;
+                    continue;
+                }
+            }
+            if (!live) continue;
+            __half *dst = kind == 0 ? p.q_out + (t * heads + h) * D
+                                    : static_cast<__half *>(p.cache[0]) + (slot * heads + h) * D;
+            *reinterpret_cast<uint4 *>(dst + d0) = pack_pairs(x);
         }
-        if (!live) continue;
-        __half *dst = kind == 0 ? p.q_out + (t * heads + h) * D
-                                : static_cast<__half *>(p.cache[0]) + (slot * heads + h) * D;
-        *reinterpret_cast<uint4 *>(dst + d0) = pack_pairs(x);
+        if (!more) break;
     }
 }
 
@@ -341,11 +404,24 @@ int norm_rope_write(void *q_out, const void *q, const void *k, const void *v, in
     p.num_slots = num_blocks * block_size;
     p.num_heads = num_heads;
     p.num_kv_heads = num_kv_heads;
-    const int job_rows = 32 / (head_dim / 8) * kRows;
-    p.query_jobs = (num_heads + job_rows - 1) / job_rows;
-    p.row_jobs = (num_kv_heads + job_rows - 1) / job_rows;
-    p.jobs_per_token = static_cast<uint32_t>(p.query_jobs + 2 * p.row_jobs);
-    if (num_tokens > INT32_MAX / static_cast<int64_t>(p.jobs_per_token)) return PKV_ERR_UNSUPPORTED;
+    const int chunk_rows = 32 / (head_dim / 8) * kRows;
+    p.query_chunks = (num_heads + chunk_rows - 1) / chunk_rows;
+    p.row_chunks = (num_kv_heads + chunk_rows - 1) / chunk_rows;
+    p.token_chunks = p.query_chunks + 2 * p.row_chunks;
+    if (num_tokens > INT32_MAX / static_cast<int64_t>(p.token_chunks)) return PKV_ERR_UNSUPPORTED;
+    // the job length with the shortest estimated time: rounds of the resident
+    // warps, times a job's chunks and its start-up (about a chunk's time)
+    const int64_t warps = static_cast<int64_t>(sm_count()) * kMinBlocks * (kThreads / 32);
+    int64_t best = INT64_MAX;
+    for (int c = 1; c <= p.token_chunks; ++c) {
+        const int64_t jobs = num_tokens * ((p.token_chunks + c - 1) / c);
+        const int64_t cost = (jobs + warps - 1) / warps * (c + kJobStart);
+        if (cost < best) {
+            best = cost;
+            p.job_chunks = c;
+        }
+    }
+    p.jobs_per_token = static_cast<uint32_t>((p.token_chunks + p.job_chunks - 1) / p.job_chunks);
     p.num_jobs = static_cast<uint32_t>(num_tokens) * p.jobs_per_token;
     p.err = device_error_record();
     if (p.err == nullptr) return PKV_ERR_CUDA;
