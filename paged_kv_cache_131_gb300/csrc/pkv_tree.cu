@@ -232,9 +232,13 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Every lane waits; false if any lane gave up.
-__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity) {
+// Every lane waits; false if any lane gave up.  The long wait is a call: in
+// line at every place it cost a batch of short items 14% (instruction fetches).
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait_bounded(bar, parity));
+}
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || wait_long(bar, parity);
 }
 
 __device__ __forceinline__ void tensor_g2s_2d(uint32_t dst, const void *tmap, int c0, int c1,
@@ -431,12 +435,14 @@ __device__ __forceinline__ float load_early(const float *p) {
 __device__ __forceinline__ int table_entry(const TreeParams &p, int seq, int b) {
     return load_early(p.block_tables + static_cast<int64_t>(seq) * p.max_blocks + b);
 }
+__device__ __noinline__ void record_block(const TreeParams &p, int seq, int b) {
+    record_error(p.err, PKV_DEVERR_BLOCK_ID, static_cast<int64_t>(seq) * p.max_blocks + b);
+}
 // The block id of entry b, or -1 when it is out of range (recorded when
 // `report`).
 __device__ __forceinline__ int checked_id(const TreeParams &p, int id, int seq, int b, bool report) {
     if (id >= 0 && static_cast<int64_t>(id) < p.num_blocks) return id;
-    if (report)
-        record_error(p.err, PKV_DEVERR_BLOCK_ID, static_cast<int64_t>(seq) * p.max_blocks + b);
+    if (report) record_block(p, seq, b);
     return -1;
 }
 __device__ __forceinline__ int block_id(const TreeParams &p, int seq, int b, bool report) {
@@ -549,7 +555,7 @@ __device__ __noinline__ void clean_values(uint8_t *vb, int key0, int keys, int c
                                           uint32_t *flags) {
     constexpr int kUnits = 8 * CH;  // units of a row
     constexpr int kThreads = kSoftmaxWarps * 32;
-    constexpr int kScan = 4;
+    constexpr int kScan = 2;
     const int end = keys * kUnits;
     const int thread = threadIdx.x - kSoftmaxWarp * 32;
 #pragma unroll 1
@@ -570,25 +576,25 @@ __device__ __noinline__ void clean_values(uint8_t *vb, int key0, int keys, int c
     fence_proxy_async_smem();
 }
 
-// The elements that were left out of a row's O (fp32 bits of dims d0 .. d0 +
-// 31), where the row sees them: a weight times an infinity or a NaN is that,
-// whatever the (positive) weight.
+// Adds to a row's stored results the elements that were left out, where the
+// row sees them: a weight times an infinity or a NaN is that, whatever the
+// (positive) weight.  n results from dim d0 on: fp16 ones, or the fp32 ones of
+// a partial state (groups of four dims, kRows groups apart).
 template <int D, bool FP8>
-__device__ __forceinline__ void add_non_finite(const TreeParams &p, const PieceHead &pc,
-                                               const uint32_t *flags, const uint64_t *mask, int d0,
-                                               uint32_t (&o)[32]) {
-#pragma unroll 1
-    for (int node = 0; node < pc.Q; ++node) {
+__device__ __noinline__ void add_non_finite(const TreeParams &p, int seq, int kvh, int ctx, int Q,
+                                            const uint32_t *flags, const uint64_t *mask, int d0,
+                                            int n, __half *out, float *part) {
+    for (int node = 0; node < Q; ++node) {
         if (!((flags[node >> 5] >> (node & 31)) & 1u) ||
             !((__ldg(mask + (node >> 6)) >> (node & 63)) & 1))
             continue;
-        const int key = pc.L - pc.Q + node;
-        const int id = block_id(p, pc.seq, key / kBS, false);
+        const int key = ctx + node;
+        const int id = block_id(p, seq, key / kBS, false);
         if (id < 0) continue;
         const int64_t at =
-            ((static_cast<int64_t>(id) * kBS + key % kBS) * p.num_kv_heads + pc.kvh) * D + d0;
-#pragma unroll
-        for (int d = 0; d < 32; ++d) {
+            ((static_cast<int64_t>(id) * kBS + key % kBS) * p.num_kv_heads + kvh) * D + d0;
+#pragma unroll 1
+        for (int d = 0; d < n; ++d) {
             float x;
             if constexpr (FP8) {
                 __nv_fp8_e4m3 c;
@@ -597,7 +603,9 @@ __device__ __forceinline__ void add_non_finite(const TreeParams &p, const PieceH
             } else {
                 x = __half2float(static_cast<const __half *>(p.v_cache)[at + d]);
             }
-            if (!isfinite(x)) o[d] = __float_as_uint(__uint_as_float(o[d]) + x);
+            if (isfinite(x)) continue;
+            if (out != nullptr) out[d] = __float2half_rn(__half2float(out[d]) + x);
+            else part[(d >> 2) * (4 * kRows) + (d & 3)] += x;
         }
     }
 }
@@ -622,7 +630,9 @@ __device__ __forceinline__ void codes_to_half(const uint4 &c, uint4 &lo, uint4 &
 // lanes take half a row each of two neighbouring rows, opposite halves, so
 // that their reads and their writes fall on eight different 16-byte columns;
 // a thread's units are whole blocks apart, their places constants apart.
-// `clean`: the values of a step that reaches past the context.
+// `clean`: the values of a step that reaches past the context.  (Two units at a
+// time in a rolled loop: unrolled, 64 ragged FP8 sequences took 109 us instead
+// of 97, for the instruction cache.)
 template <int D, bool V>
 __device__ __forceinline__ void convert_tile(const uint8_t *codes, uint8_t *tile, int keys,
                                              bool clean, int key0, int ctx, int L,
@@ -642,14 +652,14 @@ __device__ __forceinline__ void convert_tile(const uint8_t *codes, uint8_t *tile
                              : (t >> 3) * (CH * 1024) + c * 1024 + (t & 7) * 128);
     uint8_t *d0 = row + ((x ^ (t & 7)) * 16), *d1 = row + (((x + 1) ^ (t & 7)) * 16);
     if (keys == kStepKeys && !clean) {
+#pragma unroll 1
+        for (int i0 = 0; i0 < kUnits; i0 += 2) {
+            uint4 in[2];
 #pragma unroll
-        for (int i0 = 0; i0 < kUnits; i0 += 4) {
-            uint4 in[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2; ++i)
                 in[i] = *reinterpret_cast<const uint4 *>(src + (i0 + i) * kRowsApart * D);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2; ++i) {
                 uint4 lo, hi;
                 codes_to_half(in[i], lo, hi);
                 *reinterpret_cast<uint4 *>(d0 + (i0 + i) * kTileApart) = lo;
@@ -803,6 +813,7 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
     const bool busy_cta = cta < busy;
     if (!busy_cta && threadIdx.x == 0) p.borders[cta].pieces = 0;
 
+    bool ok = busy_cta;  // false: a wait gave up
     if (warp < kSoftmaxWarp) {
         if (!busy_cta) {
         } else if (warp == 0) {
@@ -811,7 +822,6 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
             int cur_ids;
             PieceHead cur = next_piece(p, w, cta, cur_ids);
             int gs = 0;  // steps staged
-            bool ok = true;
 #pragma unroll 1
             for (int it = 0; ok; ++it) {
                 const int rec = it & 1;
@@ -870,7 +880,6 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                 cur_ids = nxt_ids;
             }
             if (!ok) {
-                if (lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT, cta);
                 // let the last copies land before the CTA can exit
 #pragma unroll 1
                 for (int s = 0; s < KS && s < gs; ++s) {
@@ -881,7 +890,6 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
         } else if (warp == 1) {
             // ============================== values ==============================
             int gs = 0;
-            bool ok = true;
 #pragma unroll 1
             for (int it = 0; ok; ++it) {
                 const int rec = it & 1;
@@ -926,7 +934,6 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                 }
             }
             if (!ok) {
-                if (lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT, cta);
 #pragma unroll 1
                 for (int s = 0; s < VS && s < gs; ++s) {
                     const int last = gs - 1 - ((gs - 1 - s) % VS);
@@ -936,7 +943,6 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
         } else if (warp == 2) {
             // ==================== query tiles and score MMAs ====================
             int gs = 0, q_staged = 0;
-            bool ok = true;
 #pragma unroll 1
             for (int it = 0; ok; ++it) {
                 const int rec = it & 1;
@@ -998,7 +1004,6 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                 }
             }
             if (!ok) {
-                if (lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT, cta);
                 if (q_staged) wait_bounded(br.q_full(), (q_staged - 1) & 1);
             }
         } else {
@@ -1022,7 +1027,6 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
             }
             __syncwarp();
             int gs = 0;
-            bool ok = true;
 #pragma unroll 1
             for (int it = 0; ok; ++it) {
                 const int rec = it & 1;
@@ -1062,7 +1066,6 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                     __syncwarp();
                 }
             }
-            if (!ok && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT, cta);
         }
     } else if (FP8 && warp >= kConvertWarp) {
         // ========================= codes to fp16 tiles =========================
@@ -1070,7 +1073,6 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
         // the scales one step ahead.
         const int tid = threadIdx.x - kConvertWarp * 32;
         int gs = 0;
-        bool ok = busy_cta;
 #pragma unroll 1
         for (int it = 0; ok; ++it) {
             const int rec = it & 1;
@@ -1161,7 +1163,6 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                 }
             }
         }
-        if (!ok && busy_cta && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT, cta);
     } else {
         // =============================== softmax ===============================
         const int wh = (warp - kSoftmaxWarp) >> 2;
@@ -1170,7 +1171,6 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
         const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32 + wh * 16) << 16);
         const float sl2 = p.scale_log2;
         int gs = 0;
-        bool ok = busy_cta;
 #pragma unroll 1
         for (int it = 0; ok; ++it) {
             const int rec = it & 1;
@@ -1384,8 +1384,6 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                     uint32_t o[32];
                     tc::ld32_halves<DH>(tl + kTmemO + 32 * k, o);
                     tc::wait_ld();
-                    if (any != 0 && row_ok)
-                        add_non_finite<D, FP8>(p, pc, my_flags, mask, DH * h + 32 * k, o);
                     if (whole) {
                         // exchanged inside groups of four lanes, so that a store
                         // of the warp covers 64 bytes of eight rows (16 bytes of
@@ -1422,12 +1420,21 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                 }
                 tc::fence_before_sync();
                 __syncwarp();
+                if (any != 0 && row_ok)
+                    add_non_finite<D, FP8>(
+                        p, pc.seq, pc.kvh, ctx, pc.Q, my_flags, mask, DH * h, DH,
+                        whole ? p.out + (static_cast<int64_t>(pc.q0 + (rr >> logG)) * H +
+                                         pc.kvh * G + (rr & (G - 1))) * D + DH * h
+                              : nullptr,
+                        reinterpret_cast<float *>(p.part_o) +
+                            ((static_cast<int64_t>(pc.slot) * (D / 4) + DH * h / 4) * kRows + r) * 4);
+                __syncwarp();
             }
             if (lane == 0) mbar_arrive(br.o_free());
         }
-        if (!ok && busy_cta && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT, cta);
     }
 
+    if (busy_cta && !ok && lane == 0) record_error(p.err, PKV_DEVERR_TIMEOUT, cta);
     // every role is done: hand the tensor memory back
     tc::fence_before_sync();
     __syncthreads();
