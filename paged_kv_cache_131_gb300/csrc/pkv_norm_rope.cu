@@ -327,8 +327,8 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks)
                         for (int e = 0; e < 4; ++e) {
                             const uint64_t q = mul_f32x2(x[e], r2);
                             const float2 f = f32x2_split(fma_f32x2(fma_f32x2(q, ns2, x[e]), r2, q));
-                            v[2 * e] = f.x;
-                            v[2 * e + 1] = f.y;
+                            v[2 * e] = copysignf(f.x, v[2 * e]);  // (the correction of -0 is +0)
+                            v[2 * e + 1] = copysignf(f.y, v[2 * e + 1]);
                         }
                     } else {
 #pragma unroll

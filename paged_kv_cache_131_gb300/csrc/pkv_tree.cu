@@ -1111,7 +1111,9 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                 if (!ok) break;
                 {
                     const int ring = gs % kScaleRing;
-                    scales[ring * 2 * kStepKeys + tid] = ks;
+                    // (the dot product with a key of infinities is NaN, but its
+                    // dot product with the codes times infinity need not be)
+                    scales[ring * 2 * kStepKeys + tid] = isfinite(ks) ? ks : NAN;
                     // (a drafted row's scale that is not finite counts as its
                     // non-finite elements do: left out here, added at the end)
                     const bool out = !isfinite(vs) && tid + key0 >= ctx;

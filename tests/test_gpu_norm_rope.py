@@ -119,6 +119,8 @@ CASES = [
     (7, 50, 8, 4, 128, 0, True),      # norm alone
     (8, 50, 8, 4, 128, 0, False),     # a plain write with the queries copied
     (9, 2047, 2, 1, 64, 48, False),
+    (10, 30, 7, 3, 128, 128, True),   # rows that leave chunks part empty
+    (11, 9000, 6, 2, 64, 64, True),   # jobs of several chunks
 ]
 
 
@@ -155,6 +157,34 @@ def test_values_quantise_as_the_plain_write_does():
     v = c.d["v"].contiguous()
     pkv.pkv_cache_write_fp8(v, v, dev(c.slots), *ref, BS, c.NB)
     assert torch.equal(caches[1], ref[1]) and torch.equal(caches[3], ref[3])
+
+
+def test_values_of_every_magnitude_quantise_as_the_plain_write_does():
+    # the correctly rounded quotient, from fp16's smallest numbers to its largest
+    rng = np.random.default_rng(27)
+    c = Case(27, 3000, 1, 4, 128, 0, norm=False)
+    v = c.d["v"]
+    v.copy_(dev((rng.standard_normal(v.shape) * 10.0 ** rng.uniform(-8, 4.6, v.shape[:2] + (1,)))
+                .clip(-65504, 65504).astype(np.float16)))
+    v[0, 0], v[1, 1] = 0, 2.0 ** -24
+    _, caches = c.run(True, False)
+    ref = [torch.full_like(x, 0x5A if x.dtype == torch.uint8 else 9.0) for x in caches]
+    w = v.contiguous()
+    pkv.pkv_cache_write_fp8(w, w, dev(c.slots), *ref, BS, c.NB)
+    assert torch.equal(caches[1], ref[1]) and torch.equal(caches[3], ref[3])
+
+
+def test_tokens_apart():
+    # every other token of a wider tensor, and rows of a token reversed in time
+    c = Case(28, 40, 8, 2, 64, 64)
+    ref, caches = c.run(False, False)
+    for n in c.d:
+        wide = torch.full((80,) + tuple(c.d[n].shape[1:]), float("nan"), dtype=torch.float16,
+                          device="cuda")
+        wide[::2] = c.d[n]
+        c.d[n] = wide[::2]
+    got, again = c.run(False, False)
+    assert torch.equal(got, ref) and all(torch.equal(a, b) for a, b in zip(caches, again))
 
 
 @pytest.mark.parametrize("fp8", [False, True])

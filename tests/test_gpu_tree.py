@@ -147,6 +147,10 @@ CASES = [
     (12, [5000], [4], 2, 1, 128),                        # one head: split over many CTAs
     (13, [260] * 40, [3] * 40, 8, 4, 64),
     (14, [16, 31, 47, 64, 97, 113], [1, 2, 3, 4, 5, 6], 2, 2, 128),
+    (15, [300, 70], [33, 9], 12, 3, 64),                 # three KV heads
+    (16, [190, 260], [40, 17], 40, 5, 128),
+    (17, [700], [256], 8, 1, 64),                        # sixteen tiles, four mask words
+    (18, [100, 400, 90, 390, 80], [3, 40, 70, 1, 20], 16, 2, 128),  # 1, 3, 5, 1, 2 tiles
 ]
 
 
@@ -226,7 +230,7 @@ def test_non_finite_drafted_rows_reach_only_those_that_see_them(fp8, value):
             assert (got[hit] == value).all()
         fin = np.where(np.isfinite(ref), ref, 0)
         lim = spec.tree_tolerance(fin, {k: np.where(np.isfinite(x), x, 8.0) for k, x in tol.items()}, 128)
-        assert (np.abs(got - ref)[~hit] <= lim[~hit]).all()
+        assert (np.abs(got[~hit] - ref[~hit]) <= lim[~hit]).all()
     # keys: a masked score is dropped whatever it is
     t = Tree(54, [60], [20], 8, 2, 128, fp8=fp8)
     ref = t.run()
@@ -343,4 +347,113 @@ def test_a_long_cache_past_32_bits_of_bytes():
     d["tables"] = torch.where(d["tables"] < t.NB, d["tables"] + (NB - t.NB), d["tables"])
     t.NB = NB
     assert np.array_equal(t.call().cpu().numpy().astype(np.float64), ref)
+    assert pkv.pkv_get_device_error() == (0, -1)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["fp16", "fp8"])
+def test_more_sequences_than_threads(fp8):
+    rng = np.random.default_rng(91)
+    nodes = [int(n) for n in rng.integers(0, 4, 700)]
+    nodes[13], nodes[600] = 40, 70  # three and five tiles among the many of one
+    lens = [n + int(c) for n, c in zip(nodes, rng.integers(0, 60, 700))]
+    Tree(92, lens, nodes, 16, 2, 64, fp8=fp8).check()
+
+
+def test_nothing_to_do_leaves_the_outputs():
+    t = Tree(93, [5, 0], [0, 0], 8, 2, 64)
+    t.q = np.zeros((3, 8, 64), np.float16)  # rows of no sequence
+    t.mask = np.ones((3, 1), bool)
+    d = t.stage()
+    t.call()
+    assert pkv.pkv_get_device_error() == (0, -1) and (d["out"] == 7.0).all()
+
+
+def test_fp8_scales_over_many_orders():
+    # value scales from 1e-7 to 100 and key scales from 1e-5 to 0.1, row by row
+    t = Tree(94, [700, 300], [20, 33], 8, 2, 128, fp8=True, spread=3.0)
+    rng = np.random.default_rng(95)
+    live = np.isfinite(t.parts[1])
+    t.parts[1][live] = 10.0 ** rng.uniform(-5, -1, live.sum())
+    t.parts[3][live] = 10.0 ** rng.uniform(-7, 2, live.sum())
+    t.check()
+    # and all of them far out (an output of 1e-12 is nothing in fp16)
+    for v in (1e-12, 90.0):
+        t.parts[3][live] = v
+        t.check()
+
+
+@pytest.mark.parametrize("value", [np.nan, np.inf])
+def test_fp8_scales_that_are_not_finite(value):
+    t = Tree(96, [300], [20], 8, 2, 128, fp8=True)
+    ref = t.run()
+    b, o = t.slot(0, 7)
+    t.parts[3][b, o, 1] = value  # the value scale of drafted token 7, KV head 1
+    got = t.run()
+    sees = t.mask[:, 7]
+    assert sees.any() and not sees.all()
+    assert np.array_equal(got[~sees], ref[~sees]) and np.array_equal(got[:, :4], ref[:, :4])
+    assert not np.isfinite(got[sees][:, 4:]).any()
+    k, v = t.values()
+    with np.errstate(invalid="ignore"):
+        want = t.want()[0]
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    t = Tree(96, [300], [20], 8, 2, 128, fp8=True)
+    t.parts[1][b, o, 0] = value  # a key scale: rows that do not see it stay as they were
+    got = t.run()
+    assert np.array_equal(got[~sees], ref[~sees]) and np.array_equal(got[:, 4:], ref[:, 4:])
+    assert np.isnan(got[sees][:, :4]).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["fp16", "fp8"])
+def test_non_finite_context_reaches_every_row(fp8):
+    t = Tree(97, [300], [20], 8, 2, 128, fp8=fp8)
+    ref = t.run()
+    b, o = t.tables[0, 3], 5  # a position of the context, KV head 0
+    if fp8:
+        t.parts[2][b, o, 0, 9] = 0x7F
+    else:
+        t.parts[1][b, o, 0, 9] = np.nan
+    got = t.run()
+    hit = np.zeros(got.shape, bool)
+    hit[:, :4, 9] = True
+    assert np.isnan(got[hit]).all() and np.array_equal(got[~hit], ref[~hit])
+
+
+def test_calls_of_other_kinds_follow_on_the_stream():
+    # the merge lets the next kernel start early: a decode, a chunk attention
+    # and a cache write that follow at once see what they should, and leave the
+    # tree's outputs alone
+    t = Tree(98, [900, 333, 64], [12, 30, 5], 16, 4, 128)
+    d = t.stage()
+    S = 3
+    q = torch.randn(S, 16, 128, device="cuda").half()
+    lens = torch.tensor([880, 300, 59], dtype=torch.int32, device="cuda")
+    qs = torch.arange(S + 1, dtype=torch.int32, device="cuda")
+    dws = torch.zeros(pkv.pkv_decode_workspace_bytes(S, 16, 4, 128, 1000), dtype=torch.uint8,
+                      device="cuda")
+    cws = torch.zeros(pkv.pkv_chunk_workspace_bytes(S, 16, 4, 128, S, 1, 1000), dtype=torch.uint8,
+                      device="cuda")
+    outs = [torch.zeros_like(q) for _ in range(2)]
+
+    def follow():
+        a = (d["tables"], lens)
+        pkv.pkv_decode_attention(outs[0], q, *d["caches"], *a, t.scale, 16, 4, 128, BS, 1000, t.NB,
+                                 dws)
+        t.call()
+        pkv.pkv_chunk_attention(outs[1], q, *d["caches"], *a, qs, t.scale, 16, 4, 128, BS, 1, 1000,
+                                t.NB, cws)
+
+    t.call()
+    torch.cuda.synchronize()
+    ref = d["out"].clone()
+    follow()
+    torch.cuda.synchronize()
+    dref = [x.clone() for x in outs]
+    for _ in range(30):
+        t.call()
+        follow()
+        t.call()
+    torch.cuda.synchronize()
+    assert torch.equal(d["out"], ref)
+    assert torch.equal(outs[0], dref[0]) and torch.equal(outs[1], dref[1])
     assert pkv.pkv_get_device_error() == (0, -1)
