@@ -19,10 +19,10 @@
 // factors made), small ones a chunk per warp.
 //
 // Bound: HBM -- every row read and written once; the table's rows come from L2.
-// 32 query and 8 KV heads of 128 dims: 16384 tokens 75.5 us into fp16 caches
-// (5.45 TB/s), 85 us into FP8 ones (4.3 TB/s: the scales' divisions).  Chunks of
-// 4 rows: 77 and 90 us; 4 resident blocks instead of 3: 86 and 100 (spills); a
-// chunk per warp: 139 and 154 (the factors are then made per chunk).
+// 32 query and 8 KV heads of 128 dims: 16384 tokens 74.4 us into fp16 caches
+// (5.5 TB/s), 82 us into FP8 ones (4.5 TB/s).  Chunks of 4 rows: 77 and 90 us;
+// a third more resident warps: 86 and 100 (spills); a chunk per warp: 139 and
+// 154 (the factors are then made per chunk).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -38,9 +38,9 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kRows = 2;       // rows per row group and chunk
-constexpr int kMinBlocks = 3;  // resident blocks per SM
+constexpr int kMinBlocks = 6;  // resident blocks per SM
 constexpr int kJobStart = 4;   // a job's start-up, in chunks
 
 struct NormRopeParams {

@@ -1582,15 +1582,26 @@ int make_code_map(CUtensorMap *map, const void *cache, int64_t num_blocks, int r
                   D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-// Query rows [Tq][heads][D] by 128 bytes of 16 rows: `group` heads of 16/group
-// tokens.
-int make_query_map(CUtensorMap *map, const void *q, int64_t tokens, int heads, int D, int group) {
+// fp16 values [NB * 16][row_bytes] as {128 bytes, rows, chunks}: 16 rows of a
+// head's chunks, chunk by chunk.
+int make_value_map(CUtensorMap *map, const void *cache, int64_t num_blocks, int row_bytes, int D) {
+    const cuuint64_t row = static_cast<cuuint64_t>(row_bytes);
+    const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(num_blocks) * kBS, row / 128};
+    const cuuint64_t strides[2] = {row, 128};
+    const cuuint32_t box[3] = {128, kBS, static_cast<cuuint32_t>(D / 64)};
+    return encode(map, cache, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Query rows [Tq][heads][D] by 128 bytes of `rows` rows: `group` heads of
+// rows/group tokens.
+int make_query_map(CUtensorMap *map, const void *q, int64_t tokens, int heads, int D, int group,
+                   int rows) {
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(heads),
                                 static_cast<cuuint64_t>(tokens)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2,
                                    static_cast<cuuint64_t>(heads) * D * 2};
     const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(group),
-                               static_cast<cuuint32_t>(16 / group)};
+                               static_cast<cuuint32_t>(rows / group)};
     return encode(map, q, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
@@ -1604,12 +1615,13 @@ int launch(TreeParams &p, void *workspace, cudaStream_t stream) {
                  : make_key_map(&p.tm_k, p.k_cache, p.num_blocks, row_bytes, D);
     if (st == PKV_OK)
         st = FP8 ? make_code_map(&p.tm_v, p.v_cache, p.num_blocks, row_bytes, D)
-                 : dec::make_kv_tensor_map(&p.tm_v, p.v_cache, p.num_blocks, row_bytes, D / 64);
+                 : make_value_map(&p.tm_v, p.v_cache, p.num_blocks, row_bytes, D);
     if (st == PKV_OK)
-        st = dec::make_q_tensor_map(&p.tm_q, p.q, p.num_query_tokens, p.num_heads, D,
-                                    p.num_heads / Hk);
+        st = make_query_map(&p.tm_q, p.q, p.num_query_tokens, p.num_heads, D, p.num_heads / Hk,
+                            kRows);
     if (st == PKV_OK)
-        st = make_query_map(&p.tm_q16, p.q, p.num_query_tokens, p.num_heads, D, p.num_heads / Hk);
+        st = make_query_map(&p.tm_q16, p.q, p.num_query_tokens, p.num_heads, D, p.num_heads / Hk,
+                            16);
     if (st != PKV_OK) return st;
     const int ctas = sm_count();
     const Scratch z = scratch(ctas, D);

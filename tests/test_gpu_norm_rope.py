@@ -290,6 +290,26 @@ def test_cache_read_fp8(T, Hk, D):
         assert (got[~live] == 7.0).all()
 
 
+def test_cache_read_of_more_units_than_32_bits_count():
+    # 2^31 16-code units and more (69 GB of rows), nearly all of them padding
+    T, Hk, D = 4098, 65536, 128
+    if torch.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("needs 90 GB")
+    codes = torch.randint(0, 127, (1, BS, Hk, D), device="cuda", dtype=torch.uint8)
+    scale = torch.rand(1, BS, Hk, device="cuda")
+    slots = torch.full((T,), -1, device="cuda", dtype=torch.int64)
+    slots[3], slots[T - 1], slots[T - 2] = 2, 5, 11
+    rows = torch.empty(T, Hk, D, dtype=torch.float16, device="cuda")
+    rows[T - 3] = 7.0
+    pkv.pkv_cache_read_fp8(rows, None, slots, codes, None, scale, None, BS, 1)
+    for t in (3, T - 1, T - 2):
+        want = codes[0, slots[t]].view(torch.float8_e4m3fn).float() * scale[0, slots[t]][:, None]
+        assert torch.equal(rows[t], want.half())
+    assert (rows[T - 3] == 7.0).all()
+    del rows
+    torch.cuda.empty_cache()
+
+
 def test_cache_read_keys_alone_and_round_trip():
     T, Hk, D = 100, 4, 128
     x = torch.randn(T, Hk, D, device="cuda").half()
