@@ -84,6 +84,7 @@ constexpr int kTmemS = 128;
 constexpr int kTmemP = 384;
 constexpr float kRescaleLog2 = 8.f;  // move the reference past 2^8
 constexpr int kFlagWords = PKV_MAX_TREE_NODES / 32;
+constexpr int kFlagRing = 4;   // pieces whose flags are kept (see the softmax)
 constexpr int kValidRing = 8;  // steps whose blocks' validity is kept (see the softmax)
 constexpr int kScaleRing = 3;  // steps whose scales are kept (see the converters)
 // Units of an item: its steps and kItemUnits for its start-up (1, 2, 3, 4: 104.4,
@@ -172,11 +173,12 @@ struct Geo {
     static constexpr int kBars = 4 + 2 + 2 * kKStages + 2 * kVStages + 8 + 1 + 3;
     static constexpr int kOffPiece = kOffBar + kBars * 8;
     static constexpr int kOffFlags = kOffPiece + 2 * static_cast<int>(sizeof(Piece));
-    static constexpr int kOffValid = kOffFlags + 3 * kFlagWords * 4;  // (see the softmax)
+    static constexpr int kOffValid = kOffFlags + kFlagRing * kFlagWords * 4;
     static constexpr int kOffTop = kOffValid + kValidRing * 4;  // [ring][4] largest value scale
     static constexpr int kOffMisc = kOffTop + kScaleRing * kConvertWarps * 4;
     static constexpr int kOffScan = (kOffMisc + 4 + 7) / 8 * 8;  // the prologue's words
     static constexpr int kBytes = kOffScan + (kThreads / 32 + 4) * 8;
+    static_assert(kBytes + dec::kTileAlign <= dec::kSmemPerSM, "more than an SM's shared memory");
 };
 
 // mbarrier addresses (shared space) by role
@@ -256,6 +258,18 @@ __device__ __forceinline__ void tensor_g2s_4d(uint32_t dst, const void *tmap, in
         "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
         "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
         : "memory");
+}
+
+// After tc::wait_ld: registers of a tensor-memory load hold their values from
+// here on (nothing computed from them moves above this).
+__device__ __forceinline__ void landed(uint32_t (&r)[32]) {
+    asm volatile(""
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]),
+                 "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
+                 "+r"(r[31]));
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -344,7 +358,7 @@ struct SeqGeo {
 
 // Up to 64 rows are laid out as four groups of 16, one in each quarter of the
 // tile, so that every quarter of the SM has one softmax warp at work instead of
-// half of them two (FP8, 64 rows: 3200 -> 2500 cycles a step).
+// half of them two (FP8, 64 rows, 16 x 8000..32768 tokens: 208 -> 198 us).
 __device__ __forceinline__ bool spread_rows(int rows) { return rows <= kRows / 2; }
 
 __device__ __forceinline__ SeqGeo make_geo(int L, int Q, int q0, int G) {
@@ -760,7 +774,7 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
         prefetch_tensormap(&p.tm_v);
         prefetch_tensormap(&p.tm_q);
     }
-    if (threadIdx.x < 3 * kFlagWords) flags[threadIdx.x] = 0;
+    if (threadIdx.x < kFlagRing * kFlagWords) flags[threadIdx.x] = 0;
     if (warp == 2) {
         tc::tmem_alloc(sb + Gm::kOffMisc, kTmemCols);
         tc::tmem_relinquish();
@@ -1087,7 +1101,7 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
             if (lane == 0) mbar_arrive(br.piece_empty(rec));
             if (pc.done) break;
             const int ctx = pc.L - pc.Q;
-            uint32_t *my_flags = flags + (it % 3) * kFlagWords;
+            uint32_t *my_flags = flags + (it % kFlagRing) * kFlagWords;
             const int64_t off = static_cast<int64_t>(tid % kBS) * Hk + pc.kvh;
             // the scales of key tid of step n, whose block is id; 0: no such key
             auto scale_of = [&](const float *scale, int id, int n) {
@@ -1146,12 +1160,6 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                 ok = wait_all(br.v_full(vst), (gs / VS) & 1);
                 if (ok && gs >= 2) ok = wait_all(br.pv_done(b), ((gs >> 1) - 1) & 1);
                 if (!ok) break;
-                if (n == 0) {
-                    // this piece's flags: last read three pieces back, before
-                    // the P V just waited for began its piece
-                    if (tid < kFlagWords) my_flags[tid] = 0;
-                    asm volatile("bar.sync 1, 128;" ::: "memory");
-                }
                 const bool tail = key0 + kStepKeys > ctx;
                 if (tail && tid + key0 >= ctx && left_out)  // (its stored scale is 0)
                     atomicOr(&my_flags[(tid + key0 - ctx) >> 5], 1u << ((tid + key0 - ctx) & 31));
@@ -1198,7 +1206,7 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                        : nullptr;
             // bring the row's mask near, for the step that needs it
             if (row_ok) prefetch_l1(mask);
-            uint32_t *my_flags = flags + (it % 3) * kFlagWords;
+            uint32_t *my_flags = flags + (it % kFlagRing) * kFlagWords;
             float m_used = -INFINITY, l = 0.f;  // l: this thread's keys only
 
 #pragma unroll 1
@@ -1249,6 +1257,8 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                 // of this warp)
                 const uint32_t blocks = valid[gs % kValidRing];
                 tc::wait_ld();
+                landed(*reinterpret_cast<uint32_t(*)[32]>(sx));
+                landed(*reinterpret_cast<uint32_t(*)[32]>(sx + 32));
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(br.s_free(sbuf));
@@ -1309,6 +1319,7 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                         uint32_t x[32];
                         tc::ld32_halves<DH>(tl + kTmemO + 32 * c, x);
                         tc::wait_ld();
+                        landed(x);
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
@@ -1364,12 +1375,13 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                 ok = false;
                 break;
             }
-            // fp16: the flags of the piece after the next one -- every warp has
-            // read what they held for the previous piece (it has since handed
-            // over this piece's weights), and none sets them before this warp
-            // has handed over the next piece's
-            if (!FP8 && warp == kSoftmaxWarp && lane < kFlagWords)
-                flags[(it + 2) % 3 * kFlagWords + lane] = 0;
+            // The flags of the piece three ahead, whose first ones are set after
+            // every warp has read this piece's O (o_free, before the next piece's
+            // first P V, before its values or the third piece's are cleaned).
+            // Their buffer held the piece before this one's: read by every warp
+            // before this piece's first P V.
+            if (warp == kSoftmaxWarp && lane < kFlagWords)
+                flags[(it + 3) % kFlagRing * kFlagWords + lane] = 0;
             __syncwarp();
             if (live) {
                 tc::fence_after_sync();
@@ -1386,6 +1398,7 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                     uint32_t o[32];
                     tc::ld32_halves<DH>(tl + kTmemO + 32 * k, o);
                     tc::wait_ld();
+                    landed(o);
                     if (whole) {
                         // exchanged inside groups of four lanes, so that a store
                         // of the warp covers 64 bytes of eight rows (16 bytes of
