@@ -453,7 +453,10 @@ int pkv_cache_read_fp8(void *k, void *v, const int64_t *slot_mapping, int64_t nu
  *   pkv_chunk_attention.
  * Ordering: the call may start before an earlier kernel that signals
  * programmatic launch completion has finished, and waits for it before it
- * reads or writes anything.
+ * reads or writes anything.  It signals early itself: a following kernel that
+ * is launched with programmatic serialization must not read out before its
+ * own wait (so out is not to be the q of a pkv_decode_attention or a
+ * pkv_chunk_attention that follows, which read q before theirs).
  * Returns PKV_OK (no sequence or no query token launches nothing),
  * PKV_ERR_NULL, PKV_ERR_INVALID, PKV_ERR_UNSUPPORTED, PKV_ERR_ALIGNMENT (16
  * bytes; 8 for the mask, 4 for int32), PKV_ERR_WORKSPACE, PKV_ERR_CUDA.
@@ -468,7 +471,8 @@ int pkv_tree_attention(void *out, const void *q, const void *k_cache, const void
                        void *workspace, size_t workspace_bytes, pkv_stream_t stream);
 
 /* The same over FP8 caches, read as value(code) * scale of their rows (layout
- * of pkv_cache_write_fp8; caches and scales 16-byte aligned). */
+ * of pkv_cache_write_fp8; caches and scales 16-byte aligned).  A key whose
+ * scale is not finite makes the rows that see it NaN. */
 int pkv_tree_attention_fp8(void *out, const void *q, const void *k_cache, const void *v_cache,
                            const float *k_scale, const float *v_scale,
                            const int32_t *block_tables, const int32_t *seq_lens,
