@@ -31,9 +31,10 @@
 //    and at most 2^-12 of a weight's step each), with the tree's mask;
 //  * FP8: the rings hold codes, and warps 12-15 turn them into fp16 tiles
 //    (exact) for the MMAs.  A key's scale multiplies its score and its value's
-//    scale the weight, both in fp32; m then also covers the logarithm of the
-//    largest value scale of a step, so the scaled weights stay in fp16's range
-//    whatever the scales are.
+//    scale the weight, both in fp32; m is then the largest visible log2 of
+//    their product, so the scaled weights use fp16's range whatever the scales
+//    are.  (A step's largest score plus its largest scale's logarithm is an
+//    upper bound; the maximum itself is taken when that passes the reference.)
 // Value rows behind the sequence's end hold anything and are zeroed before the
 // MMA (by the softmax warps, FP8: as they are converted); drafted rows may be
 // masked for some query rows, and 0 x NaN is NaN, so their non-finite elements
@@ -168,8 +169,8 @@ struct Geo {
     // FP8: one fp16 key tile and two value tiles, and the scales
     static constexpr int kOffK16 = kOffV + kVStages * kStage;
     static constexpr int kOffV16 = kOffK16 + (FP8 ? kK : 0);
-    static constexpr int kOffScale = kOffV16 + (FP8 ? 2 * kV : 0);  // [ring][k, v][128]
-    static constexpr int kOffBar = kOffScale + (FP8 ? kScaleRing * 2 * kStepKeys * 4 : 0);
+    static constexpr int kOffScale = kOffV16 + (FP8 ? 2 * kV : 0);  // [ring][k, v, log2 v][128]
+    static constexpr int kOffBar = kOffScale + (FP8 ? kScaleRing * 3 * kStepKeys * 4 : 0);
     static constexpr int kBars = 4 + 2 + 2 * kKStages + 2 * kVStages + 8 + 1 + 3;
     static constexpr int kOffPiece = kOffBar + kBars * 8;
     static constexpr int kOffFlags = kOffPiece + 2 * static_cast<int>(sizeof(Piece));
@@ -276,6 +277,13 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// log2 of a value scale's size as the reference counts it: no less than -100 (a
+// weight relative to the reference stays finite) and no more than 121 (it stays
+// normal, and the scaled one, at most 2^8 2^7, finite in fp16).
+__device__ __forceinline__ float scale_log2(float vs) {
+    return fminf(__log2f(fmaxf(fabsf(vs), 0x1p-100f)), 121.f);
 }
 
 // Packed fp32 pairs (one instruction for two lanes' worth of fma, mul or add)
@@ -1127,11 +1135,13 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                     const int ring = gs % kScaleRing;
                     // (the dot product with a key of infinities is NaN, but its
                     // dot product with the codes times infinity need not be)
-                    scales[ring * 2 * kStepKeys + tid] = isfinite(ks) ? ks : NAN;
+                    scales[ring * 3 * kStepKeys + tid] = isfinite(ks) ? ks : NAN;
                     // (a drafted row's scale that is not finite counts as its
                     // non-finite elements do: left out here, added at the end)
                     const bool out = !isfinite(vs) && tid + key0 >= ctx;
-                    scales[ring * 2 * kStepKeys + kStepKeys + tid] = out ? 0.f : vs;
+                    scales[ring * 3 * kStepKeys + kStepKeys + tid] = out ? 0.f : vs;
+                    scales[ring * 3 * kStepKeys + 2 * kStepKeys + tid] =
+                        scale_log2(isfinite(vs) ? vs : 0.f);
                     // (the bits of non-negative floats order as they do)
                     const uint32_t top = __reduce_max_sync(
                         0xffffffffu, isfinite(vs) ? __float_as_uint(fabsf(vs)) : 0u);
@@ -1262,11 +1272,11 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(br.s_free(sbuf));
-                const float *sc = scales + (gs % kScaleRing) * 2 * kStepKeys + kHalfKeys * h;
+                const float *sc = scales + (gs % kScaleRing) * 3 * kStepKeys + kHalfKeys * h;
                 float top2 = 0.f;  // log2 of the step's largest value scale
                 if constexpr (FP8) {
                     const float *t = tops + (gs % kScaleRing) * kConvertWarps;
-                    top2 = __log2f(fmaxf(fmax3(t[0], t[1], t[2]), fmaxf(t[3], 0x1p-100f)));
+                    top2 = scale_log2(fmaxf(fmax3(t[0], t[1], t[2]), t[3]));
 #pragma unroll
                     for (int e = 0; e < kHalfKeys; e += 4) {
                         const float4 k4 = *reinterpret_cast<const float4 *>(sc + e);
@@ -1301,8 +1311,33 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                                        fmaxf(mr[6], mr[7]));
                 // the row's other half: the thread 16 lanes away
                 const float mo = __shfl_xor_sync(0xffffffffu, mx, 16);
-                const float m_new = fmaxf(m_used, fmaf(fmaxf(mx, mo), sl2, top2));
-                const bool raise = m_new > m_used + kRescaleLog2;
+                float m_new = fmaxf(m_used, fmaf(fmaxf(mx, mo), sl2, top2));
+                bool raise = m_new > m_used + kRescaleLog2;
+                if constexpr (FP8) {
+                    // the largest scale need not be at a key that the row sees,
+                    // nor at one with weight: the largest product itself
+                    if (__any_sync(0xffffffffu, raise)) {
+                        const uint64_t s2 = f32x2(sl2, sl2);
+                        float ex = -INFINITY, ey = -INFINITY;
+#pragma unroll
+                        for (int e = 0; e < kHalfKeys; e += 4) {
+                            const float4 lv =
+                                *reinterpret_cast<const float4 *>(sc + 2 * kStepKeys + e);
+                            const float2 a = f32x2_split(
+                                fma_f32x2(f32x2(__uint_as_float(sx[e]), __uint_as_float(sx[e + 1])),
+                                          s2, f32x2(lv.x, lv.y)));
+                            const float2 b = f32x2_split(fma_f32x2(
+                                f32x2(__uint_as_float(sx[e + 2]), __uint_as_float(sx[e + 3])), s2,
+                                f32x2(lv.z, lv.w)));
+                            ex = fmax3(ex, a.x, a.y);
+                            ey = fmax3(ey, b.x, b.y);
+                        }
+                        ex = fmaxf(ex, ey);
+                        ex = fmaxf(ex, __shfl_xor_sync(0xffffffffu, ex, 16));
+                        m_new = fmaxf(m_used, ex);
+                        raise = m_new > m_used + kRescaleLog2;
+                    }
+                }
                 // O holds this piece's earlier steps relative to m_used: rescale
                 // this thread's columns before the reference moves (the
                 // previous P V done first)

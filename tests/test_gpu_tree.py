@@ -382,6 +382,50 @@ def test_fp8_scales_over_many_orders():
         t.check()
 
 
+@pytest.mark.parametrize("value", [1e6, 1e20, 3e38])
+def test_fp8_a_masked_rows_large_scale_reaches_only_those_that_see_it(value):
+    for seed, lens, nodes in ((101, [300], [20]), (102, [40], [33]), (103, [900, 200], [12, 90])):
+        t = Tree(seed, lens, nodes, 8, 2, 128, fp8=True)
+        Q = nodes[0]
+        b, o = t.slot(0, Q - 1)
+        t.parts[3][b, o] = value
+        sees = t.mask[:, Q - 1].copy()
+        sees[Q:] = False
+        assert sees[:Q].sum() < Q
+        t.check(rows=~sees)
+
+
+def test_fp8_a_large_scale_of_a_key_without_weight():
+    # a context key that no row gives weight to, with a value scale 1e5 times
+    # the others'
+    t = Tree(104, [500], [12], 4, 1, 64, fp8=True)
+    t.q = np.abs(t.q).astype(np.float16)
+    table = spec.e4m3_table()
+    for p in (3, 130, 400):
+        b, o = t.tables[0, p // BS], p % BS
+        t.parts[0][b, o] = 0xF8  # -256 everywhere
+        t.parts[1][b, o] = 0.01
+        t.parts[3][b, o] = 1000.0
+    got = t.run()
+    ref, terms = t.want()
+    # These keys' scores are 14 or more below their row's largest one, so their
+    # weight times 1000 is below e^-14 1000 < 2^-10 of the largest weight, less
+    # than that weight times its own scale (0.5/150 > 2^-9).  A product of
+    # weight and scale below fp16's normal range is off by 2^-25 of the largest
+    # such product, at most (largest weight) 1.5/150, and by 448 times that in
+    # O: the bound's max |v| is that of the other rows, 448 * 1.5/150.
+    s = -256 * 0.01 * t.q.astype(np.float64).sum(-1) * t.scale
+    assert table[0xF8] == -256
+    k, v = t.values()
+    top = np.array([[(t.q[r, h].astype(np.float64) * k[t.tables[0, np.arange(488) // BS],
+                                                       np.arange(488) % BS, 0]).sum(-1).max()
+                     for h in range(4)] for r in range(12)]) * t.scale
+    assert (s - top < -14).all()
+    terms["vmax"] = np.minimum(terms["vmax"], 448 * 1.5 / 150)
+    tol = spec.tree_tolerance(ref, terms, 64)
+    assert (np.abs(got - ref) <= tol).all(), (np.abs(got - ref) / tol).max()
+
+
 @pytest.mark.parametrize("value", [np.nan, np.inf])
 def test_fp8_scales_that_are_not_finite(value):
     t = Tree(96, [300], [20], 8, 2, 128, fp8=True)
