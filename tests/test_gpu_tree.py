@@ -284,6 +284,29 @@ def test_bad_sequences_and_blocks_are_skipped_and_recorded(fp8):
         assert np.array_equal(got[rows], ref[rows]) and (got[6:15] == 7.0).all()
 
 
+@pytest.mark.parametrize("start", [(2 ** 31 - 1, -2 ** 31), (-5, 3), (9, 6), (6, 20), (1, -1)])
+def test_query_starts_that_do_not_fit_are_skipped_and_recorded(start):
+    # the first pair's difference is 1 in 32 bits
+    t = Tree(64, [90, 200, 40], [6, 9, 4], 8, 2, 64)
+    ref = t.run()
+    qs = t.qs.copy()
+    qs[1:3] = start  # of sequence 1; its neighbours end and begin there
+    t.d["qs"] = dev(qs)
+    t.d["out"].fill_(7.0)
+    t.call()
+    got = t.d["out"].cpu().numpy().astype(np.float64)
+    kind, index = pkv.pkv_get_device_error()
+    assert kind == 3 and index in (0, 1, 2)
+    ok = [i for i in range(3) if 0 <= qs[i] <= qs[i + 1] <= 19
+          and int(qs[i + 1]) - int(qs[i]) <= min(9, t.lens[i])]
+    rows = np.zeros(19, bool)
+    for i in ok:
+        rows[qs[i]:qs[i + 1]] = True
+    assert (got[~rows] == 7.0).all() and np.isfinite(got[rows]).all()
+    if 0 in ok and qs[1] == 6:
+        assert np.array_equal(got[:6], ref[:6])
+
+
 def test_rows_behind_the_last_sequence_stay():
     t = Tree(62, [90, 50], [6, 5], 8, 2, 64)
     ref = t.run()
