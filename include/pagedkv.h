@@ -440,9 +440,10 @@ int pkv_cache_read_fp8(void *k, void *v, const int64_t *slot_mapping, int64_t nu
  * query row r sees every position 0 .. L-Q-1 and drafted token j (position
  * L-Q+j) exactly when bit j % 64 of tree_mask[r*mask_words + j/64] is set
  * (bits at and past Q are ignored; a token sees itself only if its own bit is
- * set).  A row that sees nothing, and a row whose visible scores are all minus
- * infinity, gives zeros.  What a masked position holds -- infinities and NaN
- * included -- does not reach the rows that do not see it.
+ * set).  A row that sees nothing gives zeros, and so does a row whose visible
+ * scores are all minus infinity, where its visible values are finite.  What a
+ * masked position holds -- infinities and NaN included -- does not reach the
+ * rows that do not see it.
  *   tree_mask      device uint64 [num_query_tokens][mask_words], with
  *                  max_query_len <= 64*mask_words
  *   max_query_len  host bound on every Q, at most PKV_MAX_TREE_NODES
@@ -450,7 +451,8 @@ int pkv_cache_read_fp8(void *k, void *v, const int64_t *slot_mapping, int64_t nu
  *                  16-byte aligned; its contents need no preparation and carry nothing from call to
  *                  call.  Calls that share a workspace must not overlap.
  *   other arguments, supported shapes, skipped sequences and blocks as
- *   pkv_chunk_attention.
+ *   pkv_chunk_attention; max_seq_len or the block table's length stays
+ *   below 2^31 - 128 tokens.
  * Ordering: the call may start before an earlier kernel that signals
  * programmatic launch completion has finished, and waits for it before it
  * reads or writes anything.  It signals early itself: a following kernel that
@@ -508,6 +510,9 @@ typedef struct pkv_cache_desc {
  *  descs         HOST array of num_descs (0..PKV_MAX_WRITE_DESCS); read during
  *                the call only.  Quantised caches pass their scales as caches
  *                of their own (row_width 4*num_kv_heads).
+ *                Rows of different descriptors must not overlap in memory; one
+ *                that names a layer of another again is refused
+ *                (PKV_ERR_INVALID).
  *  path          device int32 [num_seqs, max_depth]; its entries before the
  *                first negative one must ascend strictly, and their positions
  *                lie inside the block table: else the sequence is left as it

@@ -1730,6 +1730,9 @@ int tree_attention(void *out, const void *q, const void *k_cache, const void *v_
     if (block_size != kBS || num_seqs > 65535 || max_query_len > PKV_MAX_TREE_NODES ||
         num_blocks > INT32_MAX / kBS || max_blocks_per_seq > INT32_MAX / kBS)
         return PKV_ERR_UNSUPPORTED;
+    // (a step past the last key is a 32-bit position too)
+    if (std::min(max_seq_len, max_blocks_per_seq * kBS) > INT32_MAX - kStepKeys)
+        return PKV_ERR_UNSUPPORTED;
     if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
         !aligned(k_scale, 16) || !aligned(v_scale, 16) || !aligned(block_tables, 4) ||
         !aligned(seq_lens, 4) || !aligned(query_start, 4) || !aligned(tree_mask, 8) ||

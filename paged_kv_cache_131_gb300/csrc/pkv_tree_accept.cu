@@ -150,6 +150,14 @@ extern "C" int pkv_tree_accept(const pkv_cache_desc *descs, int32_t num_descs,
         AcceptDesc &d = p.d[i];
         d.base = static_cast<uint8_t *>(descs[i].cache) + v.offset + v.layer * v.layer_stride;
         d.layer_stride = v.layer_stride;
+        // rows that two descriptors share would move twice
+        const int64_t span = std::max<int64_t>(v.layer_stride, 1) * num_layers;
+        for (int j = 0; j < i; ++j) {
+            const int64_t apart = d.base - p.d[j].base;
+            if (apart == 0 || (p.d[j].layer_stride == v.layer_stride && v.layer_stride > 0 &&
+                               apart < span && -apart < span && apart % v.layer_stride == 0))
+                return PKV_ERR_INVALID;
+        }
         d.block_stride = v.block_stride;
         d.row_width = v.row_width;
         const uintptr_t bits = reinterpret_cast<uintptr_t>(d.base) |

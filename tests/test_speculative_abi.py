@@ -90,6 +90,10 @@ def test_tree_attention(lib, fp8):
     for kw in (dict(H=24), dict(H=128), dict(D=96), dict(bs=32), dict(S=70000),
                dict(maxq=257, words=5)):
         assert call(**kw) == UNSUPPORTED, kw
+    # sequences whose last positions do not fit 32 bits; either bound may be large alone
+    big = (2 ** 31 - 1) // 16
+    assert call(MB=big, maxL=2 ** 31 - 1) == UNSUPPORTED
+    assert call(MB=big) == WORKSPACE and call(maxL=2 ** 31 - 1) == WORKSPACE
     for kw in (dict(q=FAKE + 8), dict(qs=FAKE + 2), dict(mask=FAKE + 4), dict(ws=FAKE + 8)):
         assert call(**kw) == ALIGN, kw
     need = lib.pkv_tree_workspace_bytes(4, 32, 8, 128, 10, 7, 100)
@@ -114,6 +118,27 @@ def test_tree_accept(lib):
         assert call(**{name: None}) == NULL, name
     assert call(n=33) == UNSUPPORTED and call(depth=257) == UNSUPPORTED
     assert call(path=FAKE + 2) == ALIGN
+
+
+def test_tree_accept_refuses_a_layer_named_twice(lib):
+    def call(*descs, layers=1, path=FAKE):
+        arr = (pkv.pkv_cache_desc * len(descs))()
+        for i, (cache, view) in enumerate(descs):
+            arr[i] = pkv.pkv_cache_desc(cache, pkv.pkv_view(*view))
+        return lib.pkv_tree_accept(arr, len(descs), layers, path, 4, FAKE, FAKE, 2, 4, 16, 8, None)
+
+    a = (FAKE, (0, 8192, 1024, 64, 0))
+    assert call(a, a) == INVALID
+    assert call(a, (FAKE, (512, 8192, 1024, 32, 0)), a) == INVALID
+    # the same layer by another offset, or inside the other's run of layers
+    assert call(a, (FAKE - 8192, (0, 8192, 1024, 64, 1))) == INVALID
+    assert call(a, (FAKE, (0, 8192, 1024, 64, 3)), layers=4) == INVALID
+    assert call((FAKE, (0, 8192, 1024, 64, 3)), a, layers=4) == INVALID
+    # neighbours are fine (the last descriptor's rows are too wide for a launch)
+    wide = (FAKE + (1 << 40) + 1, (0, 1 << 40, 1 << 34, 1 << 30, 0))
+    assert call(a, (FAKE, (0, 8192, 1024, 64, 1)), wide) == UNSUPPORTED
+    assert call(a, (FAKE, (0, 8192, 1024, 64, 4)), (FAKE, (512, 8192, 1024, 64, 2)), wide,
+                layers=4) == UNSUPPORTED
 
 
 def test_the_binding_refuses_what_does_not_fit(lib):
