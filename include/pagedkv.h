@@ -447,6 +447,8 @@ int pkv_cache_read_fp8(void *k, void *v, const int64_t *slot_mapping, int64_t nu
  *   tree_mask      device uint64 [num_query_tokens][mask_words], with
  *                  max_query_len <= 64*mask_words
  *   max_query_len  host bound on every Q, at most PKV_MAX_TREE_NODES
+ *   out            may be q itself (each row is read before it is written),
+ *                  and must not overlap the inputs otherwise
  *   workspace      pkv_tree_workspace_bytes(...) bytes of device scratch,
  *                  16-byte aligned; its contents need no preparation and carry nothing from call to
  *                  call.  Calls that share a workspace must not overlap.

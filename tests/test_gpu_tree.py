@@ -307,6 +307,17 @@ def test_query_starts_that_do_not_fit_are_skipped_and_recorded(start):
         assert np.array_equal(got[:6], ref[:6])
 
 
+@pytest.mark.parametrize("fp8", [False, True], ids=["fp16", "fp8"])
+def test_in_place_queries(fp8):
+    # whole items, items split over many CTAs and several tiles
+    t = Tree(65, [90, 6000, 300, 17, 500], [6, 20, 70, 1, 33], 16, 2, 128, fp8=fp8)
+    ref = t.run()
+    for _ in range(5):
+        t.d["q"] = dev(t.q)
+        got = t.call(out=t.d["q"]).cpu().numpy().astype(np.float64)
+        assert np.array_equal(got, ref)
+
+
 def test_rows_behind_the_last_sequence_stay():
     t = Tree(62, [90, 50], [6, 5], 8, 2, 64)
     ref = t.run()
