@@ -95,7 +95,9 @@ constexpr int kItemUnits = 3;
 // merge: threads and rows of a block
 constexpr int kMergeThreads = 256;
 constexpr int kMergeRows = 16;
-constexpr int kMergePieces = 8;  // in flight
+// Partial states in flight per thread: the more of them, the fewer round trips
+// for an item cut into many pieces, but the fewer blocks per SM.
+constexpr int kMergeFew = 4, kMergeMany = 8;
 
 struct TreeParams {
     CUtensorMap tm_k;
@@ -1503,11 +1505,11 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
 // and D/4 / 16 groups of four dims, rows side by side as the states lie; the
 // result is turned round in shared memory for whole rows of output.  Bound:
 // the latency of loads out of L2, so two pieces are asked for before the
-// border is known and kMergePieces at a time after that, the running maximum
-// and sum kept as in the tile kernel (maxima first, then four pieces at a
-// time: 2 us more for one sequence cut into 19 pieces, 1 us for a batch's).
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads)
+// border is known and PIECES at a time after that, the running maximum and sum
+// kept as in the tile kernel (maxima first, then four pieces at a time: 2 us
+// more for one sequence cut into 19 pieces).
+template <int D, int PIECES>
+__global__ void __launch_bounds__(kMergeThreads, PIECES == kMergeFew ? 4 : 2)
     tree_merge_kernel(const __grid_constant__ TreeParams p) {
     constexpr int kGroups = kMergeThreads / kMergeRows;  // threads per row
     constexpr int NQ = D / 4 / kGroups;                  // groups of four dims per thread
@@ -1521,8 +1523,8 @@ __global__ void __launch_bounds__(kMergeThreads)
     const int rl = threadIdx.x % kMergeRows, g = threadIdx.x / kMergeRows;
     const float2 *ml0 = p.part_ml + static_cast<int64_t>(2 * c0) * kRows + row0 + rl;
     const float4 *o0 = p.part_o + (static_cast<int64_t>(2 * c0) * (D / 4) + g) * kRows + row0 + rl;
-    float2 ml[kMergePieces];
-    float4 x[kMergePieces][NQ];
+    float2 ml[PIECES];
+    float4 x[PIECES][NQ];
     auto load = [&](int j, int i) {  // piece i into place j
         const int64_t slot = 2 * i + (i == 0);
         ml[j] = __ldcg(ml0 + slot * kRows);
@@ -1537,7 +1539,7 @@ __global__ void __launch_bounds__(kMergeThreads)
     auto add = [&](int n) {
         float top = M;
 #pragma unroll
-        for (int j = 0; j < kMergePieces; ++j)
+        for (int j = 0; j < PIECES; ++j)
             if (j < n) top = fmaxf(top, ml[j].x);
         // (a piece without a visible finite score weighs nothing, but a NaN in
         // its sum or its O stays)
@@ -1547,7 +1549,7 @@ __global__ void __launch_bounds__(kMergeThreads)
 #pragma unroll
         for (int e = 0; e < 4 * NQ; ++e) o[e] *= f;
 #pragma unroll
-        for (int j = 0; j < kMergePieces; ++j) {
+        for (int j = 0; j < PIECES; ++j) {
             if (j >= n) break;
             const float w = ml[j].x == -INFINITY ? 1.f : ex2(ml[j].x - M);
             den = fmaf(ml[j].y, w, den);
@@ -1569,10 +1571,10 @@ __global__ void __launch_bounds__(kMergeThreads)
     const int G = p.num_heads / p.num_kv_heads, logG = __ffs(G) - 1;
     add(2);
 #pragma unroll 1
-    for (int i = 2; i < b.pieces; i += kMergePieces) {
-        const int n = min(kMergePieces, b.pieces - i);
+    for (int i = 2; i < b.pieces; i += PIECES) {
+        const int n = min(PIECES, b.pieces - i);
 #pragma unroll
-        for (int j = 0; j < kMergePieces; ++j)
+        for (int j = 0; j < PIECES; ++j)
             if (j < n) load(j, i + j);
         add(n);
     }
@@ -1728,7 +1730,15 @@ int launch(TreeParams &p, void *workspace, cudaStream_t stream) {
     cfg.gridDim = dim3(static_cast<unsigned>(ctas - 1), kRows / kMergeRows);
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, static_cast<Fn>(tree_merge_kernel<D>), p);
+    // Fewer items than half the CTAs are cut into many pieces (one sequence of
+    // 1041 tokens: few in flight 10.7 us, many 10.3; 60000 tokens of one KV head
+    // 29 and 27); otherwise into two or three (32 x 63 nodes of groups of 8:
+    // 132 and 134; 64 ragged sequences 99.2 and 100.2).
+    const int64_t items = static_cast<int64_t>(p.num_seqs) * Hk * p.max_tiles;
+    e = cudaLaunchKernelEx(&cfg,
+                           2 * items < ctas ? static_cast<Fn>(tree_merge_kernel<D, kMergeMany>)
+                                            : static_cast<Fn>(tree_merge_kernel<D, kMergeFew>),
+                           p);
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? PKV_OK : cuda_failure(e, "tree_merge_kernel launch");
 }
