@@ -77,12 +77,11 @@ constexpr int kSoftmaxWarps = 8;
 constexpr int kHalfKeys = kStepKeys / 2;
 constexpr int kConvertWarp = kSoftmaxWarp + kSoftmaxWarps;
 constexpr int kConvertWarps = 4;
-// tensor memory: O in columns [0, head_dim), two score buffers of 128 columns,
-// two weight buffers (fp16 pairs) of 64
+// tensor memory: O in columns [0, head_dim), two score buffers of 128 columns
+// (and what Geo says)
 constexpr int kTmemCols = 512;
 constexpr int kTmemO = 0;
 constexpr int kTmemS = 128;
-constexpr int kTmemP = 384;
 constexpr float kRescaleLog2 = 8.f;  // move the reference past 2^8
 constexpr int kFlagWords = PKV_MAX_TREE_NODES / 32;
 constexpr int kFlagRing = 4;   // pieces whose flags are kept (see the softmax)
@@ -155,6 +154,19 @@ struct Piece : PieceHead {
 template <int D, bool FP8>
 struct Geo {
     static constexpr int kThreads = (kConvertWarp + (FP8 ? kConvertWarps : 0)) * 32;
+    // Where shared memory's bandwidth counts (FP8: the codes are read and the
+    // tiles written there too, 2400 cycles of it for 128 keys), or tensor memory
+    // has the columns, the query tile is copied to tensor memory once and the
+    // score MMAs read the keys alone from shared memory.  FP8 with 128 dims
+    // gives one of the two weight buffers (64 columns of fp16 pairs each) for
+    // it.  (FP8, 16 x 8000..32768 tokens: 186.6 -> 183.8 us, 64 ragged ones 99.0
+    // -> 97.3; 64 dims 37.9 -> 37.7, FP8 47.5 -> 47.1.  fp16 with 128 dims and
+    // one weight buffer: 131 -> 148.)
+    static constexpr bool kQTmem = FP8 || D == 64;
+    static constexpr int kTmemQ = D == 64 ? 64 : 384;
+    static constexpr int kPBuffers = kQTmem && D == 128 ? 1 : 2;
+    static constexpr int kTmemP = kPBuffers == 1 ? 448 : 384;
+    static constexpr int kPApart = 64 * (kPBuffers - 1);
     static constexpr int kChunks = D / 64;                // 128-byte chunks of a head row
     static constexpr int kQ = kChunks * kRows * 128;      // [chunk][row][128 B]
     // fp16 tiles, as the MMAs read them: keys [8 rows][chunk][row][128 B],
@@ -991,7 +1003,8 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(br.piece_empty(rec));
                 if (pc.done) break;
-                // the query tile, once the previous piece's last scores are done
+                // the query tile, once the previous piece's last scores are done, or
+                // it is in tensor memory
                 if (it >= 1) ok = wait_all(br.q_empty(), (it - 1) & 1);
                 if (!ok) break;
                 if (lane == 0)
@@ -1008,6 +1021,22 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                 }
                 q_staged = it + 1;
                 ok = wait_all(br.q_full(), it & 1);
+                if constexpr (Gm::kQTmem) {
+                    // (the previous piece's last scores are done with the last one)
+                    if (ok && gs >= 1) ok = wait_all(br.s_full((gs - 1) & 1), ((gs - 1) >> 1) & 1);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    if (lane == 0) {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            tc::cp_128x256b(tmem + Gm::kTmemQ + 8 * kk,
+                                            tc::smem_desc(sb + (kk >> 2) * (kRows * 128) +
+                                                              (kk & 3) * 32,
+                                                          16, 1024, tc::kSwizzle128B));
+                        tc::commit(br.q_empty());
+                    }
+                    __syncwarp();
+                }
 #pragma unroll 1
                 for (int n = 0; n < pc.nsteps && ok; ++n, ++gs) {
                     const int ks = gs % KS, b = gs & 1;
@@ -1025,17 +1054,24 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                         const uint32_t k_s =
                             sb + (FP8 ? Gm::kOffK16 : Gm::kOffK + ks * Gm::kStage);
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk)
-                            tc::mma_ss(tmem + kTmemS + 128 * b,
-                                       tc::smem_desc(sb + (kk >> 2) * (kRows * 128) + (kk & 3) * 32,
-                                                     16, 1024, tc::kSwizzle128B),
-                                       tc::smem_desc(k_s + (kk >> 2) * 1024 + (kk & 3) * 32, 16,
-                                                     CH * 1024, tc::kSwizzle128B),
-                                       idesc, kk > 0);
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint64_t k_desc =
+                                tc::smem_desc(k_s + (kk >> 2) * 1024 + (kk & 3) * 32, 16, CH * 1024,
+                                              tc::kSwizzle128B);
+                            if constexpr (Gm::kQTmem)
+                                tc::mma_ts(tmem + kTmemS + 128 * b, tmem + Gm::kTmemQ + 8 * kk,
+                                           k_desc, idesc, kk > 0);
+                            else
+                                tc::mma_ss(tmem + kTmemS + 128 * b,
+                                           tc::smem_desc(sb + (kk >> 2) * (kRows * 128) +
+                                                             (kk & 3) * 32,
+                                                         16, 1024, tc::kSwizzle128B),
+                                           k_desc, idesc, kk > 0);
+                        }
                         tc::commit(br.s_full(b));
                         mbar_arrive(br.s_full(b));  // passes the step's validity and scales on
                         if (!FP8) tc::commit(br.k_empty(ks));
-                        if (n == pc.nsteps - 1) tc::commit(br.q_empty());
+                        if (!Gm::kQTmem && n == pc.nsteps - 1) tc::commit(br.q_empty());
                     }
                     __syncwarp();
                 }
@@ -1092,7 +1128,7 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                             sb + (FP8 ? Gm::kOffV16 + b * Gm::kV : Gm::kOffV + vs * Gm::kStage);
 #pragma unroll 1
                         for (int k = 0; k < nb; ++k)
-                            tc::mma_ts(tmem + kTmemO, tmem + kTmemP + 64 * b + 8 * k,
+                            tc::mma_ts(tmem + kTmemO, tmem + Gm::kTmemP + Gm::kPApart * b + 8 * k,
                                        tc::smem_desc(v_s + k * Gm::kVBlock, kBS * 128, 1024,
                                                      tc::kSwizzle128B),
                                        kIdescPV, (n > 0 || k > 0) ? 1u : 0u);
@@ -1380,10 +1416,11 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                 }
                 if (raise) m_used = m_new;
                 const float ms = m_used == -INFINITY ? 0.f : m_used;
-                // weights 2^(s - m), fp16 pairs; the P V of two steps back is
-                // done with this buffer
-                if (gs >= 2) {
-                    if (!wait_all(br.pv_done(sbuf), ((gs >> 1) - 1) & 1)) {
+                // weights 2^(s - m), fp16 pairs; the P V of as many steps back as
+                // there are buffers is done with this one
+                if (gs >= Gm::kPBuffers) {
+                    const int last = gs - Gm::kPBuffers;
+                    if (!wait_all(br.pv_done(last & 1), (last >> 1) & 1)) {
                         ok = false;
                         break;
                     }
@@ -1408,7 +1445,7 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                     }
                     x[e] = pack_half2(p0, p1);
                 }
-                tc::st32_halves<32>(tl + kTmemP + 64 * sbuf, x);
+                tc::st32_halves<32>(tl + Gm::kTmemP + Gm::kPApart * sbuf, x);
                 const float2 la =
                     f32x2_split(add_f32x2(add_f32x2(l2[0], l2[1]), add_f32x2(l2[2], l2[3])));
                 l += la.x + la.y;
