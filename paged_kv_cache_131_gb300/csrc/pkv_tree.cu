@@ -27,8 +27,8 @@
 //  * warps 4-11, two threads per row: the softmax.  The reference m moves only
 //    when the maximum grows by more than 2^8 (weights stay <= 256, O is
 //    rescaled in tensor memory first); weights are rounded to fp16 for the MMA
-//    (the normaliser sums them unrounded: the rounding errors are independent
-//    and at most 2^-12 of a weight's step each), with the tree's mask;
+//    (an error of at most 2^-11 of a weight; the normaliser sums them as they
+//    were, in 32 bits), with the tree's mask;
 //  * FP8: the rings hold codes, and warps 12-15 turn them into fp16 tiles
 //    (exact) for the MMAs.  A key's scale multiplies its score and its value's
 //    scale the weight, both in fp32; m is then the largest visible log2 of
@@ -381,7 +381,7 @@ struct SeqGeo {
 
 // Up to 64 rows are laid out as four groups of 16, one in each quarter of the
 // tile, so that every quarter of the SM has one softmax warp at work instead of
-// half of them two (FP8, 64 rows, 16 x 8000..32768 tokens: 208 -> 198 us).
+// half of them two (FP8, 64 rows, 16 x 8000..32768 tokens: 208 -> 198 us then).
 __device__ __forceinline__ bool spread_rows(int rows) { return rows <= kRows / 2; }
 
 __device__ __forceinline__ SeqGeo make_geo(int L, int Q, int q0, int G) {
