@@ -443,7 +443,11 @@ int pkv_cache_read_fp8(void *k, void *v, const int64_t *slot_mapping, int64_t nu
  * set).  A row that sees nothing gives zeros, and so does a row whose visible
  * scores are all minus infinity, where its visible values are finite.  What a
  * masked position holds -- infinities and NaN included -- does not reach the
- * rows that do not see it.
+ * rows that do not see it.  Scores, maxima, sums and outputs are fp32; the
+ * softmax weights (FP8: times their value's scale) are rounded to fp16 for the
+ * product with the values, each by 2^-11 of itself or, where that is more, by
+ * 2^-36 of the row's largest one; the sum they are divided by holds them as
+ * they were.
  *   tree_mask      device uint64 [num_query_tokens][mask_words], with
  *                  max_query_len <= 64*mask_words
  *   max_query_len  host bound on every Q, at most PKV_MAX_TREE_NODES

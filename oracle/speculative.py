@@ -84,8 +84,10 @@ def tree_tolerance(ref, t, head_dim):
     """Largest |got - ref| of fp32 arithmetic with fp16 weights and outputs.
 
     Output rounding: half a step, 2^-11 |ref|, or 2^-25 below the normal range.
-    Weights rounded to fp16: 2^-11 relative each (A 2^-11), or 2^-25 of the
-    largest weight when subnormal, against a normaliser of unrounded weights.
+    Weights rounded to fp16: 2^-11 relative each (A 2^-11), or, when subnormal,
+    2^-25 where the row's largest weight is 2^11 or more: 2^-36 of it, and less
+    than 2^-35 with the reference's own rounding; against a normaliser of
+    unrounded weights.
     Scores: a sum of head_dim products in fp32, (head_dim + 4) 2^-24 of
     sum |q||k|, and 4 2^-24 for the scaling, the subtraction of the maximum and
     the exponential's argument; an error d of a score moves its weight by d
@@ -95,7 +97,7 @@ def tree_tolerance(ref, t, head_dim):
     d = (head_dim + 8) * 2.0 ** -24 * t["smax"]
     rel = 2.0 ** -11 + 2 * d + 2.0 ** -20 + (t["nvis"] / 16 + 64) * 2.0 ** -23
     return (np.abs(ref) * 2.0 ** -11 + 2.0 ** -25 + rel * t["A"] +
-            t["nvis"] * 2.0 ** -25 * t["vmax"] / t["sumw"])
+            t["nvis"] * 2.0 ** -35 * t["vmax"] / t["sumw"])
 
 
 def tree_accept(rows, path, ctx_lens, block_tables, block_size):

@@ -24,11 +24,14 @@
 //  * warp 2 stages a piece's query tile and issues S = Q K^T into one of two
 //    score buffers, so the scores of the next step are computed while the
 //    softmax works on this one; warp 3 issues O += P V;
-//  * warps 4-11, two threads per row: the softmax.  The reference m moves only
-//    when the maximum grows by more than 2^8 (weights stay <= 256, O is
-//    rescaled in tensor memory first); weights are rounded to fp16 for the MMA
-//    (an error of at most 2^-11 of a weight; the normaliser sums them as they
-//    were, in 32 bits), with the tree's mask;
+//  * warps 4-11, two threads per row: the softmax, with the tree's mask.
+//    Weights are rounded to fp16 for the MMA, the normaliser sums them as they
+//    were, in 32 bits.  The reference m is set 2^11 below the largest score and
+//    moves only when that grows by more than 2^4 (O is rescaled in tensor memory
+//    first), so the row's largest weight lies in [2^11, 2^15] and uses fp16's
+//    range: rounding costs a weight 2^-11 of itself where it is above 2^-25 of
+//    the row's largest one, and 2^-36 of the largest below that, which many
+//    keys of little weight behind one of large weight would add up;
 //  * FP8: the rings hold codes, and warps 12-15 turn them into fp16 tiles
 //    (exact) for the MMAs.  A key's scale multiplies its score and its value's
 //    scale the weight, both in fp32; m is then the largest visible log2 of
@@ -82,7 +85,13 @@ constexpr int kConvertWarps = 4;
 constexpr int kTmemCols = 512;
 constexpr int kTmemO = 0;
 constexpr int kTmemS = 128;
-constexpr float kRescaleLog2 = 8.f;  // move the reference past 2^8
+// The largest weight where the reference is set, and the largest that it stays
+// for (fp16 ends below 2^16).  The higher it is set, the less is lost at the low
+// end and the sooner it moves: set at 0 (staying up to 8), 7, 11 and 13, 32
+// sequences of 63 nodes with groups of 8 take 131.2, 130.9, 130.8 and 149.2 us,
+// FP8 with 16 x 8000..32768 tokens 184.0, 182.2, 182.0 and 183.9.
+constexpr float kSetLog2 = 11.f;
+constexpr float kTopLog2 = 15.f;
 constexpr int kFlagWords = PKV_MAX_TREE_NODES / 32;
 constexpr int kFlagRing = 4;   // pieces whose flags are kept (see the softmax)
 constexpr int kValidRing = 8;  // steps whose blocks' validity is kept (see the softmax)
@@ -294,11 +303,11 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// log2 of a value scale's size as the reference counts it: no less than -100 (a
-// weight relative to the reference stays finite) and no more than 121 (it stays
-// normal, and the scaled one, at most 2^8 2^7, finite in fp16).
+// log2 of a value scale's size as the reference counts it: no less than -40 (448
+// times a smaller one is nothing in fp16, and a weight, at most 2^15 2^40, can be
+// summed in fp32) and up to 128 (a weight of 2^11 2^-128 is still normal).
 __device__ __forceinline__ float scale_log2(float vs) {
-    return fminf(__log2f(fmaxf(fabsf(vs), 0x1p-100f)), 121.f);
+    return __log2f(fmaxf(fabsf(vs), 0x1p-40f));
 }
 
 // Packed fp32 pairs (one instruction for two lanes' worth of fma, mul or add)
@@ -316,6 +325,11 @@ __device__ __forceinline__ float2 f32x2_split(uint64_t r) {
 __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t d;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma_ru_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rp.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
 __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
@@ -1362,8 +1376,10 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                                        fmaxf(mr[6], mr[7]));
                 // the row's other half: the thread 16 lanes away
                 const float mo = __shfl_xor_sync(0xffffffffu, mx, 16);
-                float m_new = fmaxf(m_used, fmaf(fmaxf(mx, mo), sl2, top2));
-                bool raise = m_new > m_used + kRescaleLog2;
+                // (rounded up, and the bound down: no weight passes 2^15)
+                float m_new = __fmaf_ru(fmaxf(mx, mo), sl2, top2);
+                const float bound = __fadd_rd(m_used, kTopLog2);
+                bool raise = m_new > bound;
                 if constexpr (FP8) {
                     // the largest scale need not be at a key that the row sees,
                     // nor at one with weight: the largest product itself
@@ -1375,9 +1391,9 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                             const float4 lv =
                                 *reinterpret_cast<const float4 *>(sc + 2 * kStepKeys + e);
                             const float2 a = f32x2_split(
-                                fma_f32x2(f32x2(__uint_as_float(sx[e]), __uint_as_float(sx[e + 1])),
-                                          s2, f32x2(lv.x, lv.y)));
-                            const float2 b = f32x2_split(fma_f32x2(
+                                fma_ru_f32x2(f32x2(__uint_as_float(sx[e]), __uint_as_float(sx[e + 1])),
+                                             s2, f32x2(lv.x, lv.y)));
+                            const float2 b = f32x2_split(fma_ru_f32x2(
                                 f32x2(__uint_as_float(sx[e + 2]), __uint_as_float(sx[e + 3])), s2,
                                 f32x2(lv.z, lv.w)));
                             ex = fmax3(ex, a.x, a.y);
@@ -1385,13 +1401,14 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                         }
                         ex = fmaxf(ex, ey);
                         ex = fmaxf(ex, __shfl_xor_sync(0xffffffffu, ex, 16));
-                        m_new = fmaxf(m_used, ex);
-                        raise = m_new > m_used + kRescaleLog2;
+                        m_new = ex;
+                        raise = m_new > bound;
                     }
                 }
                 // O holds this piece's earlier steps relative to m_used: rescale
                 // this thread's columns before the reference moves (the
                 // previous P V done first)
+                m_new = __fsub_ru(m_new, kSetLog2);
                 const bool resc = raise && n > 0 && m_used != -INFINITY;
                 if (__any_sync(0xffffffffu, resc)) {
                     if (!wait_all(br.pv_done((gs - 1) & 1), ((gs - 1) >> 1) & 1)) {
