@@ -33,8 +33,8 @@
 //    the row's largest one, and 2^-36 of the largest below that, which many
 //    keys of little weight behind one of large weight would add up;
 //  * FP8: the rings hold codes, and warps 12-15 turn them into fp16 tiles
-//    (exact) for the MMAs.  A key's scale multiplies its score and its value's
-//    scale the weight, both in fp32; m is then the largest visible log2 of
+//    (exact) for the MMAs.  A key's scale, times scale log2(e), multiplies its
+//    score and its value's scale the weight, both in fp32; m is then the largest visible log2 of
 //    their product, so the scaled weights use fp16's range whatever the scales
 //    are.  (A step's largest score plus its largest scale's logarithm is an
 //    upper bound; the maximum itself is taken when that passes the reference.)
@@ -123,7 +123,7 @@ struct TreeParams {
     const int32_t *query_start;
     const uint64_t *mask;
     int32_t mask_words;
-    float scale_log2;     // |scale| log2(e), > 0
+    float scale_log2;     // |scale| log2(e), > 0: scores times this are in log2 units
     int32_t negate;       // the scale is negative: the MMA negates the scores
     int32_t num_heads;
     int32_t num_kv_heads;
@@ -321,16 +321,6 @@ __device__ __forceinline__ float2 f32x2_split(uint64_t r) {
     float2 v;
     asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
     return v;
-}
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t fma_ru_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rp.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
 }
 __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
     uint64_t d;
@@ -1200,7 +1190,7 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                     const int ring = gs % kScaleRing;
                     // (the dot product with a key of infinities is NaN, but its
                     // dot product with the codes times infinity need not be)
-                    scales[ring * 3 * kStepKeys + tid] = isfinite(ks) ? ks : NAN;
+                    scales[ring * 3 * kStepKeys + tid] = isfinite(ks) ? ks * p.scale_log2 : NAN;
                     // (a drafted row's scale that is not finite counts as its
                     // non-finite elements do: left out here, added at the end)
                     const bool out = !isfinite(vs) && tid + key0 >= ctx;
@@ -1254,7 +1244,6 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
         const int quarter = warp & 3;
         const int h = lane >> 4;
         const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32 + wh * 16) << 16);
-        const float sl2 = p.scale_log2;
         int gs = 0;
 #pragma unroll 1
         for (int it = 0; ok; ++it) {
@@ -1355,6 +1344,23 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                         sx[e + 3] = __float_as_uint(b.y);
                     }
                 }
+                // to log2 units, rounded before anything is subtracted: a reference
+                // made from a rounded score differs from it exactly, where one that
+                // is rounded on its own is off by up to 2^12 at scores of 2^36, more
+                // than the weights' range (with the subtraction in one fma instead,
+                // which outputs zeros from 2^28 on: 32 x 63 nodes 130.5 against
+                // 130.6 us, 128 x 300 tokens 40.2 and 41.0, 64 dims 37.6 and 38.4;
+                // FP8, where the key's scale holds the factor, 182.4 and 184.1)
+                if constexpr (!FP8) {
+                    const uint64_t f2 = f32x2(p.scale_log2, p.scale_log2);
+#pragma unroll
+                    for (int e = 0; e < kHalfKeys; e += 2) {
+                        const float2 a = f32x2_split(mul_f32x2(
+                            f32x2(__uint_as_float(sx[e]), __uint_as_float(sx[e + 1])), f2));
+                        sx[e] = __float_as_uint(a.x);
+                        sx[e + 1] = __float_as_uint(a.y);
+                    }
+                }
                 const bool masked = tail || blocks != 0xffffffffu;
                 if (masked) {
 #pragma unroll
@@ -1376,25 +1382,24 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                                        fmaxf(mr[6], mr[7]));
                 // the row's other half: the thread 16 lanes away
                 const float mo = __shfl_xor_sync(0xffffffffu, mx, 16);
-                // (rounded up, and the bound down: no weight passes 2^15)
-                float m_new = __fmaf_ru(fmaxf(mx, mo), sl2, top2);
+                float m_new = fmaxf(mx, mo) + top2;
+                // (rounded down, and the reference up: fp16 holds every weight)
                 const float bound = __fadd_rd(m_used, kTopLog2);
                 bool raise = m_new > bound;
                 if constexpr (FP8) {
                     // the largest scale need not be at a key that the row sees,
                     // nor at one with weight: the largest product itself
                     if (__any_sync(0xffffffffu, raise)) {
-                        const uint64_t s2 = f32x2(sl2, sl2);
                         float ex = -INFINITY, ey = -INFINITY;
 #pragma unroll
                         for (int e = 0; e < kHalfKeys; e += 4) {
                             const float4 lv =
                                 *reinterpret_cast<const float4 *>(sc + 2 * kStepKeys + e);
                             const float2 a = f32x2_split(
-                                fma_ru_f32x2(f32x2(__uint_as_float(sx[e]), __uint_as_float(sx[e + 1])),
-                                             s2, f32x2(lv.x, lv.y)));
-                            const float2 b = f32x2_split(fma_ru_f32x2(
-                                f32x2(__uint_as_float(sx[e + 2]), __uint_as_float(sx[e + 3])), s2,
+                                add_f32x2(f32x2(__uint_as_float(sx[e]), __uint_as_float(sx[e + 1])),
+                                          f32x2(lv.x, lv.y)));
+                            const float2 b = f32x2_split(add_f32x2(
+                                f32x2(__uint_as_float(sx[e + 2]), __uint_as_float(sx[e + 3])),
                                 f32x2(lv.z, lv.w)));
                             ex = fmax3(ex, a.x, a.y);
                             ey = fmax3(ey, b.x, b.y);
@@ -1443,14 +1448,14 @@ __global__ void __launch_bounds__(Geo<D, FP8>::kThreads, 1)
                     }
                     tc::fence_after_sync();
                 }
-                const uint64_t a2 = f32x2(sl2, sl2), nms2 = f32x2(-ms, -ms);
+                const uint64_t nms2 = f32x2(-ms, -ms);
                 uint64_t l2[4] = {0ull, 0ull, 0ull, 0ull};
                 uint32_t x[32];
                 float4 v4;  // FP8: the value scales of four keys
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
-                    const float2 t = f32x2_split(fma_f32x2(
-                        f32x2(__uint_as_float(sx[2 * e]), __uint_as_float(sx[2 * e + 1])), a2, nms2));
+                    const float2 t = f32x2_split(add_f32x2(
+                        f32x2(__uint_as_float(sx[2 * e]), __uint_as_float(sx[2 * e + 1])), nms2));
                     float p0 = ex2(t.x), p1 = ex2(t.y);
                     l2[e & 3] = add_f32x2(l2[e & 3], f32x2(p0, p1));
                     if constexpr (FP8) {

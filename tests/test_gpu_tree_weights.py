@@ -158,3 +158,38 @@ def test_fp8_value_scales_at_the_types_ends():
     tol = (np.abs(ref) * 2.0 ** -11 + 2.0 ** -25 + (2.0 ** -11 + 2.0 ** -13) * terms["A"] +
            terms["nvis"] * 2.0 ** -35 * 2.25 / terms["sumw"] + 2.0 ** -13 * np.abs(ref))
     assert (np.abs(got - ref) <= tol).all(), np.max(np.abs(got - ref) / tol)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["fp16", "fp8"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("size", [200, 1000, 2000, 8000, 30000, 60000, -8000])
+def test_scores_of_every_size(size, D, fp8):
+    """Scores up to 2^36 in units of log2, far apart from each other: the largest
+    one a row sees takes all the weight, and its value is the output.
+
+    Keys are multiples c of one +-1 vector, c spread evenly over [-size, size] (in
+    fp16, whose step is a tenth of their distance at most): neighbours among n
+    keys are 2/n of the largest score apart, 2^-10 and more, where 32-bit sums are
+    off by D 2^-24 of it, 2^-17.  The smallest distance is 2^-10 2^19 units: the
+    runner-up's weight is nothing."""
+    t = Tree(12, [300, 40, 1900], [20, 9, 3], 8, 2, D, fp8=fp8,
+             scale=np.sign(size) * D ** -0.5)
+    a = abs(size)
+    rng = np.random.default_rng(13)
+    u = rng.choice([-1, 1], D)
+    t.q[:] = a * u * rng.choice([-1, 1], t.q.shape[:2])[..., None]
+    for i, n in enumerate(t.lens):
+        p = np.arange(n)
+        b, o = t.tables[i, p // BS], p % BS
+        for h in range(2):
+            c = rng.permutation(np.linspace(-a, a, n))
+            if fp8:
+                t.parts[0][b, o, h] = np.where(u > 0, 0x7E, 0xFE)  # 448, -448
+                t.parts[1][b, o, h] = c / 448
+            else:
+                t.parts[0][b, o, h] = c[:, None] * u
+    got = t.run()
+    ref, terms = t.want()
+    assert (terms["sumw"] < 1 + 1e-6).all()
+    tol = np.abs(ref) * 2.0 ** -9 + 2.0 ** -24  # value, weight, quotient, output
+    assert (np.abs(got - ref) <= tol).all(), (np.isnan(got).sum(), (got == 0).sum(), got.size)
