@@ -565,14 +565,26 @@ def pkv_tree_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: int, h
                                                num_query_tokens, max_query_len, max_seq_len))
 
 
+def _view_inside(cache, view, num_layers, block_size, num_blocks, name):
+    """Refuses a view whose last row (of num_layers layers from view.layer on) lies
+    past the end of the tensor ``cache``."""
+    end = (view.offset + (view.layer + num_layers - 1) * view.layer_stride +
+           (num_blocks - 1) * view.block_stride + block_size * view.row_width)
+    if end > cache.nbytes:
+        raise ValueError(f"{name}: the view's rows end at byte {end}, past the end of its tensor "
+                         f"({cache.nbytes} bytes)")
+
+
 def pkv_tree_accept(caches, num_layers: int, path, ctx_lens, block_tables, block_size: int,
                     num_blocks: int, stream=None, check: bool = True) -> int:
     """Move the cache rows of each sequence's accepted path to their positions: see
     pkv_tree_accept in pagedkv.h.
 
-    caches: sequence of (cache, view) with a CUDA tensor and a pkv_view-like view;
-    path: CUDA int32 [S, max_depth], negative past a path's end; ctx_lens: CUDA
-    int32 [S]; block_tables: CUDA int32 [S, MB].
+    caches: sequence of (cache, view) with a CUDA tensor, used as bytes, and a
+    pkv_view-like view, whose rows -- num_layers layers from view.layer on, num_blocks
+    blocks each -- lie inside the tensor (ValueError otherwise); path: CUDA int32
+    [S, max_depth], negative past a path's end; ctx_lens: CUDA int32 [S];
+    block_tables: CUDA int32 [S, MB].
     """
     import torch
     i32 = torch.int32
@@ -584,7 +596,9 @@ def pkv_tree_accept(caches, num_layers: int, path, ctx_lens, block_tables, block
     arr = (pkv_cache_desc * max(1, len(caches)))()
     for i, (cache, view) in enumerate(caches):
         arr[i].cache = _arg(cache, f"caches[{i}]", cache.dtype, cache.shape, dev)
-        arr[i].view = _as_view(view)
+        view = arr[i].view = _as_view(view)
+        if S and depth and num_layers:
+            _view_inside(cache, view, num_layers, block_size, num_blocks, f"caches[{i}]")
     st = load().pkv_tree_accept(
         arr, len(caches), num_layers, _arg(path, "path", i32, (S, depth), dev), depth,
         _arg(ctx_lens, "ctx_lens", i32, (S,), dev),
