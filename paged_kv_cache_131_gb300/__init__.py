@@ -439,6 +439,8 @@ def _norm_rope_write(name, q_out, q, k, v, positions, slot_mapping, k_cache, v_c
         None if k_weight is None else _arg(k_weight, "k_weight", f16, (D,), dev),
         eps, table, max_pos, rot, bool(interleaved))
     kind = f16 if scales is None else torch.uint8
+    if num_blocks is None:
+        num_blocks = k_cache.shape[0]
     rows = (num_blocks, block_size, Hk, D)
     args = [_arg(q_out, "q_out", f16, (T, H, D), dev), qp, kp, vp, qs, ks, vs, ctypes.byref(nr),
             pos, _arg(slot_mapping, "slot_mapping", i64, (T,), dev), T,
@@ -452,15 +454,16 @@ def _norm_rope_write(name, q_out, q, k, v, positions, slot_mapping, k_cache, v_c
 
 def pkv_norm_rope_write(q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, cos_sin=None,
                         q_weight=None, k_weight=None, eps: float = 1e-6,
-                        interleaved: bool = False, block_size: int = 16, num_blocks: int = 0,
-                        stream=None, check: bool = True) -> int:
+                        interleaved: bool = False, block_size: int = 16,
+                        num_blocks: int | None = None, stream=None, check: bool = True) -> int:
     """Per-head norm, rotation and cache write in one pass: see pkv_norm_rope_write
     in pagedkv.h.
 
     q [T, H, D], k, v [T, Hk, D]: CUDA fp16, tokens may be strided; q_out: CUDA
     fp16 [T, H, D]; positions, slot_mapping: CUDA int64 [T]; caches: CUDA fp16
     [NB, bs, Hk, D]; cos_sin: CUDA fp32 [max_position, rot_dim] or None;
-    q_weight, k_weight: CUDA fp16 [D] or None.
+    q_weight, k_weight: CUDA fp16 [D] or None; num_blocks: the caches' NB when not
+    given.
     """
     return _norm_rope_write("pkv_norm_rope_write", q_out, q, k, v, positions, slot_mapping,
                             k_cache, v_cache, None, cos_sin, q_weight, k_weight, eps, interleaved,
@@ -470,7 +473,7 @@ def pkv_norm_rope_write(q_out, q, k, v, positions, slot_mapping, k_cache, v_cach
 def pkv_norm_rope_write_fp8(q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, k_scale,
                             v_scale, cos_sin=None, q_weight=None, k_weight=None,
                             eps: float = 1e-6, interleaved: bool = False, block_size: int = 16,
-                            num_blocks: int = 0, stream=None, check: bool = True) -> int:
+                            num_blocks: int | None = None, stream=None, check: bool = True) -> int:
     """pkv_norm_rope_write into E4M3 caches (uint8 [NB, bs, Hk, D]) and fp32 scales
     [NB, bs, Hk]: see pagedkv.h."""
     return _norm_rope_write("pkv_norm_rope_write_fp8", q_out, q, k, v, positions, slot_mapping,
