@@ -96,9 +96,10 @@ constexpr int kFlagWords = PKV_MAX_TREE_NODES / 32;
 constexpr int kFlagRing = 4;   // pieces whose flags are kept (see the softmax)
 constexpr int kValidRing = 8;  // steps whose blocks' validity is kept (see the softmax)
 constexpr int kScaleRing = 3;  // steps whose scales are kept (see the converters)
-// Units of an item: its steps and kItemUnits for its start-up (1, 2, 3, 4: 104.4,
-// 101.8, 101.2, 101.2 us for 64 ragged sequences of 16 nodes; 150.5, 145.2,
-// 141.4, 139.8 for 32 of 63 nodes with groups of 8).
+// Units of an item: its steps and kItemUnits for its start-up.  2, 3, 4, 5: 32
+// sequences of 63 nodes with groups of 8 take 135.2, 131.5, 131.3, 132.9 us, over
+// FP8 caches 191.4, 193.6, 197.0, 201.4; 64 ragged sequences of 16 nodes 100.1,
+// 99.4, 99.7, 99.7, over FP8 caches 96.3, 97.3, 98.7, 99.9.
 constexpr int kItemUnits = 3;
 // merge: threads and rows of a block
 constexpr int kMergeThreads = 256;
@@ -164,7 +165,7 @@ template <int D, bool FP8>
 struct Geo {
     static constexpr int kThreads = (kConvertWarp + (FP8 ? kConvertWarps : 0)) * 32;
     // Where shared memory's bandwidth counts (FP8: the codes are read and the
-    // tiles written there too, 2400 cycles of it for 128 keys), or tensor memory
+    // tiles written there too, 2030 cycles of a 128-key step's 2790), or tensor memory
     // has the columns, the query tile is copied to tensor memory once and the
     // score MMAs read the keys alone from shared memory.  FP8 with 128 dims
     // gives one of the two weight buffers (64 columns of fp16 pairs each) for
@@ -172,7 +173,7 @@ struct Geo {
     // -> 97.3; 64 dims 37.9 -> 37.7, FP8 47.5 -> 47.1.  fp16 with 128 dims and
     // one weight buffer: 131 -> 148.)
     static constexpr bool kQTmem = FP8 || D == 64;
-    static constexpr int kTmemQ = D == 64 ? 64 : 384;
+    [[maybe_unused]] static constexpr int kTmemQ = D == 64 ? 64 : 384;
     static constexpr int kPBuffers = kQTmem && D == 128 ? 1 : 2;
     static constexpr int kTmemP = kPBuffers == 1 ? 448 : 384;
     static constexpr int kPApart = 64 * (kPBuffers - 1);
