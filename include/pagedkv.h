@@ -50,8 +50,12 @@ typedef enum pkv_device_error {
                                 max_seq_len allow; index = seq                         */
     PKV_DEVERR_TIMEOUT = 4,  /* a staging wait gave up (about 2 s); index = CTA id   */
     PKV_DEVERR_POSITION = 5, /* position outside [0, max_position); index = token    */
-    PKV_DEVERR_PATH = 6      /* accepted path not ascending or past the block table;
+    PKV_DEVERR_PATH = 6,     /* accepted path not ascending or past the block table;
                                 index = seq                                           */
+    PKV_DEVERR_FREE_LIST = 7, /* the free list's count outside [0, capacity], or more
+                                blocks given back than it has room for; index = count */
+    PKV_DEVERR_TREE = 8      /* drafted token outside the vocabulary, or a parent that
+                                does not come before its node; index = node's row     */
 } pkv_device_error;
 
 /*
@@ -345,6 +349,140 @@ size_t pkv_chunk_workspace_bytes(int32_t num_seqs, int32_t num_heads, int32_t nu
                                  int32_t max_query_len, int32_t max_seq_len);
 
 /* ------------------------------------------------------------------------
+ * Attention whose scores follow rules of the model: capped, biased by distance,
+ * limited to a window, with a prefix that every token sees. */
+
+/*
+ * With s = scale * q . k of a token at position a and a key at position b:
+ *     s' = softcap * tanh(s / softcap)              if softcap > 0
+ *     s'' = s' - slopes[h] * |a - b|                for query head h, if slopes
+ * and the token sees the key if b <= a and (window > 0) a - b < window, or if
+ * b < prefix_lens[i] (of sequence i; later positions than its own included, up
+ * to the sequence's length).
+ */
+typedef struct pkv_score_rules {
+    float softcap;              /* >= 0, finite; 0: not capped                    */
+    int32_t window;             /* >= 0; 0: every earlier position                */
+    const float *slopes;        /* device fp32 [num_heads], or NULL: no bias      */
+    const int32_t *prefix_lens; /* device int32 [num_seqs], or NULL: no prefix;
+                                   negative counts as 0                           */
+} pkv_score_rules;
+
+/*
+ * pkv_decode_attention under score rules: each sequence's one query token is at
+ * position L - 1.  Blocks that no rule lets the token see are not read.  Scores,
+ * maxima, sums and outputs are fp32; softmax weights are rounded to fp16 (each by
+ * 2^-11 of itself or, where that is more, by 2^-39 of the row's largest) and
+ * the sum they are divided by holds them rounded.  A block whose id is outside
+ * [0, num_blocks) is skipped and recorded.  NaN or infinities in positions past
+ * the sequence's length are not seen; in positions inside a block that the token
+ * reads but does not see, they are not either.
+ *  rules      HOST pointer, read during the call only; not NULL
+ *  workspace  pkv_decode_workspace_bytes(...) bytes, as for
+ *             pkv_decode_attention: zero-filled before first use, left so
+ * Runs on the balanced schedule alone: shapes that it does not take (num_seqs
+ * whose lengths do not fit shared memory beside two stages, or num_seqs *
+ * max_blocks_per_seq above 2^31 - 1) return PKV_ERR_UNSUPPORTED.  Other
+ * arguments, shapes, ordering and errors as pkv_decode_attention; slopes and
+ * prefix_lens are read before an earlier kernel that signals early has
+ * completed, like seq_lens.
+ */
+int pkv_decode_attention_scored(void *out, const void *q, const void *k_cache,
+                                const void *v_cache, const int32_t *block_tables,
+                                const int32_t *seq_lens, float scale, int32_t num_heads,
+                                int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                int32_t num_seqs, int32_t max_blocks_per_seq,
+                                int32_t max_seq_len, int64_t num_blocks, void *workspace,
+                                size_t workspace_bytes, const pkv_score_rules *rules,
+                                pkv_stream_t stream);
+
+/* The same over FP8 caches (layout of pkv_cache_write_fp8; caches and scales
+ * 16-byte aligned). */
+int pkv_decode_attention_scored_fp8(void *out, const void *q, const void *k_cache,
+                                    const void *v_cache, const float *k_scale,
+                                    const float *v_scale, const int32_t *block_tables,
+                                    const int32_t *seq_lens, float scale, int32_t num_heads,
+                                    int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                    int32_t num_seqs, int32_t max_blocks_per_seq,
+                                    int32_t max_seq_len, int64_t num_blocks, void *workspace,
+                                    size_t workspace_bytes, const pkv_score_rules *rules,
+                                    pkv_stream_t stream);
+
+/* pkv_chunk_attention under score rules: new token j of a sequence is at
+ * position L - Q + j.  Workspace (pkv_chunk_workspace_bytes), other arguments,
+ * shapes, ordering and errors as pkv_chunk_attention. */
+int pkv_chunk_attention_scored(void *out, const void *q, const void *k_cache,
+                               const void *v_cache, const int32_t *block_tables,
+                               const int32_t *seq_lens, const int32_t *query_start, float scale,
+                               int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                               int32_t block_size, int32_t num_seqs, int32_t max_blocks_per_seq,
+                               int32_t num_query_tokens, int32_t max_query_len,
+                               int32_t max_seq_len, int64_t num_blocks, void *workspace,
+                               size_t workspace_bytes, const pkv_score_rules *rules,
+                               pkv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A step's bookkeeping on the device. */
+
+/* Largest num_seqs of pkv_resize_sequences. */
+#define PKV_MAX_RESIZE_SEQS 8192
+
+/*
+ * Block tables, slot maps and the free list of a step, from the lengths that
+ * the sequences have (L = seq_lens[i]) and are to have (N = new_lens[i]): a
+ * scheduler's allocation, decided on the device, in one launch.  With
+ * have = ceil(L / block_size) and want = ceil(N / block_size), over the
+ * sequences in order:
+ *  - shrinking (N < L: drafts taken back, or with N = 0 a finished request):
+ *    blocks have > k >= want go back on the free list, the first of them (in
+ *    order of sequence and k) on top.  Their table entries are left as they
+ *    were; entries past a sequence's length are never read.
+ *  - growing (N > L): new blocks come off the top of the list (blocks given back
+ *    in the same call first) into entries have .. want - 1, and each new token
+ *    gets a row: token L + j is row query_start[i] + j, with
+ *        positions[row] = L + j,  slot_mapping[row] = id * block_size + offset.
+ *    A sequence is granted its tokens if the rows up to its last one fit
+ *    max_tokens and, where it needs blocks, the blocks needed up to it fit the
+ *    list; else it keeps its length and entries, and its rows get slot -1.
+ *  - out_lens[i] = N if granted (or N <= L), else L: compare with new_lens.
+ *  - query_start[i] = new tokens asked for by the sequences before i, at most
+ *    max_tokens; rows from query_start[num_seqs] on get slot -1 and position 0,
+ *    so the writes of a step captured for max_tokens rows skip them.
+ * Taking a step back (the same call with the two lengths exchanged) leaves the
+ * free list as it was.
+ *  block_tables    device int32 [num_seqs, max_blocks_per_seq], updated.  A
+ *                  sequence must not give back blocks that another one uses: a
+ *                  finished request with a shared prefix shrinks to the prefix,
+ *                  not to 0.
+ *  seq_lens, new_lens, out_lens  device int32 [num_seqs]; out_lens may be
+ *                  seq_lens.  A length outside [0, max_blocks_per_seq *
+ *                  block_size] leaves its sequence as it was, recorded
+ *                  (PKV_DEVERR_SEQ_LEN).
+ *  free_blocks     device int32 [free_capacity]: the list, its top at
+ *                  free_count[0] - 1; entries from out_free_count[0] on hold
+ *                  nothing of use afterwards.
+ *  free_count, out_free_count  device int32 [1]; may be the same.  A count
+ *                  outside [0, free_capacity] is clamped, blocks past the
+ *                  capacity are dropped, both recorded (PKV_DEVERR_FREE_LIST).
+ *  query_start     device int32 [num_seqs + 1], written.
+ *  slot_mapping, positions  device int64 [max_tokens], written; positions may be
+ *                  NULL.  A block id outside [0, num_blocks), from the table or
+ *                  the list, gives slot -1, recorded (PKV_DEVERR_BLOCK_ID).
+ * Other buffers must not overlap.  Any block_size; num_seqs at most
+ * PKV_MAX_RESIZE_SEQS; max_tokens and free_capacity below 2^30.  Ordering as
+ * pkv_norm_rope_write.  Returns PKV_OK (num_seqs == 0 launches nothing),
+ * PKV_ERR_NULL, PKV_ERR_INVALID, PKV_ERR_UNSUPPORTED, PKV_ERR_ALIGNMENT (4
+ * bytes; 8 for int64), PKV_ERR_CUDA.
+ */
+int pkv_resize_sequences(int32_t *block_tables, const int32_t *seq_lens,
+                         const int32_t *new_lens, int32_t *out_lens, int32_t *free_blocks,
+                         const int32_t *free_count, int32_t *out_free_count,
+                         int32_t *query_start, int64_t *slot_mapping, int64_t *positions,
+                         int32_t num_seqs, int32_t max_blocks_per_seq, int32_t max_tokens,
+                         int32_t free_capacity, int32_t block_size, int64_t num_blocks,
+                         pkv_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * One speculative step around the cache: the new tokens' queries, keys and
  * values leave the QKV product (pkv_norm_rope_write), a tree of drafted tokens
  * is verified against the cache (pkv_tree_attention), and the accepted path's
@@ -537,6 +675,59 @@ int pkv_tree_accept(const pkv_cache_desc *descs, int32_t num_descs, int32_t num_
                     const int32_t *path, int32_t max_depth, const int32_t *ctx_lens,
                     const int32_t *block_tables, int32_t num_seqs, int32_t max_blocks_per_seq,
                     int32_t block_size, int64_t num_blocks, pkv_stream_t stream);
+
+/*
+ * Verification of drafted trees (a chain is a tree) against the target's
+ * probabilities, from given random numbers: the accepted path of each sequence,
+ * as pkv_tree_accept takes it, and its next token, distributed as the target
+ * alone would have drawn them.
+ *
+ * Sequence i's nodes are rows query_start[i] .. query_start[i+1]-1; node 0 is the
+ * last token known before the step, always accepted.  parents[row] is a node's
+ * parent as an index within its sequence, smaller than its own (node 0's is not
+ * read; another node with a negative parent is padding).  p = target_probs[row]
+ * is the target's distribution after a node, q = draft_probs[row] the one that
+ * its children were drawn from, independently.  From node 0 on, the children x
+ * of the current node, in order, with W = 1 and C = 0 at first:
+ *     R(t) = max(p(t) - C q(t), 0)
+ *     accept x if accept_uniforms[x] * W * q(token x) < R(token x): x is the
+ *     current node next;  else C += W, W = sum_t R(t) with the new C.
+ * Without draft_probs a child is a fixed guess (q is 1 at its token): accept if
+ * accept_uniforms[x] * W < R(token x), else W -= R(token x) and R(token x) = 0.
+ * Where no child is accepted, the next token is the lowest index at which the
+ * running sum of R passes sample_uniforms[i] times its whole sum; an empty R
+ * (W = 0) stands back for the last one that was not.  A path of max_depth nodes
+ * ends there, with the next token drawn from p.
+ * Tests and sums are carried in 64 bits (an element of R is rounded to 32).
+ *  path           device int32 [num_seqs, max_depth], written: the accepted
+ *                 nodes, then -1
+ *  path_lens      device int32 [num_seqs], written: accepted nodes, node 0
+ *                 counted; 0 (and next token -1) for a sequence without nodes
+ *  next_tokens    device int32 [num_seqs], written; -1 where p is zero everywhere
+ *  draft_tokens, parents  device int32 [num_nodes].  A token outside [0,
+ *                 vocab_size) or a parent that is not smaller leaves its node out
+ *                 as if it were padding, recorded (PKV_DEVERR_TREE).
+ *  target_probs   device fp32 [num_nodes] rows of vocab_size at target_stride
+ *                 elements (>= vocab_size); rows sum to 1 up to rounding.
+ *                 Negative values and NaN count as 0; infinities are not handled.
+ *  draft_probs    the same at draft_stride, or NULL; leaves' rows are not read
+ *  accept_uniforms, sample_uniforms  device fp32 [num_nodes], [num_seqs], in
+ *                 [0, 1) (others are taken as the nearest of these)
+ *  A sequence with more than PKV_MAX_TREE_NODES nodes, or whose rows are not
+ *  inside [0, num_nodes), is recorded (PKV_DEVERR_SEQ_LEN) and treated as
+ *  without nodes.
+ * max_depth at most PKV_MAX_ACCEPT_DEPTH.  Ordering as pkv_norm_rope_write.
+ * Returns PKV_OK (num_seqs == 0 launches nothing), PKV_ERR_NULL,
+ * PKV_ERR_INVALID, PKV_ERR_UNSUPPORTED, PKV_ERR_ALIGNMENT (4 bytes),
+ * PKV_ERR_CUDA.
+ */
+int pkv_tree_verify(int32_t *path, int32_t max_depth, int32_t *path_lens, int32_t *next_tokens,
+                    const int32_t *draft_tokens, const int32_t *parents,
+                    const int32_t *query_start, const float *target_probs,
+                    int64_t target_stride, const float *draft_probs, int64_t draft_stride,
+                    const float *accept_uniforms, const float *sample_uniforms,
+                    int32_t num_seqs, int32_t num_nodes, int32_t vocab_size,
+                    pkv_stream_t stream);
 
 /* Bytes of the built-in scratch of pkv_decode_attention_noalloc (16 MiB). */
 #define PKV_NOALLOC_SCRATCH_BYTES ((size_t)16 << 20)

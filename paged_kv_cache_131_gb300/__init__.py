@@ -21,7 +21,9 @@ __all__ = [
     "pkv_chunk_workspace_bytes", "pkv_norm_rope", "pkv_cache_desc", "pkv_norm_rope_write",
     "pkv_norm_rope_write_fp8", "pkv_cache_read_fp8", "pkv_tree_attention",
     "pkv_tree_attention_fp8", "pkv_tree_workspace_bytes", "pkv_tree_accept",
-    "PKV_MAX_TREE_NODES", "PKV_MAX_ACCEPT_DEPTH",
+    "pkv_score_rules", "pkv_decode_attention_scored", "pkv_decode_attention_scored_fp8",
+    "pkv_chunk_attention_scored", "pkv_resize_sequences", "pkv_tree_verify",
+    "PKV_MAX_TREE_NODES", "PKV_MAX_ACCEPT_DEPTH", "PKV_MAX_RESIZE_SEQS",
     "PKV_COMPUTE_AUTO", "PKV_COMPUTE_SIMT", "PKV_COMPUTE_MMA", "PKV_SCHEDULE_AUTO",
     "PKV_SCHEDULE_GRID", "PKV_SCHEDULE_BALANCED", "DEVICE_ERRORS",
 ]
@@ -32,8 +34,9 @@ library_path = os.path.join(_HERE, "libpagedkv.so")
 PKV_COMPUTE_AUTO, PKV_COMPUTE_SIMT, PKV_COMPUTE_MMA = 0, 1, 2
 PKV_SCHEDULE_AUTO, PKV_SCHEDULE_GRID, PKV_SCHEDULE_BALANCED = 0, 1, 2
 PKV_MAX_TREE_NODES, PKV_MAX_ACCEPT_DEPTH = 256, 256
+PKV_MAX_RESIZE_SEQS = 8192
 DEVICE_ERRORS = {0: "none", 1: "slot", 2: "block_id", 3: "seq_len", 4: "timeout", 5: "position",
-                 6: "path"}
+                 6: "path", 7: "free_list", 8: "tree"}
 
 EXPORTED_SYMBOLS = [
     "pkv_cache_write", "pkv_decode_attention", "pkv_decode_attention_ex",
@@ -43,7 +46,9 @@ EXPORTED_SYMBOLS = [
     "pkv_cache_write_fp8", "pkv_decode_attention_fp8", "pkv_chunk_attention",
     "pkv_chunk_workspace_bytes", "pkv_norm_rope_write", "pkv_norm_rope_write_fp8",
     "pkv_cache_read_fp8", "pkv_tree_attention", "pkv_tree_attention_fp8",
-    "pkv_tree_workspace_bytes", "pkv_tree_accept",
+    "pkv_tree_workspace_bytes", "pkv_tree_accept", "pkv_decode_attention_scored",
+    "pkv_decode_attention_scored_fp8", "pkv_chunk_attention_scored", "pkv_resize_sequences",
+    "pkv_tree_verify",
 ]
 
 
@@ -76,6 +81,11 @@ class pkv_norm_rope(ctypes.Structure):
                 ("eps", ctypes.c_float), ("cos_sin", ctypes.c_void_p),
                 ("max_position", ctypes.c_int64), ("rot_dim", ctypes.c_int32),
                 ("interleaved", ctypes.c_int32)]
+
+
+class pkv_score_rules(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("slopes", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p)]
 
 
 class pkv_cache_desc(ctypes.Structure):
@@ -140,6 +150,18 @@ def load(path: str | None = None):
     lib.pkv_tree_accept.restype = ctypes.c_int
     lib.pkv_tree_accept.argtypes = [ctypes.POINTER(pkv_cache_desc), _i32, _i32, _p, _i32, _p, _p,
                                     _i32, _i32, _i32, _i64, _p]
+    rules = ctypes.POINTER(pkv_score_rules)
+    lib.pkv_decode_attention_scored.restype = ctypes.c_int
+    lib.pkv_decode_attention_scored.argtypes = dec + [rules, _p]
+    lib.pkv_decode_attention_scored_fp8.restype = ctypes.c_int
+    lib.pkv_decode_attention_scored_fp8.argtypes = dec[:4] + [_p, _p] + dec[4:] + [rules, _p]
+    lib.pkv_chunk_attention_scored.restype = ctypes.c_int
+    lib.pkv_chunk_attention_scored.argtypes = lib.pkv_chunk_attention.argtypes[:-1] + [rules, _p]
+    lib.pkv_resize_sequences.restype = ctypes.c_int
+    lib.pkv_resize_sequences.argtypes = [_p] * 10 + [_i32] * 5 + [_i64, _p]
+    lib.pkv_tree_verify.restype = ctypes.c_int
+    lib.pkv_tree_verify.argtypes = [_p, _i32] + [_p] * 6 + [_i64, _p, _i64, _p, _p, _i32, _i32,
+                                                            _i32, _p]
     lib.pkv_decode_workspace_bytes.restype = _sz
     lib.pkv_decode_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32, _i32]
     lib.pkv_decode_workspace_bytes_ex.restype = _sz
@@ -608,6 +630,186 @@ def pkv_tree_accept(caches, num_layers: int, path, ctx_lens, block_tables, block
         _arg(block_tables, "block_tables", i32, (S, MB), dev), S, MB, block_size, num_blocks,
         _raw_stream(stream, dev))
     return _check(st, "pkv_tree_accept") if check else st
+
+
+def _rules(softcap, window, slopes, prefix_lens, num_heads, num_seqs, dev):
+    import torch
+    return pkv_score_rules(
+        softcap, window,
+        None if slopes is None else _arg(slopes, "slopes", torch.float32, (num_heads,), dev),
+        None if prefix_lens is None else _arg(prefix_lens, "prefix_lens", torch.int32, (num_seqs,),
+                                              dev))
+
+
+def _decode_scored(name, out, q, k_cache, v_cache, scales, block_tables, seq_lens, scale,
+                   num_heads, num_kv_heads, head_dim, block_size, max_seq_len, num_blocks,
+                   workspace, softcap, window, slopes, prefix_lens, stream, check):
+    import torch
+    f16, f32, i32 = torch.float16, torch.float32, torch.int32
+    dev = _current(q, "q")
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [S, MB]")
+    S, MB = q.shape[0], block_tables.shape[1]
+    qshape = (S, num_heads, head_dim)
+    rows = (num_blocks, block_size, num_kv_heads, head_dim)
+    kind = f16 if scales is None else torch.uint8
+    args = [_arg(out, "out", f16, qshape, dev), _arg(q, "q", f16, qshape, dev),
+            _arg(k_cache, "k_cache", kind, rows, dev), _arg(v_cache, "v_cache", kind, rows, dev)]
+    if scales is not None:
+        args += [_arg(scales[0], "k_scale", f32, rows[:3], dev),
+                 _arg(scales[1], "v_scale", f32, rows[:3], dev)]
+    rules = _rules(softcap, window, slopes, prefix_lens, num_heads, S, dev)
+    st = getattr(load(), name)(
+        *args, _arg(block_tables, "block_tables", i32, (S, MB), dev),
+        _arg(seq_lens, "seq_lens", i32, (S,), dev), scale, num_heads, num_kv_heads, head_dim,
+        block_size, S, MB, max_seq_len, num_blocks, *_workspace(workspace, dev),
+        ctypes.byref(rules), _raw_stream(stream, dev))
+    return _check(st, name) if check else st
+
+
+def pkv_decode_attention_scored(out, q, k_cache, v_cache, block_tables, seq_lens, scale: float,
+                                num_heads: int, num_kv_heads: int, head_dim: int, block_size: int,
+                                max_seq_len: int, num_blocks: int, workspace=None,
+                                softcap: float = 0.0, window: int = 0, slopes=None,
+                                prefix_lens=None, stream=None, check: bool = True) -> int:
+    """Paged decode attention under score rules: see pkv_score_rules and
+    pkv_decode_attention_scored in pagedkv.h.
+
+    softcap: scores become softcap * tanh(score / softcap) (0: not); window: the
+    last that many positions are seen (0: all); slopes: CUDA fp32 [H], -slope *
+    distance added to the scores, or None; prefix_lens: CUDA int32 [S], first
+    positions seen whatever the window, or None.  Other arguments as
+    pkv_decode_attention; the workspace is needed.
+    """
+    return _decode_scored("pkv_decode_attention_scored", out, q, k_cache, v_cache, None,
+                          block_tables, seq_lens, scale, num_heads, num_kv_heads, head_dim,
+                          block_size, max_seq_len, num_blocks, workspace, softcap, window, slopes,
+                          prefix_lens, stream, check)
+
+
+def pkv_decode_attention_scored_fp8(out, q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                                    seq_lens, scale: float, num_heads: int, num_kv_heads: int,
+                                    head_dim: int, block_size: int, max_seq_len: int,
+                                    num_blocks: int, workspace=None, softcap: float = 0.0,
+                                    window: int = 0, slopes=None, prefix_lens=None, stream=None,
+                                    check: bool = True) -> int:
+    """pkv_decode_attention_scored over E4M3 caches (uint8) and fp32 scales."""
+    return _decode_scored("pkv_decode_attention_scored_fp8", out, q, k_cache, v_cache,
+                          (k_scale, v_scale), block_tables, seq_lens, scale, num_heads,
+                          num_kv_heads, head_dim, block_size, max_seq_len, num_blocks, workspace,
+                          softcap, window, slopes, prefix_lens, stream, check)
+
+
+def pkv_chunk_attention_scored(out, q, k_cache, v_cache, block_tables, seq_lens, query_start,
+                               scale: float, num_heads: int, num_kv_heads: int, head_dim: int,
+                               block_size: int, max_query_len: int, max_seq_len: int,
+                               num_blocks: int, workspace=None, softcap: float = 0.0,
+                               window: int = 0, slopes=None, prefix_lens=None, stream=None,
+                               check: bool = True) -> int:
+    """Attention of each sequence's new tokens under score rules: see pkv_score_rules
+    and pkv_chunk_attention_scored in pagedkv.h.
+
+    softcap, window, slopes, prefix_lens: as pkv_decode_attention_scored (a token
+    also sees the prefix positions behind its own); other arguments as
+    pkv_chunk_attention.
+    """
+    import torch
+    f16, i32 = torch.float16, torch.int32
+    dev = _current(q, "q")
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [S, MB]")
+    Tq, S, MB = q.shape[0], seq_lens.numel(), block_tables.shape[1]
+    qshape = (Tq, num_heads, head_dim)
+    rows = (num_blocks, block_size, num_kv_heads, head_dim)
+    rules = _rules(softcap, window, slopes, prefix_lens, num_heads, S, dev)
+    st = load().pkv_chunk_attention_scored(
+        _arg(out, "out", f16, qshape, dev), _arg(q, "q", f16, qshape, dev),
+        _arg(k_cache, "k_cache", f16, rows, dev), _arg(v_cache, "v_cache", f16, rows, dev),
+        _arg(block_tables, "block_tables", i32, (S, MB), dev),
+        _arg(seq_lens, "seq_lens", i32, (S,), dev),
+        _arg(query_start, "query_start", i32, (S + 1,), dev), scale, num_heads, num_kv_heads,
+        head_dim, block_size, S, MB, Tq, max_query_len, max_seq_len, num_blocks,
+        *_workspace(workspace, dev), ctypes.byref(rules), _raw_stream(stream, dev))
+    return _check(st, "pkv_chunk_attention_scored") if check else st
+
+
+def pkv_resize_sequences(block_tables, seq_lens, new_lens, out_lens, free_blocks, free_count,
+                         out_free_count, query_start, slot_mapping, positions, block_size: int,
+                         num_blocks: int, stream=None, check: bool = True) -> int:
+    """Block tables, slot maps and the free list of a step, from the lengths that the
+    sequences have and are to have: see pkv_resize_sequences in pagedkv.h.
+
+    block_tables: CUDA int32 [S, MB], updated; seq_lens, new_lens, out_lens: CUDA
+    int32 [S] (out_lens may be seq_lens); free_blocks: CUDA int32 [capacity], a
+    stack of free_count[0] entries; free_count, out_free_count: CUDA int32 [1] (may
+    be the same); query_start: CUDA int32 [S + 1]; slot_mapping, positions: CUDA
+    int64 [max_tokens] (positions may be None).
+    """
+    import torch
+    i32, i64 = torch.int32, torch.int64
+    dev = _current(seq_lens, "seq_lens")
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [S, MB]")
+    S, MB, T, cap = (seq_lens.numel(), block_tables.shape[1], slot_mapping.numel(),
+                     free_blocks.numel())
+    st = load().pkv_resize_sequences(
+        _arg(block_tables, "block_tables", i32, (S, MB), dev),
+        _arg(seq_lens, "seq_lens", i32, (S,), dev), _arg(new_lens, "new_lens", i32, (S,), dev),
+        _arg(out_lens, "out_lens", i32, (S,), dev),
+        _arg(free_blocks, "free_blocks", i32, (cap,), dev),
+        _arg(free_count, "free_count", i32, (1,), dev),
+        _arg(out_free_count, "out_free_count", i32, (1,), dev),
+        _arg(query_start, "query_start", i32, (S + 1,), dev),
+        _arg(slot_mapping, "slot_mapping", i64, (T,), dev),
+        None if positions is None else _arg(positions, "positions", i64, (T,), dev), S, MB, T, cap,
+        block_size, num_blocks, _raw_stream(stream, dev))
+    return _check(st, "pkv_resize_sequences") if check else st
+
+
+def _prob_rows(t, name, T, V, dev):
+    """(device pointer, row stride in elements) of fp32 rows [T, V] whose elements are
+    packed; rows may be strided (a slice of padded ones)."""
+    import torch
+    if t.dtype is not torch.float32 or t.shape != (T, V) or t.get_device() != dev:
+        _arg(t, name, torch.float32, (T, V), dev)
+    st, sv = t.stride()
+    if (V > 1 and sv != 1) or (T > 1 and st < V):
+        raise ValueError(f"{name}: a row's elements must be packed, rows apart")
+    return t.data_ptr(), st if T > 1 else V
+
+
+def pkv_tree_verify(path, path_lens, next_tokens, draft_tokens, parents, query_start,
+                    target_probs, draft_probs, accept_uniforms, sample_uniforms, stream=None,
+                    check: bool = True) -> int:
+    """Verification of drafted trees against the target's probabilities from given
+    random numbers: see pkv_tree_verify in pagedkv.h.
+
+    path: CUDA int32 [S, max_depth], path_lens, next_tokens: CUDA int32 [S],
+    written; draft_tokens, parents: CUDA int32 [T]; query_start: CUDA int32
+    [S + 1]; target_probs, draft_probs: CUDA fp32 [T, V], rows may be strided
+    (draft_probs None: fixed guesses); accept_uniforms: CUDA fp32 [T];
+    sample_uniforms: CUDA fp32 [S].
+    """
+    import torch
+    i32, f32 = torch.int32, torch.float32
+    dev = _current(path, "path")
+    if path.dim() != 2 or target_probs.dim() != 2:
+        raise ValueError("path must be [S, max_depth], target_probs [T, V]")
+    S, depth = path.shape
+    T, V = target_probs.shape
+    tp, ts = _prob_rows(target_probs, "target_probs", T, V, dev)
+    dp, ds = (None, 0) if draft_probs is None else _prob_rows(draft_probs, "draft_probs", T, V, dev)
+    st = load().pkv_tree_verify(
+        _arg(path, "path", i32, (S, depth), dev), depth,
+        _arg(path_lens, "path_lens", i32, (S,), dev),
+        _arg(next_tokens, "next_tokens", i32, (S,), dev),
+        _arg(draft_tokens, "draft_tokens", i32, (T,), dev),
+        _arg(parents, "parents", i32, (T,), dev),
+        _arg(query_start, "query_start", i32, (S + 1,), dev), tp, ts, dp, ds,
+        _arg(accept_uniforms, "accept_uniforms", f32, (T,), dev),
+        _arg(sample_uniforms, "sample_uniforms", f32, (S,), dev), S, T, V,
+        _raw_stream(stream, dev))
+    return _check(st, "pkv_tree_verify") if check else st
 
 
 def pkv_decode_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,

@@ -96,6 +96,12 @@ constexpr int kTmemS = 128;
 constexpr int kTmemP = 256;
 constexpr int kTmemQ = 384;
 constexpr float kRescaleLog2 = 8.f;            // move the reference past 2^8
+// Under score rules the weights stand 2^11 higher and the reference moves past
+// 2^4, so that they reach 2^15 and keep fp16's 11 bits down to 2^-25 of the
+// row's largest (a capped or biased row can spread much of its mass over many
+// small weights).
+constexpr float kRuleRescaleLog2 = 4.f;
+constexpr float kRuleShiftLog2 = 11.f;
 // rates of the split between the call's two kernels (see the plan kernel)
 // (single precision: this GPU's double-precision rate is low)
 constexpr float kHbmBytesPerUs = 6.0e6f;        // decode stream, whole GPU
@@ -143,14 +149,18 @@ struct ChunkParams {
     float2 *part_ml;
     float *part_o;
     ErrorRecord *err;
+    // score rules (the kernels under rules only)
+    dec::RuleParams rules;
+    const __half *v_cache;
 };
 
-// An item as the producer hands it to the other warps (64 bytes).
+// An item as the producer hands it to the other warps.
 struct ItemInfo {
     int seq, part, kvh, tile;
     int nsteps, nblk, L, Q;
-    int q0, nparts, done, pad;
+    int q0, nparts, done, prefix;
     uint32_t valid[kPartBlocks / 32];  // one bit per block of the partition: id in range
+    int pb, skip, pad0, pad1;  // (under rules) see Span
 };
 
 // Shared memory (from a 1024-aligned base): the query tile being staged,
@@ -250,8 +260,10 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 // ours (too few rows) or invalid (recorded when `report`).
 struct SeqGeo {
     int L, Q, q0, rows, tiles, parts;
+    int prefix;  // (under rules) positions below are seen by every token, <= L
 };
 
+template <bool kRules>
 __device__ __forceinline__ bool seq_geo(const ChunkParams &p, int s, int G, bool report,
                                         SeqGeo &sg) {
     const int L = __ldg(p.seq_lens + s);
@@ -269,7 +281,44 @@ __device__ __forceinline__ bool seq_geo(const ChunkParams &p, int s, int G, bool
     if (sg.rows < p.min_rows || sg.rows == 0) return false;
     sg.tiles = (sg.rows + kRows - 1) / kRows;
     sg.parts = (L + kPartTokens - 1) / kPartTokens;
+    sg.prefix = 0;
+    if constexpr (kRules) {
+        if (p.rules.prefix_lens != nullptr)
+            sg.prefix = max(0, min(L, __ldg(p.rules.prefix_lens + s)));
+        if (p.rules.window < L) {
+            // a tile's window spans window + 128 / G - 1 positions at most
+            const int most = (sg.prefix + kBS - 1) / kBS +
+                             (p.rules.window + kRows / G) / kBS + 2;
+            sg.parts = min(sg.parts, (most + kPartBlocks - 1) / kPartBlocks);
+        }
+    }
     return true;
+}
+
+// Under rules: the blocks that some row of a tile sees, in order -- the first pb
+// (the prefix's) and, `skip` blocks later, those from the first row's window to
+// the last row's position; nblk in all.  Partitions divide this list.
+struct Span {
+    int pb, skip, nblk;
+};
+
+__device__ __forceinline__ int span_block(int pb, int skip, int v) { return v < pb ? v : v + skip; }
+
+__device__ __forceinline__ Span tile_span(const SeqGeo &sg, int tile, int G, int window) {
+    const int a0 = sg.L - sg.Q + tile * (kRows / G);  // positions of the first
+    const int a1 = sg.L - sg.Q + (min(sg.rows, (tile + 1) * kRows) - 1) / G;  // and last row
+    Span sp;
+    sp.pb = (sg.prefix + kBS - 1) / kBS;
+    const int end = a1 / kBS + 1, w0 = max(0, a0 - window + 1) / kBS;
+    sp.skip = max(0, w0 - sp.pb);
+    sp.nblk = sp.skip > 0 ? sp.pb + end - w0 : max(end, sp.pb);
+    return sp;
+}
+
+// Whether every row of a tile (positions a0 .. a1) sees all keys of the block
+// that starts at kp.
+__device__ __forceinline__ bool seen_whole(int kp, int a0, int a1, int window, int prefix) {
+    return kp + kBS <= prefix || (kp + kBS - 1 <= a0 && a1 - kp < window);
 }
 
 // First query tile that needs KV partition `part` (its last token reaches
@@ -282,13 +331,18 @@ __device__ __forceinline__ int first_tile(const SeqGeo &sg, int part, int G) {
     return min(sg.tiles - 1, max(0, t));
 }
 
+template <bool kRules>
 __device__ __forceinline__ int seq_items(const SeqGeo &sg, int G, int Hk) {
+    // (under rules: every partition of every tile; the empty ones are passed over
+    // when they are taken)
+    if constexpr (kRules) return sg.parts * sg.tiles * Hk;
     int n = 0;
     for (int pt = 0; pt < sg.parts; ++pt) n += sg.tiles - first_tile(sg, pt, G);
     return n * Hk;
 }
 
 // One CTA: the list of the sequences this kernel takes and their item counts.
+template <bool kRules>
 __global__ void __launch_bounds__(1024) chunk_plan_kernel(const __grid_constant__ ChunkParams p,
                                                           int G) {
     __shared__ int wsum[32];
@@ -307,8 +361,8 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const __grid_constant_
     for (int s0 = 0; s0 < p.num_seqs; s0 += blockDim.x) {
         const int s = s0 + threadIdx.x;
         SeqGeo sg;
-        const bool mine = s < p.num_seqs && seq_geo(p, s, G, true, sg);
-        const int cnt = mine ? seq_items(sg, G, p.num_kv_heads) : 0;
+        const bool mine = s < p.num_seqs && seq_geo<kRules>(p, s, G, true, sg);
+        const int cnt = mine ? seq_items<kRules>(sg, G, p.num_kv_heads) : 0;
         float my_steps = 0.f;
         unsigned long long my_dec = 0;
         if (mine) {
@@ -321,11 +375,29 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const __grid_constant_
                                R * nt * (nt - 1.f) * 0.5f + static_cast<float>(sg.Q);
             my_steps = keys * (1.f / kStepKeys) * static_cast<float>(p.num_kv_heads) +
                        0.5f * static_cast<float>(cnt);
+            if constexpr (kRules) {
+                // from the first, middle and last tile's blocks
+                const int w = p.rules.window;
+                const float b = static_cast<float>(tile_span(sg, 0, G, w).nblk) +
+                                4.f * static_cast<float>(tile_span(sg, sg.tiles / 2, G, w).nblk) +
+                                static_cast<float>(tile_span(sg, sg.tiles - 1, G, w).nblk);
+                my_steps = nt * static_cast<float>(p.num_kv_heads) *
+                           (b * (1.f / (6.f * kStepBlocks)) + 0.5f);
+            }
         } else if (s < p.num_seqs && p.max_cols > 0) {
             const int L = __ldg(p.seq_lens + s);
             const int Q = __ldg(p.query_start + s + 1) - __ldg(p.query_start + s);
             if (Q > 0 && Q <= L && Q * G <= p.max_cols && L <= p.max_blocks_per_seq * kBS)
                 my_dec = static_cast<unsigned long long>((L + kBS - 1) / kBS);
+            if constexpr (kRules) {
+                if (my_dec > 0) {
+                    const int pl = p.rules.prefix_lens != nullptr
+                                       ? max(0, min(L, __ldg(p.rules.prefix_lens + s)))
+                                       : 0;
+                    my_dec -= max(0, max(0, L - Q - p.rules.window + 1) / kBS -
+                                         (pl + kBS - 1) / kBS);
+                }
+            }
         }
         // one shared atomic per warp and counter
 #pragma unroll
@@ -442,14 +514,17 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const __grid_constant_
 
 // Block ids of an item's partition: lane l holds blocks l, 32 + l, 64 + l and
 // 96 + l of it; -1 past the item or out of range (recorded when `report`).
+// (pb, skip: under rules the list of blocks is a tile's Span.)
 __device__ __forceinline__ void load_ids(const ChunkParams &p, int seq, int blo, int nblk,
-                                         int lane, bool report, int (&ids)[kPartBlocks / 32]) {
+                                         int lane, bool report, int (&ids)[kPartBlocks / 32],
+                                         int pb = 0, int skip = 0) {
 #pragma unroll
     for (int w = 0; w < kPartBlocks / 32; ++w) {
         const int b = w * 32 + lane;
         int id = -1;
         if (b < nblk) {
-            const int64_t at = static_cast<int64_t>(seq) * p.max_blocks_per_seq + blo + b;
+            const int64_t at = static_cast<int64_t>(seq) * p.max_blocks_per_seq +
+                               span_block(pb, skip, blo + b);
             id = __ldg(p.block_tables + at);
             if (id < 0 || static_cast<int64_t>(id) >= p.num_blocks) {
                 if (report) record_error(p.err, PKV_DEVERR_BLOCK_ID, at);
@@ -490,12 +565,57 @@ __device__ __forceinline__ int3 decode_item(const SeqGeo &sg, int local, int G, 
 // scalars; block ids are spread over the lanes).
 struct Fetched {
     int done, seq, part, kvh, tile, nsteps, nblk, L, Q, q0, nparts;
+    int prefix, pb, skip;  // (under rules)
     int ids[kPartBlocks / 32];
     uint32_t valid[kPartBlocks / 32];
 };
 
+template <bool kRules>
 __device__ __forceinline__ void fetch_item(const ChunkParams &p, int n_big, int total, int G,
                                            int logG, int lane, Fetched &f) {
+    if constexpr (kRules) {
+        // items in list order until one has blocks (the list ends every search)
+        for (;;) {
+            int item = 0;
+            if (lane == 0) item = atomicAdd(p.work, 1);
+            item = __shfl_sync(0xffffffffu, item, 0);
+            f.done = item >= total;
+            if (f.done) return;
+            int lo = 0, hi = n_big - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (__ldcg(p.big_cum + mid) <= item) lo = mid;
+                else hi = mid - 1;
+            }
+            const int seq = __ldcg(p.big_seq + lo);
+            SeqGeo sg;
+            seq_geo<true>(p, seq, G, false, sg);
+            const int local = item - __ldcg(p.big_cum + lo), per = sg.tiles * p.num_kv_heads;
+            const int part = local / per, rest = local - part * per;
+            const int tile = sg.tiles - 1 - rest / p.num_kv_heads;
+            const Span sp = tile_span(sg, tile, G, p.rules.window);
+            const int blo = part * kPartBlocks;
+            if (blo >= sp.nblk) continue;
+            f.seq = seq;
+            f.part = part;
+            f.kvh = rest % p.num_kv_heads;
+            f.tile = tile;
+            f.nblk = min(kPartBlocks, sp.nblk - blo);
+            f.nsteps = (f.nblk + kStepBlocks - 1) / kStepBlocks;
+            f.L = sg.L;
+            f.Q = sg.Q;
+            f.q0 = sg.q0;
+            f.nparts = (sp.nblk + kPartBlocks - 1) / kPartBlocks;
+            f.prefix = sg.prefix;
+            f.pb = sp.pb;
+            f.skip = sp.skip;
+            load_ids(p, seq, blo, f.nblk, lane, true, f.ids, sp.pb, sp.skip);
+#pragma unroll
+            for (int w = 0; w < kPartBlocks / 32; ++w)
+                f.valid[w] = __ballot_sync(0xffffffffu, f.ids[w] >= 0);
+            return;
+        }
+    }
     int item = 0;
     if (lane == 0) item = atomicAdd(p.work, 1);
     item = __shfl_sync(0xffffffffu, item, 0);
@@ -510,7 +630,7 @@ __device__ __forceinline__ void fetch_item(const ChunkParams &p, int n_big, int 
     }
     const int seq = __ldcg(p.big_seq + lo);
     SeqGeo sg;
-    seq_geo(p, seq, G, false, sg);  // (the plan listed it: valid)
+    seq_geo<false>(p, seq, G, false, sg);  // (the plan listed it: valid)
     const int3 d = decode_item(sg, item - __ldcg(p.big_cum + lo), G, p.num_kv_heads);
     const int j_last = (min(sg.rows, (d.z + 1) * kRows) - 1) >> logG;
     const int kv_end = sg.L - sg.Q + j_last + 1;  // keys [0, kv_end) for the tile
@@ -531,7 +651,97 @@ __device__ __forceinline__ void fetch_item(const ChunkParams &p, int n_big, int 
     for (int w = 0; w < kPartBlocks / 32; ++w) f.valid[w] = __ballot_sync(0xffffffffu, f.ids[w] >= 0);
 }
 
-template <int D>
+// The row's scores of this thread's 64 keys under the rules, in place: in log2
+// units, masked ones minus infinity, mx their maximum.  The keys are four blocks
+// of the tile's list from place v0 on, nbg of them there, bad ones not in vmask.
+// True if the warp's rows see every key (the masks are passed over then).
+__device__ __forceinline__ bool rule_scores(const ChunkParams &p, uint32_t (&sx)[kGroupKeys],
+                                            int nbg, uint32_t vmask, int v0, int pb, int skip,
+                                            int prefix, int pos, float slope, float sl2,
+                                            float &mx) {
+    int kp[kGroupKeys / kBS];  // positions of the blocks' first keys
+    bool whole = nbg == kGroupKeys / kBS && vmask == 0xFu;
+#pragma unroll
+    for (int b = 0; b < kGroupKeys / kBS; ++b) {
+        kp[b] = span_block(pb, skip, v0 + b) * kBS;
+        whole = whole && seen_whole(kp[b], pos, pos, p.rules.window, prefix);
+    }
+    const bool fast = __all_sync(0xffffffffu, whole);
+    if (p.rules.cap_log2 > 0.f) {
+#pragma unroll
+        for (int e = 0; e < kGroupKeys; ++e)
+            sx[e] = __float_as_uint(dec::capped_score(__uint_as_float(sx[e]), p.rules.cap_log2,
+                                                      p.rules.cap_scale));
+    } else {
+#pragma unroll
+        for (int e = 0; e < kGroupKeys; ++e) sx[e] = __float_as_uint(__uint_as_float(sx[e]) * sl2);
+    }
+    if (p.rules.slopes != nullptr) {
+#pragma unroll
+        for (int b = 0; b < kGroupKeys / kBS; ++b) {
+            const float d0 = static_cast<float>(kp[b] - pos);
+#pragma unroll
+            for (int i = 0; i < kBS; ++i) {
+                uint32_t &x = sx[b * kBS + i];
+                x = __float_as_uint(fmaf(-slope, fabsf(d0 + static_cast<float>(i)), __uint_as_float(x)));
+            }
+        }
+    }
+    if (!fast) {
+#pragma unroll
+        for (int e = 0; e < kGroupKeys; ++e) {
+            const int b = e / kBS, at = kp[b] + e % kBS;
+            const bool vis = b < nbg && ((vmask >> b) & 1u) &&
+                             dec::rule_sees(pos, at, p.rules.window, prefix);
+            if (!vis) sx[e] = __float_as_uint(kNegInf);
+        }
+    }
+    float mr[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mr[i] = kNegInf;
+#pragma unroll
+    for (int e = 0; e < kGroupKeys / 2; ++e)
+        mr[e & 7] = fmax3(mr[e & 7], __uint_as_float(sx[2 * e]), __uint_as_float(sx[2 * e + 1]));
+    mx = fmax3(fmax3(mr[0], mr[1], mr[2]), fmax3(mr[3], mr[4], mr[5]), fmaxf(mr[6], mr[7]));
+    return fast;
+}
+
+// Value block `vb` ([chunk][token][128 B]): rows from `end` on zeroed, and of the
+// others the elements that are not finite; true if there were any.
+template <int CH>
+__device__ __noinline__ bool clean_block(uint8_t *vb, int end, int lane, bool *touched) {
+    bool bad = false;
+    for (int i = lane; i < CH * kBS * 8; i += 32) {
+        uint4 *at = reinterpret_cast<uint4 *>(vb + i * 16);
+        const int token = (i >> 3) & (kBS - 1);
+        if (token >= end) {
+            *at = make_uint4(0u, 0u, 0u, 0u);
+            *touched = true;
+            continue;
+        }
+        const uint4 x = *at;
+        uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        bool mine = false;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if ((w[k] & 0x7C00u) == 0x7C00u) {
+                w[k] &= 0xFFFF0000u;
+                mine = true;
+            }
+            if ((w[k] & 0x7C000000u) == 0x7C000000u) {
+                w[k] &= 0xFFFFu;
+                mine = true;
+            }
+        }
+        if (mine) {
+            *at = make_uint4(w[0], w[1], w[2], w[3]);
+            *touched = bad = true;
+        }
+    }
+    return bad;
+}
+
+template <int D, bool kRules>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_attention_kernel(const __grid_constant__ ChunkParams p) {
     using Gm = Geo<D>;
@@ -543,7 +753,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sb = smem_u32(smem);
     const Bars br{sb + Gm::kOffBar};
     ItemInfo *info = reinterpret_cast<ItemInfo *>(smem + Gm::kOffInfo);
-    // misc: [0] tensor-memory base
+    // misc: [0] tensor-memory base, [1], [2] (under rules) 1 + the last item of
+    // either parity whose values were not all finite where some row is masked
     volatile int *misc = reinterpret_cast<volatile int *>(smem + Gm::kOffMisc);
 
     const int Hk = p.num_kv_heads, H = p.num_heads;
@@ -569,6 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(br.s_full(), 1);
         mbar_init(br.s_free(), kSoftmaxWarps);
         mbar_init(br.o_free(), kSoftmaxWarps);
+        misc[1] = misc[2] = 0;
         fence_mbarrier_init();
     }
     // the work list, the caches and the outputs are written by earlier
@@ -595,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int gs = 0;  // steps staged
         bool ok = true;
         Fetched cur;
-        fetch_item(p, n_big, total, G, logG, lane, cur);
+        fetch_item<kRules>(p, n_big, total, G, logG, lane, cur);
         for (int it = 0; ok; ++it) {
             const int slot = it & 1;
             if (it >= 2 && !wait_all(br.q_empty(slot), ((it >> 1) - 1) & 1)) {
@@ -616,6 +828,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     in.Q = cur.Q;
                     in.q0 = cur.q0;
                     in.nparts = cur.nparts;
+                    if constexpr (kRules) {
+                        in.prefix = cur.prefix;
+                        in.pb = cur.pb;
+                        in.skip = cur.skip;
+                    }
 #pragma unroll
                     for (int w = 0; w < kPartBlocks / 32; ++w) in.valid[w] = cur.valid[w];
                 }
@@ -657,7 +874,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       b * (kBS * 128),
                                   &p.tm_k, 0, id >= 0 ? id * kBS : -kBS, cur.kvh * CH + c,
                                   br.k_full(ks));
-                if (n == fetch_at) fetch_item(p, n_big, total, G, logG, lane, nxt);
+                if (n == fetch_at) fetch_item<kRules>(p, n_big, total, G, logG, lane, nxt);
             }
             cur = nxt;
         }
@@ -682,11 +899,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const ItemInfo &in = info[slot];
             const int done = in.done, seq = in.seq, part = in.part, kvh = in.kvh;
             const int nsteps = in.nsteps, nblk = in.nblk;
+            const int pb = kRules ? in.pb : 0, skip = kRules ? in.skip : 0;
             __syncwarp();
             if (lane == 0) mbar_arrive(br.q_empty(slot));
             if (done) break;
             int ids[kPartBlocks / 32];
-            load_ids(p, seq, part * kPartBlocks, nblk, lane, false, ids);
+            load_ids(p, seq, part * kPartBlocks, nblk, lane, false, ids, pb, skip);
             for (int n = 0; n < nsteps; ++n, ++gs) {
                 const int vs = gs % kVStages;
                 if (gs >= kVStages && !wait_all(br.v_empty(vs), ((gs / kVStages) - 1) & 1)) {
@@ -784,6 +1002,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const ItemInfo &in = info[slot];
             const int done = in.done, nsteps = in.nsteps, nblk = in.nblk, L = in.L;
             const int blo = in.part * kPartBlocks;
+            int pb = 0, skip = 0, prefix = 0, a0 = 0, a1 = 0;
+            if constexpr (kRules) {
+                pb = in.pb;
+                skip = in.skip;
+                prefix = in.prefix;
+                a0 = L - in.Q + in.tile * (kRows >> logG);
+                a1 = min(a0 + (kRows >> logG), L) - 1;
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(br.q_empty(slot));
             if (done) break;
@@ -793,7 +1019,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = wait_all(br.v_full(vs), (g / kVStages) & 1);
                 if (!ok) break;
                 const uint32_t v_s = sb + Gm::kOffV + vs * Gm::kV;
-                if (m == nsteps - 1) {
+                if constexpr (kRules) {
+                    // blocks that some row does not see whole: value rows past the
+                    // sequence's end zeroed, and the others' elements that are not
+                    // finite (0 * NaN is not 0), which the rows that see them add
+                    // at the end
+                    bool dirty = false, touched = false;
+                    for (int b = 0; b < nb; ++b) {
+                        const int kp = span_block(pb, skip, blo + m * kStepBlocks + b) * kBS;
+                        if (seen_whole(kp, a0, a1, p.rules.window, prefix) && kp + kBS <= L) continue;
+                        uint8_t *vb = smem + Gm::kOffV + vs * Gm::kV + b * Gm::kVBlock;
+                        const bool bad = clean_block<CH>(vb, L - kp, lane, &touched);
+                        dirty = dirty || bad;
+                    }
+                    if (touched) fence_proxy_async_smem();
+                    if (__any_sync(0xffffffffu, dirty) && lane == 0) misc[1 + (it & 1)] = it + 1;
+                    __syncwarp();
+                } else if (m == nsteps - 1) {
                     // value rows at and past the sequence end hold anything
                     // (their weights are 0, but 0 * NaN is not): zero them
                     const int t0 = L - (blo + m * kStepBlocks + nb - 1) * kBS;
@@ -853,6 +1095,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int done = in.done, seq = in.seq, part = in.part, kvh = in.kvh, tile = in.tile;
             const int nsteps = in.nsteps, nblk = in.nblk, L = in.L, Q = in.Q, q0 = in.q0;
             const int nparts = in.nparts;
+            const int in_pb = in.pb, in_skip = in.skip, in_prefix = in.prefix;
             uint32_t valid[kPartBlocks / 32];
 #pragma unroll
             for (int w = 0; w < kPartBlocks / 32; ++w) valid[w] = in.valid[w];
@@ -873,6 +1116,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool row_ok = rr < rows;
             const int j = rr >> logG;
             const int lim = row_ok ? L - Q + j : -1;  // last key position this row sees
+            int pb = 0, skip = 0, prefix = 0, pos = 0;
+            float slope = 0.f;
+            if constexpr (kRules) {
+                pb = in_pb;
+                skip = in_skip;
+                prefix = in_prefix;
+                pos = L - Q + min(j, Q - 1);  // (rows past the last: as it, not written)
+                if (p.rules.slopes != nullptr)
+                    slope = __ldg(p.rules.slopes + kvh * G + (rr & (G - 1))) * dec::kLog2e;
+            }
             const int64_t orow = static_cast<int64_t>(q0 + j) * H + kvh * G + (rr & (G - 1));
             float m_used = kNegInf, l = 0.f;  // l: this thread's keys only
 
@@ -903,7 +1156,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // every key of the warp is visible and the scale is not
                 // negative, else the scores are scaled and masked and their
                 // maximum taken again
-                const bool fast = __all_sync(0xffffffffu, nbg == 4 && vmask == 0xFu &&
+                bool fast;
+                float mx;
+                if constexpr (kRules) {
+                    fast = rule_scores(p, sx, nbg, vmask, part * kPartBlocks + b0, pb, skip, prefix,
+                                       pos, slope, sl2, mx);
+                } else {
+                fast = __all_sync(0xffffffffu, nbg == 4 && vmask == 0xFu &&
                                                               kbase + kGroupKeys - 1 <= lim &&
                                                               sl2 >= 0.f);
                 float mr[8];
@@ -913,7 +1172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int e = 0; e < kGroupKeys / 2; ++e)
                     mr[e & 7] = fmax3(mr[e & 7], __uint_as_float(sx[2 * e]),
                                       __uint_as_float(sx[2 * e + 1]));
-                float mx = fmax3(fmax3(mr[0], mr[1], mr[2]), fmax3(mr[3], mr[4], mr[5]),
+                mx = fmax3(fmax3(mr[0], mr[1], mr[2]), fmax3(mr[3], mr[4], mr[5]),
                                  fmaxf(mr[6], mr[7]));
                 if (!fast) {
 #pragma unroll
@@ -930,10 +1189,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     mx *= sl2;
                 }
+                }
                 // the row's other half: the thread 16 lanes away
                 const float mo = __shfl_xor_sync(0xffffffffu, mx, 16);
                 const float m_new = fmaxf(m_used, fmaxf(mx, mo));
-                const bool raise = m_new > m_used + kRescaleLog2;
+                const bool raise = m_new > m_used + (kRules ? kRuleRescaleLog2 : kRescaleLog2);
                 // O holds this item's earlier steps relative to m_used: rescale
                 // this thread's columns before the reference moves (the
                 // previous P V done first)
@@ -964,7 +1224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // fp16 pairs: column 32 h + i of the buffer holds keys
                 // 64 h + 2i, 2i+1; the P V of two steps back must be done
                 // with this buffer
-                const float a = fast ? sl2 : 1.f;
+                const float a = fast && !kRules ? sl2 : 1.f;
                 const int pb = g & 1;
                 if (g >= 2) {
                     if (!wait_all(br.pv_done(pb), ((g - 2) >> 1) & 1)) {
@@ -974,7 +1234,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::fence_after_sync();
                 }
                 // key pairs in packed fp32 lanes: one fma and one add per pair
-                const uint64_t a2 = f32x2(a, a), nms2 = f32x2(-ms, -ms);
+                const float nms = kRules ? kRuleShiftLog2 - ms : -ms;
+                const uint64_t a2 = f32x2(a, a), nms2 = f32x2(nms, nms);
                 uint64_t l2[4] = {0ull, 0ull, 0ull, 0ull};
                 uint32_t x[32];
 #pragma unroll
@@ -1013,6 +1274,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::wait_ld();
 #pragma unroll
                 for (int d = 0; d < DH; ++d) o[d] = __uint_as_float(ob[d]);
+            }
+            if constexpr (kRules) {
+                // values that are not finite, left out of the MMAs where some row is
+                // masked: added here by the rows that see them
+                if (misc[1 + (it & 1)] == it + 1) {
+                    const int a0 = L - Q + tile * (kRows >> logG);
+                    const int a1 = min(a0 + (kRows >> logG), L) - 1;
+                    for (int b = 0; b < nblk; ++b) {
+                        const int blk = span_block(pb, skip, part * kPartBlocks + b);
+                        const int kp = blk * kBS;
+                        if (seen_whole(kp, a0, a1, p.rules.window, prefix) && kp + kBS <= L) continue;
+                        const int64_t id = __ldg(p.block_tables +
+                                                 static_cast<int64_t>(seq) * p.max_blocks_per_seq + blk);
+                        if (id < 0 || id >= p.num_blocks) continue;
+                        for (int t = 0; t < min(kBS, L - kp); ++t) {
+                            if (!dec::rule_sees(pos, kp + t, p.rules.window, prefix)) continue;
+                            const __half *v = p.v_cache + ((id * kBS + t) * Hk + kvh) * D + DH * h;
+#pragma unroll
+                            for (int d = 0; d < DH; ++d) {
+                                const float x = __half2float(v[d]);
+                                if (!isfinite(x)) o[d] += x;
+                            }
+                        }
+                    }
+                }
             }
             tc::fence_before_sync();
             __syncwarp();
@@ -1099,9 +1385,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 using ChunkFn = void (*)(const ChunkParams);
 
-ChunkFn select(int D) {
-    if (D == 128) return chunk_attention_kernel<128>;
-    if (D == 64) return chunk_attention_kernel<64>;
+ChunkFn select(int D, bool scored) {
+    if (D == 128) return scored ? chunk_attention_kernel<128, true> : chunk_attention_kernel<128, false>;
+    if (D == 64) return scored ? chunk_attention_kernel<64, true> : chunk_attention_kernel<64, false>;
     return nullptr;
 }
 
@@ -1151,17 +1437,19 @@ extern "C" size_t pkv_chunk_workspace_bytes(int32_t num_seqs, int32_t num_heads,
                                z.o_bytes);
 }
 
-extern "C" int pkv_chunk_attention(void *out, const void *q, const void *k_cache,
-                                   const void *v_cache, const int32_t *block_tables,
-                                   const int32_t *seq_lens, const int32_t *query_start,
-                                   float scale, int32_t num_heads, int32_t num_kv_heads,
-                                   int32_t head_dim, int32_t block_size, int32_t num_seqs,
-                                   int32_t max_blocks_per_seq, int32_t num_query_tokens,
-                                   int32_t max_query_len, int32_t max_seq_len,
-                                   int64_t num_blocks, void *workspace, size_t workspace_bytes,
-                                   pkv_stream_t stream) {
-    using namespace pkv;
-    using namespace pkv::chunk;
+namespace pkv {
+namespace chunk {
+namespace {
+
+// Either entry point (rules null: without score rules, scored false).
+int chunk_attention(void *out, const void *q, const void *k_cache, const void *v_cache,
+                    const int32_t *block_tables, const int32_t *seq_lens,
+                    const int32_t *query_start, float scale, int32_t num_heads,
+                    int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_seqs,
+                    int32_t max_blocks_per_seq, int32_t num_query_tokens, int32_t max_query_len,
+                    int32_t max_seq_len, int64_t num_blocks, void *workspace,
+                    size_t workspace_bytes, bool scored, const pkv_score_rules *rules,
+                    pkv_stream_t stream) {
     if (num_seqs < 0 || num_query_tokens < 0) return PKV_ERR_INVALID;
     if (num_seqs == 0 || num_query_tokens == 0) return PKV_OK;
     if (!out || !q || !k_cache || !v_cache || !block_tables || !seq_lens || !query_start)
@@ -1179,6 +1467,11 @@ extern "C" int pkv_chunk_attention(void *out, const void *q, const void *k_cache
         !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(query_start, 4) ||
         (workspace != nullptr && !aligned(workspace, 16)))
         return PKV_ERR_ALIGNMENT;
+    dec::RuleParams rp{};
+    if (scored) {
+        const int st = dec::make_rules(rules, scale, &rp);
+        if (st != PKV_OK) return st;
+    }
     const auto z = sizes(num_seqs, num_heads, num_kv_heads, head_dim, num_query_tokens,
                          max_query_len, max_seq_len);
     // work items (and their prefix sums) are 32-bit: at most
@@ -1190,7 +1483,7 @@ extern "C" int pkv_chunk_attention(void *out, const void *q, const void *k_cache
     const int64_t need = z.bal_bytes + z.list_bytes + z.counters_bytes + z.ml_bytes + z.o_bytes;
     if (workspace == nullptr || static_cast<int64_t>(workspace_bytes) < need)
         return PKV_ERR_WORKSPACE;
-    ChunkFn fn = select(head_dim);
+    ChunkFn fn = select(head_dim, scored);
     if (fn == nullptr) return PKV_ERR_UNSUPPORTED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
@@ -1219,13 +1512,14 @@ extern "C" int pkv_chunk_attention(void *out, const void *q, const void *k_cache
         b.query_start = query_start;
         b.max_cols = 8 * z.col_tiles;
         b.num_query_tokens = num_query_tokens;
+        b.rules = rp;
         const int st = dec::setup_balanced(b, z.bal, b.max_cols, ws, k_cache, v_cache);
         if (st != PKV_OK) return st;
         b.err = device_error_record();
         if (b.err == nullptr) return PKV_ERR_CUDA;
         min_rows = b.max_cols + 1;
         if (static_cast<int64_t>(max_query_len) * G < min_rows)  // no long chunks
-            return dec::launch_balanced(b, z.bal, head_dim, G, false, false, s, z.col_tiles);
+            return dec::launch_balanced(b, z.bal, head_dim, G, false, false, s, z.col_tiles, scored);
         use_bal = true;
     }
 
@@ -1247,6 +1541,8 @@ extern "C" int pkv_chunk_attention(void *out, const void *q, const void *k_cache
     p.num_query_tokens = num_query_tokens;
     p.min_rows = min_rows;
     p.num_blocks = num_blocks;
+    p.rules = rp;
+    p.v_cache = static_cast<const __half *>(v_cache);
     uint8_t *cws = ws + z.bal_bytes;
     p.num_seqs = num_seqs;
     p.big_seq = reinterpret_cast<int *>(cws);
@@ -1291,7 +1587,8 @@ extern "C" int pkv_chunk_attention(void *out, const void *q, const void *k_cache
     pcfg.stream = s;
     pcfg.attrs = attr;
     pcfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&pcfg, chunk_plan_kernel, p, G);
+    cudaError_t e = cudaLaunchKernelEx(
+        &pcfg, scored ? chunk_plan_kernel<true> : chunk_plan_kernel<false>, p, G);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_failure(e, "chunk plan launch");
     cudaLaunchConfig_t cfg = {};
@@ -1312,5 +1609,39 @@ extern "C" int pkv_chunk_attention(void *out, const void *q, const void *k_cache
     // tile kernel only before it exits
     b.defer_wait = 1;
     b.active_ctas = p.split;  // its ranges over the SMs the plan left it
-    return dec::launch_balanced(b, z.bal, head_dim, G, false, false, s, z.col_tiles);
+    return dec::launch_balanced(b, z.bal, head_dim, G, false, false, s, z.col_tiles, scored);
+}
+
+}  // namespace
+}  // namespace chunk
+}  // namespace pkv
+
+extern "C" int pkv_chunk_attention(void *out, const void *q, const void *k_cache,
+                                   const void *v_cache, const int32_t *block_tables,
+                                   const int32_t *seq_lens, const int32_t *query_start,
+                                   float scale, int32_t num_heads, int32_t num_kv_heads,
+                                   int32_t head_dim, int32_t block_size, int32_t num_seqs,
+                                   int32_t max_blocks_per_seq, int32_t num_query_tokens,
+                                   int32_t max_query_len, int32_t max_seq_len,
+                                   int64_t num_blocks, void *workspace, size_t workspace_bytes,
+                                   pkv_stream_t stream) {
+    return pkv::chunk::chunk_attention(out, q, k_cache, v_cache, block_tables, seq_lens,
+                                       query_start, scale, num_heads, num_kv_heads, head_dim,
+                                       block_size, num_seqs, max_blocks_per_seq, num_query_tokens,
+                                       max_query_len, max_seq_len, num_blocks, workspace,
+                                       workspace_bytes, false, nullptr, stream);
+}
+
+extern "C" int pkv_chunk_attention_scored(
+    void *out, const void *q, const void *k_cache, const void *v_cache,
+    const int32_t *block_tables, const int32_t *seq_lens, const int32_t *query_start, float scale,
+    int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+    int32_t num_seqs, int32_t max_blocks_per_seq, int32_t num_query_tokens, int32_t max_query_len,
+    int32_t max_seq_len, int64_t num_blocks, void *workspace, size_t workspace_bytes,
+    const pkv_score_rules *rules, pkv_stream_t stream) {
+    return pkv::chunk::chunk_attention(out, q, k_cache, v_cache, block_tables, seq_lens,
+                                       query_start, scale, num_heads, num_kv_heads, head_dim,
+                                       block_size, num_seqs, max_blocks_per_seq, num_query_tokens,
+                                       max_query_len, max_seq_len, num_blocks, workspace,
+                                       workspace_bytes, true, rules, stream);
 }

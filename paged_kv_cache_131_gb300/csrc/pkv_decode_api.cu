@@ -55,8 +55,105 @@ int check_decode_args(const void *out, const void *q, const void *k_cache, const
     return PKV_OK;
 }
 
+int make_rules(const pkv_score_rules *rules, float scale, RuleParams *out) {
+    if (rules == nullptr) return PKV_ERR_NULL;
+    if (!std::isfinite(rules->softcap) || rules->softcap < 0.f || rules->window < 0)
+        return PKV_ERR_INVALID;
+    if (!aligned(rules->slopes, 4) || !aligned(rules->prefix_lens, 4)) return PKV_ERR_ALIGNMENT;
+    out->cap_log2 = out->cap_scale = 0.f;
+    if (rules->softcap > 0.f) {
+        const double cap = rules->softcap;
+        out->cap_log2 = static_cast<float>(cap * 1.4426950408889634);
+        out->cap_scale = static_cast<float>(static_cast<double>(scale) / cap);
+        if (!std::isfinite(out->cap_log2) || !std::isfinite(out->cap_scale))
+            return PKV_ERR_INVALID;
+    }
+    out->window = rules->window > 0 ? rules->window : INT32_MAX;
+    out->slopes = rules->slopes;
+    out->prefix_lens = rules->prefix_lens;
+    return PKV_OK;
+}
+
+namespace {
+
+// Decode under score rules over fp16 or (scales given) FP8 caches.
+int decode_scored(void *out, const void *q, const void *k_cache, const void *v_cache, bool fp8,
+                  const float *k_scale, const float *v_scale, const int32_t *block_tables,
+                  const int32_t *seq_lens, float scale, int32_t num_heads, int32_t num_kv_heads,
+                  int32_t head_dim, int32_t block_size, int32_t num_seqs,
+                  int32_t max_blocks_per_seq, int32_t max_seq_len, int64_t num_blocks,
+                  void *workspace, size_t workspace_bytes, const pkv_score_rules *rules,
+                  cudaStream_t stream) {
+    if (num_seqs == 0) return PKV_OK;
+    if (num_seqs > 0 && fp8 && (!k_scale || !v_scale)) return PKV_ERR_NULL;
+    int st = check_decode_args(out, q, k_cache, v_cache, block_tables, seq_lens, scale, num_heads,
+                               num_kv_heads, head_dim, block_size, num_seqs, max_blocks_per_seq,
+                               max_seq_len, num_blocks);
+    if (st != PKV_OK) return st;
+    BalancedParams p{};
+    st = make_rules(rules, scale, &p.rules);
+    if (st != PKV_OK) return st;
+    if ((fp8 && (!aligned(k_scale, 16) || !aligned(v_scale, 16))) ||
+        (workspace != nullptr && !aligned(workspace, 16)))
+        return PKV_ERR_ALIGNMENT;
+    if (!balanced_fits_index(num_seqs, max_blocks_per_seq)) return PKV_ERR_UNSUPPORTED;
+    const int G = num_heads / num_kv_heads;
+    const BalancedShape shape =
+        balanced_shape(num_seqs, num_kv_heads, G, head_dim, sm_count(), fp8, 0, true);
+    if (!shape.ok) return PKV_ERR_UNSUPPORTED;
+    if (workspace == nullptr || static_cast<int64_t>(workspace_bytes) < shape.workspace)
+        return PKV_ERR_WORKSPACE;
+    p.out = static_cast<__half *>(out);
+    p.q = static_cast<const __half *>(q);
+    p.k_cache = static_cast<const __half *>(k_cache);  // (FP8: bytes, read as such)
+    p.v_cache = static_cast<const __half *>(v_cache);
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    p.num_seqs = num_seqs;
+    p.num_heads = num_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.num_blocks = num_blocks;
+    st = setup_balanced(p, shape, G, workspace, k_cache, v_cache);
+    if (st != PKV_OK) return st;
+    p.err = device_error_record();
+    if (p.err == nullptr) return PKV_ERR_CUDA;
+    return launch_balanced(p, shape, head_dim, G, false, fp8, stream, 0, true);
+}
+
+}  // namespace
+
 }  // namespace dec
 }  // namespace pkv
+
+extern "C" int pkv_decode_attention_scored(
+    void *out, const void *q, const void *k_cache, const void *v_cache,
+    const int32_t *block_tables, const int32_t *seq_lens, float scale, int32_t num_heads,
+    int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_seqs,
+    int32_t max_blocks_per_seq, int32_t max_seq_len, int64_t num_blocks, void *workspace,
+    size_t workspace_bytes, const pkv_score_rules *rules, pkv_stream_t stream) {
+    return pkv::dec::decode_scored(out, q, k_cache, v_cache, false, nullptr, nullptr, block_tables,
+                                   seq_lens, scale, num_heads, num_kv_heads, head_dim, block_size,
+                                   num_seqs, max_blocks_per_seq, max_seq_len, num_blocks,
+                                   workspace, workspace_bytes, rules,
+                                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int pkv_decode_attention_scored_fp8(
+    void *out, const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+    const float *v_scale, const int32_t *block_tables, const int32_t *seq_lens, float scale,
+    int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+    int32_t num_seqs, int32_t max_blocks_per_seq, int32_t max_seq_len, int64_t num_blocks,
+    void *workspace, size_t workspace_bytes, const pkv_score_rules *rules, pkv_stream_t stream) {
+    return pkv::dec::decode_scored(out, q, k_cache, v_cache, true, k_scale, v_scale, block_tables,
+                                   seq_lens, scale, num_heads, num_kv_heads, head_dim, block_size,
+                                   num_seqs, max_blocks_per_seq, max_seq_len, num_blocks,
+                                   workspace, workspace_bytes, rules,
+                                   reinterpret_cast<cudaStream_t>(stream));
+}
 
 extern "C" {
 

@@ -29,6 +29,7 @@ namespace dec {
 
 constexpr int kBS = 16;  // tokens per physical block on the decode path
 constexpr float kNegInf = -INFINITY;
+constexpr float kLog2e = 1.44269504088896341f;
 
 // Where byte b of token t's row sits in a staged tile.  The tensor copy
 // stores the tile chunk-major -- chunk c (bytes [c*C, (c+1)*C) of every row)
@@ -48,6 +49,131 @@ struct SwizzledTile {
 };
 
 // ---------------------------------------------------------------------------
+// Score rules (pkv_score_rules) as a policy applies them, everything in the
+// log2 domain: t = cap * tanh(y), y = scale q.k / cap, then a bias of -slope *
+// distance, then the mask.  tanh(y) = 1 - 2 / (1 + e^(2y)) costs two
+// special-function instructions and is off by a few 2^-24, whose limits (0 and
+// infinity of e^(2y)) come out as -1 and 1; below 1/4 that would be large beside
+// y (a cap far above the scores would swallow them), so there the series
+// y - y^3/3 + 2y^5/15 - 17y^7/315 + 62y^9/2835 is taken (its rest: 2^-27 of y).
+//
+// Softmax weights under rules stand 2^15 higher than 2^(t - max): as fp16 for
+// the P V MMA they keep 11 bits down to 2^-29 of the row's largest, and are off
+// by 2^-40 of it below that.  A capped or biased row can spread much of its
+// mass over many small weights, which a reference of 1 rounds to zero.
+constexpr float kRuleShift = 15.f;
+
+struct BlockRules {
+    int kp;           // position of the block's first key
+    int prefix;       // positions below are seen
+    int window;       // 0x7fffffff: none
+    int qpos;         // the (first) query token's position
+    float cap_log2;   // softcap * log2(e), 0: not capped
+    float cap_scale;  // scale / softcap
+};
+
+__device__ __forceinline__ float rule_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float rule_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A raw score q.k capped (in log2 units).
+__device__ __forceinline__ float capped_score(float raw, float cap_log2, float cap_scale) {
+    const float y = raw * cap_scale, y2 = y * y;
+    const float far = fmaf(-2.f, rule_rcp(1.f + rule_ex2(y * (2.f * kLog2e))), 1.f);
+    float near = fmaf(y2, 62.f / 2835.f, -17.f / 315.f);
+    near = fmaf(y2, near, 2.f / 15.f);
+    near = fmaf(y2, near, -1.f / 3.f);
+    near = fmaf(y * y2, near, y);
+    return cap_log2 * (fabsf(y) < 0.25f ? near : far);
+}
+
+// A raw score under the rules, before the mask; slope in log2 units.
+__device__ __forceinline__ float ruled_score(float raw, float scale_log2, const BlockRules &br,
+                                             float slope, int distance) {
+    const float t = br.cap_log2 > 0.f ? capped_score(raw, br.cap_log2, br.cap_scale)
+                                      : raw * scale_log2;
+    return fmaf(-slope, fabsf(static_cast<float>(distance)), t);
+}
+
+// Whether the token at position a sees the key at position b (b < L).
+__device__ __forceinline__ bool rule_sees(int a, int b, int window, int prefix) {
+    return (b <= a && a - b < window) || b < prefix;
+}
+
+// Bits of the block's nv keys that the token at br.qpos sees (every lane).
+__device__ __forceinline__ uint32_t seen_keys(const BlockRules &br, int nv, int lane) {
+    return __ballot_sync(0xffffffffu,
+                         lane < nv && rule_sees(br.qpos, br.kp + lane, br.window, br.prefix));
+}
+
+__device__ __forceinline__ void lds128(uint32_t (&w)[4], uint32_t addr) {
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr));
+}
+
+__device__ __forceinline__ float lds_half(uint32_t addr) {
+    unsigned short u;
+    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(u) : "r"(addr));
+    return __half2float(__ushort_as_half(u));
+}
+
+// Whether one head's fp16 slice of value rows [0, nv) holds an infinity or a NaN
+// (every lane).
+template <int D>
+__device__ __noinline__ bool any_non_finite(uint32_t vb, SwizzledTile tile, uint32_t head, int nv,
+                                            int lane) {
+    constexpr int kUnits = D / 8;  // 16-byte units of a row's slice
+    bool bad = false;
+    for (int e = lane; e < nv * kUnits; e += 32) {
+        uint32_t w[4];
+        lds128(w, vb + tile.at(e / kUnits, head + (e % kUnits) * 16));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            bad = bad || (w[i] & 0x7C00u) == 0x7C00u || (w[i] & 0x7C000000u) == 0x7C000000u;
+    }
+    return __any_sync(0xffffffffu, bad);
+}
+
+// Zeroes those elements, ordered before later bulk copies into the stage.
+template <int D>
+__device__ __noinline__ void zero_non_finite(uint32_t vb, SwizzledTile tile, uint32_t head, int nv,
+                                             int lane) {
+    constexpr int kUnits = D / 8;
+    for (int e = lane; e < nv * kUnits; e += 32) {
+        const uint32_t at = vb + tile.at(e / kUnits, head + (e % kUnits) * 16);
+        uint32_t w[4];
+        lds128(w, at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if ((w[i] & 0x7C00u) == 0x7C00u) w[i] &= 0xFFFF0000u;
+            if ((w[i] & 0x7C000000u) == 0x7C000000u) w[i] &= 0xFFFFu;
+        }
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3])
+                     : "memory");
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
+// What a policy keeps per column (softmax state) under rules.
+template <bool kRules, int N>
+struct RuleColumns {};
+template <int N>
+struct RuleColumns<true, N> {
+    float slope[N];  // of the column's head, log2 units
+};
+
+// ---------------------------------------------------------------------------
 // MMA policy (fp16 tiles, m16n8k16 MMAs with fp32 accumulation), both
 // products transposed so that the 16 MMA rows are tokens or head dims and
 // the G (<= 8) query heads are the 8 columns:
@@ -60,8 +186,9 @@ struct SwizzledTile {
 //     B = the fp16 weights, transposed per 8x8 half by movmatrix.  O^T's
 //     columns are the same two heads.
 
-template <int D, int G>
+template <int D, int G, bool kRules = false>
 struct MmaPolicy {
+    static constexpr bool kScored = kRules;
     static constexpr bool kColumns = false;  // columns = the G heads of one new token
     static constexpr int kRows = G;          // partial-state rows per (sequence, kv head)
     static constexpr int KS = D / 16;  // k-steps of S^T (16 head dims each)
@@ -72,6 +199,7 @@ struct MmaPolicy {
     // the same dims of head 2t+1 (g = lane/4, t = lane%4)
     float o[MT][4];
     float m[2], l[2];  // softmax state of heads 2t, 2t+1 (l: this lane's tokens)
+    RuleColumns<kRules, 2> rc;
 
     __device__ __forceinline__ void init(const __half *qg, float /*scale_log2*/, int lane) {
         const int g = lane >> 2, tig = lane & 3;
@@ -97,7 +225,7 @@ struct MmaPolicy {
     // must hold finite numbers.
     __device__ __forceinline__ void block(uint32_t kb, uint32_t vb, SwizzledTile tile,
                                           uint32_t head, int nv, float scale_log2, int lane,
-                                          float * /*pbuf*/) {
+                                          float * /*pbuf*/, const BlockRules &br = {}) {
         const int g = lane >> 2;
         // S^T = K Q^T; ldmatrix matrices: tokens 0-7 / 8-15 (rows g / g+8 of
         // A) at dims 0-7, then the same at dims 8-15; two accumulator chains
@@ -119,7 +247,14 @@ struct MmaPolicy {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int tok = g + 8 * (j >> 1);
-            x[j] = tok < nv ? (sa[j] + sb[j]) * scale_log2 : kNegInf;
+            if constexpr (kRules) {
+                const int d = br.qpos - br.kp - tok;
+                const float v = ruled_score(sa[j] + sb[j], scale_log2, br, rc.slope[j & 1], d);
+                x[j] = tok < nv && rule_sees(br.qpos, br.kp + tok, br.window, br.prefix) ? v
+                                                                                         : kNegInf;
+            } else {
+                x[j] = tok < nv ? (sa[j] + sb[j]) * scale_log2 : kNegInf;
+            }
             mx[j & 1] = fmaxf(mx[j & 1], x[j]);
         }
 #pragma unroll
@@ -128,16 +263,24 @@ struct MmaPolicy {
             mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 8));
             mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 16));
         }
-        float alpha[2];
+        float alpha[2], ref[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const float mnew = fmaxf(m[h], mx[h]);  // finite: nv >= 1
-            alpha[h] = exp2f(m[h] - mnew);
+            if constexpr (kRules) {
+                // (scores that are all minus infinity: no weight)
+                const float safe = mnew == kNegInf ? 0.f : mnew;
+                alpha[h] = exp2f(m[h] - safe);
+                ref[h] = safe - kRuleShift;
+            } else {
+                alpha[h] = exp2f(m[h] - mnew);
+                ref[h] = mnew;
+            }
             m[h] = mnew;
         }
         // weights rows = tokens 0-7 / 8-15, columns = heads
-        const uint32_t p0 = pack_half2(exp2f(x[0] - m[0]), exp2f(x[1] - m[1]));
-        const uint32_t p1 = pack_half2(exp2f(x[2] - m[0]), exp2f(x[3] - m[1]));
+        const uint32_t p0 = pack_half2(exp2f(x[0] - ref[0]), exp2f(x[1] - ref[1]));
+        const uint32_t p1 = pack_half2(exp2f(x[2] - ref[0]), exp2f(x[3] - ref[1]));
         // the normaliser sums the same fp16-rounded weights the MMA applies
         const float2 u0 = unpack_half2(p0), u1 = unpack_half2(p1);
         l[0] = l[0] * alpha[0] + (u0.x + u1.x);
@@ -159,6 +302,17 @@ struct MmaPolicy {
             uint32_t a0, a1, a2, a3;
             ldsm_x4_trans(a0, a1, a2, a3, vb + tile.at(vt, vcol + mt * 32));
             mma_16816(o[mt], a0, a1, a2, a3, pb0, pb1);
+        }
+    }
+
+    // The slopes of this lane's columns (slopes: the group's, fp32, or null).
+    __device__ __forceinline__ void init_rules(const float *slopes, int lane) {
+        if constexpr (kRules) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int hd = 2 * (lane & 3) + h;
+                rc.slope[h] = slopes != nullptr && hd < G ? __ldg(slopes + hd) * kLog2e : 0.f;
+            }
         }
     }
 
@@ -250,8 +404,9 @@ struct QueryRows {
     int lim0;         // last key position token 0 sees: L - Q
 };
 
-template <int D, int G, int NT>
+template <int D, int G, int NT, bool kRules = false>
 struct MmaColsPolicy {
+    static constexpr bool kScored = kRules;
     static constexpr bool kColumns = true;
     static constexpr int kRows = 8 * NT;  // partial-state rows (columns) per (sequence, kv head)
     static constexpr bool kZeroTailRows = true;
@@ -263,6 +418,7 @@ struct MmaColsPolicy {
     float o[NT][MT][4];
     float m[NT][2], l[NT][2];  // softmax state of columns 8c + 2t + h
     int lim[NT][2];            // last key position of those columns (-1: no column)
+    RuleColumns<kRules, NT * 2> rc;
 
     __device__ __forceinline__ void init(const QueryRows &qr, int lane) {
         const int g = lane >> 2, t = lane & 3;
@@ -299,7 +455,7 @@ struct MmaColsPolicy {
     // value tile at vb, this head's bytes from `head`; nv valid tokens.
     __device__ __forceinline__ void block(uint32_t kb, uint32_t vb, SwizzledTile tile,
                                           uint32_t head, int nv, int kp, float scale_log2,
-                                          int lane) {
+                                          int lane, const BlockRules &br = {}) {
         const int g = lane >> 2;
         const int rt = ((lane >> 3) & 1) * 8 + (lane & 7);
         const uint32_t kcol = head + (lane >> 4) * 16;
@@ -330,8 +486,15 @@ struct MmaColsPolicy {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int tok = g + 8 * (e >> 1);
-                const bool vis = tok < nv && kp + tok <= lim[c][e & 1];
-                x[c][e] = vis ? (sa[c][e] + sb[c][e]) * scale_log2 : kNegInf;
+                if constexpr (kRules) {
+                    const int a = lim[c][e & 1];
+                    const float v = ruled_score(sa[c][e] + sb[c][e], scale_log2, br,
+                                                rc.slope[2 * c + (e & 1)], a - kp - tok);
+                    x[c][e] = tok < nv && sees(c, e & 1, kp + tok, br) ? v : kNegInf;
+                } else {
+                    const bool vis = tok < nv && kp + tok <= lim[c][e & 1];
+                    x[c][e] = vis ? (sa[c][e] + sb[c][e]) * scale_log2 : kNegInf;
+                }
                 mx[c][e & 1] = fmaxf(mx[c][e & 1], x[c][e]);
             }
         }
@@ -348,6 +511,7 @@ struct MmaColsPolicy {
                 // a column with no visible key yet keeps m = -inf, l = 0, o = 0
                 msafe[c][h] = mnew == kNegInf ? 0.f : mnew;
                 alpha[c][h] = exp2f(m[c][h] - msafe[c][h]);
+                if constexpr (kRules) msafe[c][h] -= kRuleShift;
                 m[c][h] = mnew;
             }
         uint32_t pb[NT][2];
@@ -378,6 +542,52 @@ struct MmaColsPolicy {
 #pragma unroll
             for (int c = 0; c < NT; ++c) mma_16816(o[c][mt], a0, a1, a2, a3, pb[c][0], pb[c][1]);
         }
+    }
+
+    // Whether column 8c + 2t + h sees position b (b below the sequence's end).
+    __device__ __forceinline__ bool sees(int c, int h, int b, const BlockRules &br) const {
+        const int a = lim[c][h];
+        return a >= 0 && rule_sees(a, b, br.window, br.prefix);
+    }
+
+    __device__ __forceinline__ void init_rules(const QueryRows &qr, const float *slopes,
+                                               int lane) {
+        if constexpr (kRules) {
+#pragma unroll
+            for (int i = 0; i < NT * 2; ++i) {
+                const int col = 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
+                rc.slope[i] = slopes != nullptr && col < qr.ncols
+                                  ? __ldg(slopes + qr.kvh * G + col % G) * kLog2e
+                                  : 0.f;
+            }
+        }
+    }
+
+    // A block that some column does not see whole: a masked weight is 0, but 0
+    // times an infinity or a NaN is not, so the value rows' elements that are
+    // not finite are zeroed in the tile and added to the columns that see them
+    // (their weight, however small, leaves such an element what it is).  The
+    // checks are calls, so that the state stays in registers.
+    __device__ __forceinline__ void clean_values(uint32_t vb, SwizzledTile tile, uint32_t head,
+                                                 int nv, const BlockRules &br, int lane) {
+        if (!any_non_finite<D>(vb, tile, head, nv, lane)) return;
+        const int g = lane >> 2;
+#pragma unroll 1
+        for (int tok = 0; tok < nv; ++tok)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float v = lds_half(vb + tile.at(tok, head + (16 * mt + g + 8 * i) * 2));
+                    if (isfinite(v)) continue;
+#pragma unroll
+                    for (int c = 0; c < NT; ++c)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            if (sees(c, h, br.kp + tok, br)) o[c][mt][2 * i + h] += v;
+                }
+        __syncwarp();
+        zero_non_finite<D>(vb, tile, head, nv, lane);
     }
 
     __device__ __forceinline__ float l_total(int c, int h) const {
@@ -473,19 +683,22 @@ __device__ __forceinline__ uint32_t byte_perm(uint32_t x, uint32_t sel) {
     return r;
 }
 
-template <int D, int G>
+template <int D, int G, bool kRules = false>
 struct MmaFp8Policy {
+    static constexpr bool kScored = kRules;
     static constexpr bool kColumns = false;
     static constexpr int kRows = G;
     static constexpr int KS = D / 16;  // k-steps of S^T = K Q^T
     static constexpr int MT = D / 16;  // m-tiles (16 head dims each) of O^T
     static constexpr int kLaneTokens = 2;  // tokens whose scales a lane needs per block
-    static constexpr float kWeightBoost = 256.f;  // exact; removed on output
+    // exact; removed on output (under rules the weights' reference does its work)
+    static constexpr float kWeightBoost = kRules ? 1.f : 256.f;
     uint32_t qb[KS][2];  // B operand of S^T: query dims of head l/4
     // O^T, m-tile mt: c0 / c2 = dims 16mt + 2g / +1 of head 2t, c1 / c3 the
     // same dims of head 2t+1 (g = lane/4, t = lane%4)
     float o[MT][4];
     float m[2], l[2];  // online-softmax state of heads 2t, 2t+1 (l: this lane's tokens)
+    RuleColumns<kRules, 2> rc;
 
     // Token of this lane's i-th score row (i = 0, 1).
     __device__ __forceinline__ static int token_of(int lane, int i) { return (lane >> 2) + 8 * i; }
@@ -509,6 +722,16 @@ struct MmaFp8Policy {
         l[0] = l[1] = 0.f;
     }
 
+    __device__ __forceinline__ void init_rules(const float *slopes, int lane) {
+        if constexpr (kRules) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int hd = 2 * (lane & 3) + h;
+                rc.slope[h] = slopes != nullptr && hd < G ? __ldg(slopes + hd) * kLog2e : 0.f;
+            }
+        }
+    }
+
     // NB (1 or 2) staged blocks of one sequence in one online-softmax step.
     // kb8 / vb8: the key / value code tiles of each block, this head's codes
     // starting at byte `head` of each row; value rows >= nv must hold finite
@@ -519,7 +742,8 @@ struct MmaFp8Policy {
                                          SwizzledTile tile, uint32_t head, const int (&nv)[NB],
                                          float scale_log2, int lane,
                                          const float (&ks)[NB][kLaneTokens],
-                                         const float (&vs)[NB][kLaneTokens]) {
+                                         const float (&vs)[NB][kLaneTokens],
+                                         const BlockRules *br = nullptr) {
         // matrices 0/1: tokens 0-7 / 8-15, codes 0-15 of a 32-code step;
         // 2/3: the same for codes 16-31
         const int rt = ((lane >> 3) & 1) * 8 + (lane & 7);
@@ -544,14 +768,34 @@ struct MmaFp8Policy {
             for (int j = 0; j < 4; ++j) x[b][j] = sa[j] + sb[j];
         }
         // scale, mask, and the block max of each of the lane's two heads
+        float lv[NB][kLaneTokens];  // log2 of the value scales (bounded below: a zero has none)
+        if constexpr (kRules) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int r = 0; r < kLaneTokens; ++r) lv[b][r] = fmaxf(__log2f(vs[b][r]), -64.f);
+        }
         float mx[2] = {kNegInf, kNegInf};
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int r = j >> 1;  // token row: g or g+8
-                x[b][j] = token_of(lane, r) < nv[b] ? (x[b][j] * ks[b][r]) * scale_log2 : kNegInf;
-                mx[j & 1] = fmaxf(mx[j & 1], x[b][j]);
+                if constexpr (kRules) {
+                    // the reference follows the largest product of weight and value
+                    // scale, so that product fits fp16 whatever the scales are
+                    const int tok = token_of(lane, r);
+                    const BlockRules &w = br[b];
+                    const float v = ruled_score(x[b][j] * ks[b][r], scale_log2, w, rc.slope[j & 1],
+                                                w.qpos - w.kp - tok);
+                    const bool vis = tok < nv[b] &&
+                                     rule_sees(w.qpos, w.kp + tok, w.window, w.prefix);
+                    x[b][j] = vis ? v : kNegInf;
+                    mx[j & 1] = fmaxf(mx[j & 1], x[b][j] + lv[b][r]);
+                } else {
+                    x[b][j] = token_of(lane, r) < nv[b] ? (x[b][j] * ks[b][r]) * scale_log2 : kNegInf;
+                    mx[j & 1] = fmaxf(mx[j & 1], x[b][j]);
+                }
             }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -559,11 +803,18 @@ struct MmaFp8Policy {
             mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 8));
             mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 16));
         }
-        float alpha[2];
+        float alpha[2], ref[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const float mnew = fmaxf(m[h], mx[h]);  // finite: some token is valid
-            alpha[h] = exp2f(m[h] - mnew);
+            if constexpr (kRules) {
+                const float safe = mnew == kNegInf ? 0.f : mnew;
+                alpha[h] = exp2f(m[h] - safe);
+                ref[h] = safe - kRuleShift;
+            } else {
+                alpha[h] = exp2f(m[h] - mnew);
+                ref[h] = mnew;
+            }
             m[h] = mnew;
             l[h] *= alpha[h];
         }
@@ -574,9 +825,10 @@ struct MmaFp8Policy {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int r = j >> 1;
-                const float p = exp2f(x[b][j] - m[j & 1]);
+                const float p = exp2f(x[b][j] - ref[j & 1]);
                 l[j & 1] += p;
-                pw[j] = token_of(lane, r) < nv[b] ? p * (vs[b][r] * kWeightBoost) : 0.f;
+                if constexpr (kRules) pw[j] = x[b][j] == kNegInf ? 0.f : p * vs[b][r];
+                else pw[j] = token_of(lane, r) < nv[b] ? p * (vs[b][r] * kWeightBoost) : 0.f;
             }
             // rows = tokens 0-7 / 8-15, columns = heads; transposed to
             // (token pair, head) B fragments
@@ -689,6 +941,7 @@ struct ReduceScatter<1, H> {
 
 template <int D, int G>
 struct SimtPolicy {
+    static constexpr bool kScored = false;
     static constexpr bool kColumns = false;
     static constexpr int kRows = G;
     static constexpr int DPL = D / 32;                        // dims per lane: 4 or 2
@@ -858,6 +1111,21 @@ __device__ __forceinline__ void zero_tail_bytes(uint32_t vb, SwizzledTile tile, 
     constexpr int kUnits = ROW_BYTES / 16;
     for (int e = lane; e < (kBS - nv) * kUnits; e += 32) {
         const uint32_t a = vb + tile.at(nv + e / kUnits, head + (e % kUnits) * 16);
+        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(a), "r"(0u) : "memory");
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
+// Zero bytes [head, head + ROW_BYTES) of the value rows whose bit in `seen` is
+// not set, as above.
+template <int ROW_BYTES>
+__device__ __forceinline__ void zero_unseen_rows(uint32_t vb, SwizzledTile tile, uint32_t head,
+                                                 uint32_t seen, int lane) {
+    constexpr int kUnits = ROW_BYTES / 16;
+    for (int e = lane; e < kBS * kUnits; e += 32) {
+        if ((seen >> (e / kUnits)) & 1u) continue;
+        const uint32_t a = vb + tile.at(e / kUnits, head + (e % kUnits) * 16);
         asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(a), "r"(0u) : "memory");
     }
     fence_proxy_async_smem();

@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "../../include/pagedkv.h"
+
 namespace pkv {
 
 struct ErrorRecord;
@@ -74,6 +76,19 @@ int64_t grid_workspace_bytes(int64_t S, int64_t H, int64_t D, int64_t P);
 int launch_grid(const GridParams &p, int D, int G, bool simt, int num_seqs,
                 cudaStream_t stream);
 
+// Score rules (pkv_score_rules) as the kernels take them: log2 units, and a
+// window of 2^31 - 1 where there is none.
+struct RuleParams {
+    float cap_log2;   // softcap * log2(e); 0: not capped
+    float cap_scale;  // scale / softcap
+    int window;
+    const float *slopes;
+    const int32_t *prefix_lens;
+};
+
+// Argument checks of the rules and their device form.  Returns a PKV status.
+int make_rules(const pkv_score_rules *rules, float scale, RuleParams *out);
+
 // Balanced schedule.
 struct BalancedParams {
     CUtensorMap tm_k;  // whole-row boxes of the key / value caches
@@ -116,6 +131,7 @@ struct BalancedParams {
     float2 *part_ml;  // [2 * grid][heads_per_cta][rows]
     float *part_o;    // [2 * grid][heads_per_cta][rows][D]
     ErrorRecord *err;
+    RuleParams rules;  // used by the kernels under score rules only
 };
 
 struct BalancedShape {
@@ -132,8 +148,10 @@ struct BalancedShape {
 
 // Shape of the balanced launch for fp16 or FP8 caches; rows = partial-state
 // rows per (sequence, kv head): G for decode, 8 * col_tiles for chunks.
+// scored: under score rules (two more words of shared memory per sequence, so
+// never a larger grid or workspace than without).
 BalancedShape balanced_shape(int num_seqs, int num_kv_heads, int G, int D, int num_sms,
-                             bool fp8, int rows = 0);
+                             bool fp8, int rows = 0, bool scored = false);
 // Sets the fields of p that follow from the shape -- ring depth, staged row,
 // head groups, the scratch layout inside `workspace` (counters, partial
 // states for `rows` rows per (sequence, kv head)) and the tensor maps of the
@@ -142,8 +160,13 @@ BalancedShape balanced_shape(int num_seqs, int num_kv_heads, int G, int D, int n
 int setup_balanced(BalancedParams &p, const BalancedShape &shape, int rows, void *workspace,
                    const void *k_cache, const void *v_cache);
 // col_tiles: 0 for decode, else the column n-tiles (1 or 2) of MmaColsPolicy.
+// scored: under p.rules.
 int launch_balanced(const BalancedParams &p, const BalancedShape &shape, int D, int G, bool simt,
-                    bool fp8, cudaStream_t stream, int col_tiles = 0);
+                    bool fp8, cudaStream_t stream, int col_tiles = 0, bool scored = false);
+
+using BalancedFn = void (*)(const BalancedParams);
+// The kernel under score rules of a shape (pkv_decode_balanced_rules.cu), or null.
+BalancedFn select_balanced_rules(int D, int G, bool fp8, int col_tiles);
 
 inline int64_t align256(int64_t x) { return (x + 255) & ~int64_t(255); }
 

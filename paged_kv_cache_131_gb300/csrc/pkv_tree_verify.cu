@@ -1,0 +1,448 @@
+// pkv_tree_verify.cu -- verification of drafted trees against the target's
+// probabilities from given random numbers (pkv_tree_verify).
+//
+// At a node with target p and drafts q, child after child is accepted with
+// probability min(1, r/q), r being the normalised rest of the target that the
+// rejections so far have left: r_0 = p, r_{j+1} = norm(max(r_j - q, 0)).  Without
+// the norm, R_{j+1} = max(R_j - W_j q, 0) with W_j = sum R_j, and since
+// max(max(a, 0) - b, 0) = max(a - b, 0) for b >= 0, R_j = max(p - C_j q, 0) with
+// C_j = W_0 + .. + W_{j-1}: a rejection is one number and one sum over the row,
+// whatever came before it, and nothing of the row is kept or written.
+//
+// One cluster of CTAs per sequence; every warp of it walks the tree alike (the
+// nodes' probabilities are gathered into shared memory once), and all of them sum
+// a row when a child is rejected or the next token is drawn: each warp a stretch
+// of its CTA's share, the CTAs' sums exchanged through distributed shared memory.
+// The draw finds the CTA, then the warp, and that warp goes through its stretch
+// again (out of L2).
+//
+// Sums: an element of R is one fused multiply-add of the row's fp32 values (C as
+// a pair of fp32: one rounding), and a thread adds its elements into a pair of
+// fp32 (the error of each addition kept), which loses nothing that 64 bits would
+// hold; threads, warps and CTAs are added in fp64.  fp64 per element would take
+// longer than the row's bytes: this GPU's fp64 rate is 2 per cycle and SM.
+// Bound: HBM for many sequences (the rows of p and q), latency for few.
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "../../include/pagedkv.h"
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kMaxNodes = PKV_MAX_TREE_NODES;
+constexpr int kNodesPerLane = kMaxNodes / 32;
+constexpr unsigned kAll = 0xffffffffu;
+
+struct VerifyParams {
+    int32_t *path;
+    int32_t *path_lens;
+    int32_t *next_tokens;
+    const int32_t *tokens;
+    const int32_t *parents;
+    const int32_t *query_start;
+    const float *target;
+    const float *draft;
+    int64_t target_stride;
+    int64_t draft_stride;
+    const float *accept_u;
+    const float *sample_u;
+    int max_depth;
+    int num_nodes;
+    int vocab;
+    ErrorRecord *err;
+};
+
+// A uniform number as the nearest of [0, 1).
+__device__ __forceinline__ float unit(float u) {
+    return fminf(fmaxf(u, 0.f), 0.99999994f);  // 1 - 2^-24
+}
+
+// The rest of the target at a node.
+struct Rest {
+    const float *p;       // target row
+    const float *q;       // drafts' row, or null
+    float c_hi, c_lo;     // C
+    const int *gone;      // without drafts' rows: rejected tokens
+    int num_gone;
+};
+
+// Its element at index i.
+__device__ __forceinline__ float rest_of(const Rest &r, float p, float q) {
+    q = fmaxf(q, 0.f);  // (the maximum of a NaN and 0 is 0)
+    return fmaxf(fmaf(-r.c_lo, q, fmaf(-r.c_hi, q, p)), 0.f);
+}
+
+// Elements i .. i + 3 (0 outside [0, vocab)), by 16-byte loads where `vec`
+// (both rows have element i at a 16-byte boundary).
+__device__ __forceinline__ void load_rest(const Rest &r, int i, int vocab, bool vec,
+                                          float (&x)[4]) {
+    float p[4], q[4];
+    if (vec && i >= 0 && i + 4 <= vocab) {
+        const float4 a = __ldg(reinterpret_cast<const float4 *>(r.p + i));
+        p[0] = a.x; p[1] = a.y; p[2] = a.z; p[3] = a.w;
+        if (r.q != nullptr) {
+            const float4 b = __ldg(reinterpret_cast<const float4 *>(r.q + i));
+            q[0] = b.x; q[1] = b.y; q[2] = b.z; q[3] = b.w;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const bool in = i + k >= 0 && i + k < vocab;
+            p[k] = in ? __ldg(r.p + i + k) : 0.f;
+            q[k] = in && r.q != nullptr ? __ldg(r.q + i + k) : 0.f;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = r.q != nullptr ? rest_of(r, p[k], q[k]) : fmaxf(p[k], 0.f);
+    if (r.num_gone != 0)
+        for (int g = 0; g < r.num_gone; ++g)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (r.gone[g] == i + k) x[k] = 0.f;
+}
+
+// s + e += x, the rounding error of s kept in e.
+__device__ __forceinline__ void add_pair(float &s, float &e, float x) {
+    const float t = __fadd_rn(s, x);
+    const float b = __fsub_rn(t, s);
+    e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(x, b)));
+    s = t;
+}
+
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+}
+
+__global__ void __launch_bounds__(kThreads)
+    tree_verify_kernel(const __grid_constant__ VerifyParams p) {
+    // per node: its token's probability under its parent's target and drafts
+    __shared__ float node_p[kMaxNodes], node_q[kMaxNodes], node_u[kMaxNodes];
+    __shared__ int node_token[kMaxNodes];
+    __shared__ int gone[kMaxNodes];
+    __shared__ double warp_part[2][kWarps];       // this CTA's warps, by parity of the pass
+    __shared__ double cta_part[2][kMaxCluster];   // every CTA's sum, written by it
+    auto cluster = cooperative_groups::this_cluster();
+    const int cta = static_cast<int>(cluster.block_rank());
+    const int ctas = static_cast<int>(cluster.num_blocks());
+    const int seq = static_cast<int>(blockIdx.x) / ctas;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int V = p.vocab;
+    const bool drafted = p.draft != nullptr;
+
+    grid_dependency_wait();
+    const int row0 = __ldg(p.query_start + seq), row1 = __ldg(p.query_start + seq + 1);
+    int Q = row1 - row0;
+    if (row0 < 0 || row1 > p.num_nodes || Q < 0 || Q > kMaxNodes) {
+        if (cta == 0 && threadIdx.x == 0) record_error(p.err, PKV_DEVERR_SEQ_LEN, seq);
+        Q = 0;
+    }
+    int32_t *path = p.path + static_cast<int64_t>(seq) * p.max_depth;
+    if (Q == 0) {  // (the whole cluster)
+        if (cta == 0) {
+            for (int d = threadIdx.x; d < p.max_depth; d += kThreads) path[d] = -1;
+            if (threadIdx.x == 0) {
+                p.path_lens[seq] = 0;
+                p.next_tokens[seq] = -1;
+            }
+        }
+        return;
+    }
+    for (int k = threadIdx.x; k < Q; k += kThreads) {
+        const int64_t row = row0 + k;
+        const int parent = __ldg(p.parents + row), token = __ldg(p.tokens + row);
+        float a = 0.f, b = 0.f;
+        if (k > 0 && parent >= 0) {
+            if (parent >= k || token < 0 || token >= V) {
+                if (cta == 0) record_error(p.err, PKV_DEVERR_TREE, row);
+            } else {
+                a = __ldg(p.target + (row0 + parent) * p.target_stride + token);
+                if (drafted) b = __ldg(p.draft + (row0 + parent) * p.draft_stride + token);
+            }
+        }
+        node_p[k] = a;
+        node_q[k] = b;
+        node_u[k] = unit(__ldg(p.accept_u + row));
+        node_token[k] = token;
+    }
+    // every warp: the parents, node 32 j + lane in up[j] (-1: never a child)
+    int up[kNodesPerLane];
+#pragma unroll
+    for (int j = 0; j < kNodesPerLane; ++j) {
+        const int k = 32 * j + lane;
+        up[j] = -1;
+        if (k > 0 && k < Q) {
+            const int parent = __ldg(p.parents + row0 + k), token = __ldg(p.tokens + row0 + k);
+            if (parent >= 0 && parent < k && token >= 0 && token < V) up[j] = parent;
+        }
+    }
+    const float draw_u = unit(__ldg(p.sample_u + seq));
+    __syncthreads();
+    // (the first exchange writes other CTAs' shared memory: all have started)
+    cluster.sync();
+
+    int pass = 0;
+    bool vec = false;
+    int first = 0, last = 0;  // this warp's stretch of the row
+    Rest r{};
+    // Points r at node `at`'s rows with nothing rejected.
+    auto open = [&](int at) {
+        r.p = p.target + (row0 + at) * p.target_stride;
+        r.q = nullptr;
+        r.c_hi = r.c_lo = 0.f;
+        r.gone = gone;
+        r.num_gone = 0;
+        const uintptr_t pa = reinterpret_cast<uintptr_t>(r.p) & 15;
+        const float *q = drafted ? p.draft + (row0 + at) * p.draft_stride : r.p;
+        vec = pa == (reinterpret_cast<uintptr_t>(q) & 15);
+        // stretches of 128 elements from the 16-byte boundary at or before the row
+        const int skew = static_cast<int>(pa >> 2);
+        const int units = (V + skew + 127) / 128, parts = ctas * kWarps;
+        const int part = cta * kWarps + warp;
+        first = static_cast<int>(static_cast<int64_t>(units) * part / parts) * 128 - skew;
+        last = static_cast<int>(static_cast<int64_t>(units) * (part + 1) / parts) * 128 - skew;
+    };
+    // The sum of the rest over the whole row, the same in every thread of the
+    // cluster; its parts stay in warp_part / cta_part until the pass after next.
+    auto sum_rest = [&]() -> double {
+        float s = 0.f, e = 0.f;
+        for (int i = first + 4 * lane; i < last; i += 128) {
+            float x[4];
+            load_rest(r, i, V, vec, x);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) add_pair(s, e, x[k]);
+        }
+        const double w = warp_sum(static_cast<double>(s) + static_cast<double>(e));
+        const int half = pass & 1;
+        ++pass;
+        if (lane == 0) warp_part[half][warp] = w;
+        __syncthreads();
+        if (static_cast<int>(threadIdx.x) < ctas) {
+            double c = 0.;
+            for (int i = 0; i < kWarps; ++i) c += warp_part[half][i];
+            *cluster.map_shared_rank(&cta_part[half][cta], threadIdx.x) = c;
+        }
+        cluster.sync();
+        double total = 0.;
+        for (int i = 0; i < ctas; ++i) total += cta_part[half][i];
+        return total;
+    };
+
+    // ---- the walk (every warp of the cluster alike)
+    int at = 0, depth = 1;
+    bool summed = false;  // the last pass summed r as it stands
+    double total = 0.;
+    if (cta == 0 && threadIdx.x == 0) path[0] = 0;
+    for (;;) {
+        open(at);
+        summed = false;
+        int step = -1;
+        if (depth < p.max_depth) {
+            double W = 1., C = 0.;
+            bool empty = false;
+            int seen = 0;  // tokens in `gone`
+            for (int j = 0; j < kNodesPerLane && step < 0 && !empty; ++j) {
+                unsigned kids = __ballot_sync(kAll, up[j] == at);
+                while (kids != 0 && step < 0 && !empty) {
+                    const int k = 32 * j + __ffs(kids) - 1;
+                    kids &= kids - 1;
+                    const double u = node_u[k], pt = fmaxf(node_p[k], 0.f);
+                    const double qt = fmaxf(node_q[k], 0.f);
+                    if (drafted) {
+                        if (u * W * qt < fmax(pt - C * qt, 0.)) {
+                            step = k;
+                            break;
+                        }
+                        // rejected: the rest without what the drafts cover
+                        const Rest before = r;
+                        C += W;
+                        r.q = p.draft + (row0 + at) * p.draft_stride;
+                        r.c_hi = static_cast<float>(C);
+                        r.c_lo = static_cast<float>(C - static_cast<double>(r.c_hi));
+                        const double w = sum_rest();
+                        if (w > 0.) {
+                            W = total = w;
+                            summed = true;
+                        } else {
+                            r = before;
+                            summed = false;
+                            empty = true;
+                        }
+                    } else {
+                        // (a guess that was rejected before has nothing left)
+                        bool again = false;
+                        for (int g = 0; g < seen; ++g) again = again || gone[g] == node_token[k];
+                        const double have = again ? 0. : pt;
+                        if (u * W < have) {
+                            step = k;
+                            break;
+                        }
+                        if (W - have <= 0.) {
+                            empty = true;
+                        } else {
+                            W -= have;
+                            if (!again) {
+                                // every warp has read the list up to here
+                                __syncthreads();
+                                if (threadIdx.x == 0) gone[seen] = node_token[k];
+                                __syncthreads();
+                                ++seen;
+                                r.num_gone = seen;
+                            }
+                        }
+                    }
+                }
+            }
+        }
+        if (step < 0) break;
+        if (cta == 0 && threadIdx.x == 0) path[depth] = step;
+        ++depth;
+        at = step;
+    }
+
+    // ---- the next token
+    if (!summed) total = sum_rest();
+    const int half = (pass - 1) & 1;
+    if (cta == 0) {
+        for (int d = depth + threadIdx.x; d < p.max_depth; d += kThreads) path[d] = -1;
+        if (threadIdx.x == 0) p.path_lens[seq] = depth;
+    }
+    if (!(total > 0.)) {
+        if (cta == 0 && threadIdx.x == 0) p.next_tokens[seq] = -1;
+        return;
+    }
+    // the CTA, then the warp, in whose share the running sum passes u * total; the
+    // last one with any mass where rounding leaves it past the end
+    const double goal = static_cast<double>(draw_u) * total;
+    double base = 0., base_in = 0.;
+    int c = -1;
+    for (int i = 0; i < ctas; ++i) {
+        const double x = cta_part[half][i];
+        if (x > 0. && base_in <= goal) {  // (base_in: the sum before this share)
+            c = i;
+            base = base_in;
+        }
+        base_in += x;
+    }
+    if (c != cta) return;
+    int w = -1;
+    base_in = base;
+    double start = base;
+    for (int i = 0; i < kWarps; ++i) {
+        const double x = warp_part[half][i];
+        if (x > 0. && (w < 0 || base_in <= goal)) {
+            w = i;
+            start = base_in;
+        }
+        base_in += x;
+    }
+    if (w != warp) return;
+    // this warp's stretch again, 128 elements at a time
+    int token = -1, final_positive = -1;
+    double run = start;
+    for (int i = first; i < last && token < 0; i += 128) {
+        float x[4];
+        load_rest(r, i + 4 * lane, V, vec, x);
+        double own[4];
+        double s = 0.;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            s += static_cast<double>(x[k]);
+            own[k] = s;
+        }
+        double before = s;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double y = __shfl_up_sync(kAll, before, o);
+            if (lane >= o) before += y;
+        }
+        const double end = __shfl_sync(kAll, before, 31);
+        before = run + (before - s);
+        int hit = -1, positive = -1;
+#pragma unroll
+        for (int k = 3; k >= 0; --k) {
+            if (x[k] > 0.f && before + own[k] > goal) hit = i + 4 * lane + k;
+            if (x[k] > 0.f && positive < 0) positive = i + 4 * lane + k;
+        }
+        const unsigned hits = __ballot_sync(kAll, hit >= 0), some = __ballot_sync(kAll, positive >= 0);
+        if (hits != 0) token = __shfl_sync(kAll, hit, __ffs(hits) - 1);
+        if (some != 0) final_positive = __shfl_sync(kAll, positive, 31 - __clz(some));
+        run += end;
+    }
+    if (lane == 0) p.next_tokens[seq] = token >= 0 ? token : final_positive;
+}
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" int pkv_tree_verify(int32_t *path, int32_t max_depth, int32_t *path_lens,
+                               int32_t *next_tokens, const int32_t *draft_tokens,
+                               const int32_t *parents, const int32_t *query_start,
+                               const float *target_probs, int64_t target_stride,
+                               const float *draft_probs, int64_t draft_stride,
+                               const float *accept_uniforms, const float *sample_uniforms,
+                               int32_t num_seqs, int32_t num_nodes, int32_t vocab_size,
+                               pkv_stream_t stream) {
+    using namespace pkv;
+    if (num_seqs < 0 || num_nodes < 0) return PKV_ERR_INVALID;
+    if (num_seqs == 0) return PKV_OK;
+    if (!path || !path_lens || !next_tokens || !query_start || !sample_uniforms ||
+        (num_nodes > 0 && (!draft_tokens || !parents || !target_probs || !accept_uniforms)))
+        return PKV_ERR_NULL;
+    if (max_depth <= 0 || vocab_size <= 0 || target_stride < vocab_size ||
+        (draft_probs != nullptr && draft_stride < vocab_size))
+        return PKV_ERR_INVALID;
+    if (max_depth > PKV_MAX_ACCEPT_DEPTH || vocab_size > (1 << 30) ||
+        num_seqs > INT32_MAX / kMaxCluster)
+        return PKV_ERR_UNSUPPORTED;
+    if (!aligned(path, 4) || !aligned(path_lens, 4) || !aligned(next_tokens, 4) ||
+        !aligned(draft_tokens, 4) || !aligned(parents, 4) || !aligned(query_start, 4) ||
+        !aligned(target_probs, 4) || !aligned(draft_probs, 4) || !aligned(accept_uniforms, 4) ||
+        !aligned(sample_uniforms, 4))
+        return PKV_ERR_ALIGNMENT;
+    VerifyParams p{};
+    p.path = path;
+    p.path_lens = path_lens;
+    p.next_tokens = next_tokens;
+    p.tokens = draft_tokens;
+    p.parents = parents;
+    p.query_start = query_start;
+    p.target = target_probs;
+    p.draft = draft_probs;
+    p.target_stride = target_stride;
+    p.draft_stride = draft_stride;
+    p.accept_u = accept_uniforms;
+    p.sample_u = sample_uniforms;
+    p.max_depth = max_depth;
+    p.num_nodes = num_nodes;
+    p.vocab = vocab_size;
+    p.err = device_error_record();
+    if (p.err == nullptr) return PKV_ERR_CUDA;
+    const int ctas = kMaxCluster;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(num_seqs) * ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, tree_verify_kernel, p);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e == cudaSuccess ? PKV_OK : cuda_failure(e, "tree_verify_kernel launch");
+}
