@@ -118,16 +118,15 @@ def verify(tokens, parents, query_start, target, draft, accept_u, sample_u, max_
 
 
 def scored_attention(q, k, v, block_tables, seq_lens, query_start, scale, num_kv_heads,
-                     softcap=0.0, window=0, slopes=None, prefix_lens=None):
+                     softcap=0.0, window=0, slopes=None, prefix_lens=None, rows=None):
     """Attention under score rules over caches k, v [NB, bs, Hk, D] of values.
 
-    Returns out [Tq, H, D] and a bound [Tq, H, D] on what fp32 arithmetic with fp16
+    rows: only these query rows.  Returns out [Tq, H, D] and a bound [Tq, H, D] on what fp32 arithmetic with fp16
     weights and outputs may be off by.  Per key, in units of its weight: 2^-11 for
     the weight's rounding; the score's error in nats -- (D + 8) 2^-24 of
     sum |q||k| scale for the dot product, its scaling and the exponential's
-    argument, 8 2^-24 of the cap for the capping (below a quarter of the cap,
-    relative to the score, and covered by the former), 4 2^-24 of slope * distance
-    for the bias -- and 2^-20 for the exponential and sums of roundings.  A weight's
+    argument, 33 2^-24 of the capped score for the capping (8 2^-24 of the cap from a
+    quarter of it on, less below), 4 2^-24 of slope * distance for the bias -- and 2^-20 for the exponential and sums of roundings.  A weight's
     error moves the output by its share times (v - out).  Weights below fp16's
     normal range are off by 2^-36 of the largest at most."""
     q = np.asarray(q, np.float64)
@@ -141,6 +140,8 @@ def scored_attention(q, k, v, block_tables, seq_lens, query_start, scale, num_kv
         ok = (ids >= 0) & (ids < k.shape[0])
         prefix = 0 if prefix_lens is None else int(prefix_lens[i])
         for r in range(q0, q1):
+            if rows is not None and r not in rows:
+                continue
             a = L - (q1 - r)
             sees = (pos <= a) & ((a - pos < window) if window else True)
             sees = (sees | (pos < prefix)) & ok
@@ -154,7 +155,7 @@ def scored_attention(q, k, v, block_tables, seq_lens, query_start, scale, num_kv
                 err = (np.abs(K) @ np.abs(q[r, h])) * abs(scale) * (D + 8) * 2.0 ** -24
                 if softcap:
                     s = softcap * np.tanh(s / softcap)
-                    err = err + 8 * softcap * 2.0 ** -24
+                    err = err + np.abs(s) * 33 * 2.0 ** -24
                 if slopes is not None:
                     bias = float(slopes[h]) * np.abs(a - at)
                     s = s - bias

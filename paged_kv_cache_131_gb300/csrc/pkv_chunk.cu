@@ -244,6 +244,12 @@ __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c
     return d;
 }
 
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -651,49 +657,102 @@ __device__ __forceinline__ void fetch_item(const ChunkParams &p, int n_big, int 
     for (int w = 0; w < kPartBlocks / 32; ++w) f.valid[w] = __ballot_sync(0xffffffffu, f.ids[w] >= 0);
 }
 
-// The row's scores of this thread's 64 keys under the rules, in place: in log2
-// units, masked ones minus infinity, mx their maximum.  The keys are four blocks
-// of the tile's list from place v0 on, nbg of them there, bad ones not in vmask.
-// True if the warp's rows see every key (the masks are passed over then).
-__device__ __forceinline__ bool rule_scores(const ChunkParams &p, uint32_t (&sx)[kGroupKeys],
-                                            int nbg, uint32_t vmask, int v0, int pb, int skip,
-                                            int prefix, int pos, float slope, float sl2,
-                                            float &mx) {
+// The row's scores of this thread's 64 keys under the rules, in place: in units of
+// 1/a in the log2 domain (a returned), masked ones minus infinity, mx their maximum
+// times a.  The keys are four blocks of the tile's list from place v0 on, nbg of them
+// there, bad ones not in vmask.  Where the warp's rows see every key the masks are
+// passed over; capped scores up to the cap take a polynomial in packed pairs.
+__device__ __forceinline__ float rule_scores(const ChunkParams &p, uint32_t (&sx)[kGroupKeys],
+                                             int nbg, uint32_t vmask, int v0, int pb, int skip,
+                                             int prefix, int pos, float slope, float sl2,
+                                             float &mx) {
     int kp[kGroupKeys / kBS];  // positions of the blocks' first keys
-    bool whole = nbg == kGroupKeys / kBS && vmask == 0xFu;
+    bool whole = nbg == kGroupKeys / kBS && vmask == 0xFu, past = true;
 #pragma unroll
     for (int b = 0; b < kGroupKeys / kBS; ++b) {
         kp[b] = span_block(pb, skip, v0 + b) * kBS;
         whole = whole && seen_whole(kp[b], pos, pos, p.rules.window, prefix);
+        past = past && kp[b] + kBS - 1 <= pos;
     }
     const bool fast = __all_sync(0xffffffffu, whole);
+    float a = sl2;
     if (p.rules.cap_log2 > 0.f) {
+        a = p.rules.cap_log2;
+        const float cs = p.rules.cap_scale;
+        const uint64_t cs2 = f32x2(cs, cs);
+        float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int e = 0; e < kGroupKeys; ++e)
-            sx[e] = __float_as_uint(dec::capped_score(__uint_as_float(sx[e]), p.rules.cap_log2,
-                                                      p.rules.cap_scale));
-    } else {
+        for (int e = 0; e < kGroupKeys / 2; ++e)
+            top[e & 3] = fmax3(top[e & 3], fabsf(__uint_as_float(sx[2 * e])),
+                               fabsf(__uint_as_float(sx[2 * e + 1])));
+        // (a NaN score does not raise the maximum; the polynomial keeps it)
+        const float most = fmaxf(fmax3(top[0], top[1], top[2]), top[3]) * fabsf(cs);
+        if (__all_sync(0xffffffffu, most <= 1.f)) {
+            const uint64_t c0 = f32x2(dec::kTanh0, dec::kTanh0), c1 = f32x2(dec::kTanh1, dec::kTanh1),
+                           c2 = f32x2(dec::kTanh2, dec::kTanh2), c3 = f32x2(dec::kTanh3, dec::kTanh3),
+                           c4 = f32x2(dec::kTanh4, dec::kTanh4), c5 = f32x2(dec::kTanh5, dec::kTanh5),
+                           c6 = f32x2(dec::kTanh6, dec::kTanh6);
 #pragma unroll
-        for (int e = 0; e < kGroupKeys; ++e) sx[e] = __float_as_uint(__uint_as_float(sx[e]) * sl2);
-    }
-    if (p.rules.slopes != nullptr) {
+            for (int e = 0; e < kGroupKeys / 2; ++e) {
+                const uint64_t y = mul_f32x2(
+                    f32x2(__uint_as_float(sx[2 * e]), __uint_as_float(sx[2 * e + 1])), cs2);
+                const uint64_t t = mul_f32x2(y, y);
+                uint64_t r = fma_f32x2(t, c6, c5);
+                r = fma_f32x2(t, r, c4);
+                r = fma_f32x2(t, r, c3);
+                r = fma_f32x2(t, r, c2);
+                r = fma_f32x2(t, r, c1);
+                r = fma_f32x2(t, r, c0);
+                const float2 v = f32x2_split(mul_f32x2(y, r));
+                sx[2 * e] = __float_as_uint(v.x);
+                sx[2 * e + 1] = __float_as_uint(v.y);
+            }
+        } else {
 #pragma unroll
-        for (int b = 0; b < kGroupKeys / kBS; ++b) {
-            const float d0 = static_cast<float>(kp[b] - pos);
-#pragma unroll
-            for (int i = 0; i < kBS; ++i) {
-                uint32_t &x = sx[b * kBS + i];
-                x = __float_as_uint(fmaf(-slope, fabsf(d0 + static_cast<float>(i)), __uint_as_float(x)));
+            for (int e = 0; e < kGroupKeys; ++e) {
+                const float y = __uint_as_float(sx[e]) * cs;
+                sx[e] = __float_as_uint(fabsf(y) <= 1.f ? dec::tanh_near(y) : dec::tanh_far(y));
             }
         }
     }
-    if (!fast) {
+    if (p.rules.slopes != nullptr) {
+        // (scores times a, the bias added)
+        if (__all_sync(0xffffffffu, past)) {
+            // keys at and before the row: the distance grows by one per key
+#pragma unroll
+            for (int b = 0; b < kGroupKeys / kBS; ++b) {
+                const float bias = slope * static_cast<float>(kp[b] - pos);
+#pragma unroll
+                for (int i = 0; i < kBS; ++i) {
+                    uint32_t &x = sx[b * kBS + i];
+                    x = __float_as_uint(fmaf(__uint_as_float(x), a, fmaf(slope, static_cast<float>(i), bias)));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int b = 0; b < kGroupKeys / kBS; ++b) {
+                const float d0 = static_cast<float>(kp[b] - pos);
+#pragma unroll
+                for (int i = 0; i < kBS; ++i) {
+                    uint32_t &x = sx[b * kBS + i];
+                    x = __float_as_uint(fmaf(-slope, fabsf(d0 + static_cast<float>(i)),
+                                             __uint_as_float(x) * a));
+                }
+            }
+        }
+        a = 1.f;
+    }
+    if (!fast || a <= 0.f) {
+        // (a scale that is not positive is applied here: the largest product is not
+        // that of the largest score, and a masked one not minus infinity)
+        const float s = a <= 0.f ? a : 1.f;
+        if (a <= 0.f) a = 1.f;
 #pragma unroll
         for (int e = 0; e < kGroupKeys; ++e) {
             const int b = e / kBS, at = kp[b] + e % kBS;
             const bool vis = b < nbg && ((vmask >> b) & 1u) &&
                              dec::rule_sees(pos, at, p.rules.window, prefix);
-            if (!vis) sx[e] = __float_as_uint(kNegInf);
+            sx[e] = vis ? __float_as_uint(__uint_as_float(sx[e]) * s) : __float_as_uint(kNegInf);
         }
     }
     float mr[8];
@@ -702,8 +761,8 @@ __device__ __forceinline__ bool rule_scores(const ChunkParams &p, uint32_t (&sx)
 #pragma unroll
     for (int e = 0; e < kGroupKeys / 2; ++e)
         mr[e & 7] = fmax3(mr[e & 7], __uint_as_float(sx[2 * e]), __uint_as_float(sx[2 * e + 1]));
-    mx = fmax3(fmax3(mr[0], mr[1], mr[2]), fmax3(mr[3], mr[4], mr[5]), fmaxf(mr[6], mr[7]));
-    return fast;
+    mx = fmax3(fmax3(mr[0], mr[1], mr[2]), fmax3(mr[3], mr[4], mr[5]), fmaxf(mr[6], mr[7])) * a;
+    return a;
 }
 
 // Value block `vb` ([chunk][token][128 B]): rows from `end` on zeroed, and of the
@@ -1156,13 +1215,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // every key of the warp is visible and the scale is not
                 // negative, else the scores are scaled and masked and their
                 // maximum taken again
-                bool fast;
-                float mx;
+                float mx, a;
                 if constexpr (kRules) {
-                    fast = rule_scores(p, sx, nbg, vmask, part * kPartBlocks + b0, pb, skip, prefix,
-                                       pos, slope, sl2, mx);
+                    a = rule_scores(p, sx, nbg, vmask, part * kPartBlocks + b0, pb, skip, prefix,
+                                    pos, slope, sl2, mx);
                 } else {
-                fast = __all_sync(0xffffffffu, nbg == 4 && vmask == 0xFu &&
+                const bool fast = __all_sync(0xffffffffu, nbg == 4 && vmask == 0xFu &&
                                                               kbase + kGroupKeys - 1 <= lim &&
                                                               sl2 >= 0.f);
                 float mr[8];
@@ -1189,6 +1247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     mx *= sl2;
                 }
+                a = fast ? sl2 : 1.f;
                 }
                 // the row's other half: the thread 16 lanes away
                 const float mo = __shfl_xor_sync(0xffffffffu, mx, 16);
@@ -1224,7 +1283,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // fp16 pairs: column 32 h + i of the buffer holds keys
                 // 64 h + 2i, 2i+1; the P V of two steps back must be done
                 // with this buffer
-                const float a = fast && !kRules ? sl2 : 1.f;
                 const int pb = g & 1;
                 if (g >= 2) {
                     if (!wait_all(br.pv_done(pb), ((g - 2) >> 1) & 1)) {

@@ -570,14 +570,15 @@ __device__ __forceinline__ void balanced_body(const BalancedParams &p, uint8_t *
         br.window = p.rules.window;
         br.cap_log2 = p.rules.cap_log2;
         br.cap_scale = p.rules.cap_scale;
+        br.biased = p.rules.slopes != nullptr;
     }
     // under rules: values of keys that the token does not see never reach it,
     // whatever they hold
-    auto hide = [&](uint32_t vb, uint32_t head, const BlockRules &b, int nv) {
+    auto hide = [&](uint32_t vb, uint32_t head, BlockRules &b, int nv) {
         if constexpr (kScored && !Policy::kColumns) {
-            const uint32_t seen = seen_keys(b, nv, lane);
-            if (seen != 0xFFFFu)
-                zero_unseen_rows<(kFp8 ? D : D * 2)>(vb, tile, head, seen, lane);
+            b.seen = seen_keys(b, nv, lane);
+            if (b.seen != 0xFFFFu)
+                zero_unseen_rows<(kFp8 ? D : D * 2)>(vb, tile, head, b.seen, lane);
         }
     };
 
@@ -683,10 +684,11 @@ __device__ __forceinline__ void balanced_body(const BalancedParams &p, uint8_t *
                     // (a block that ends by the first token's position and starts
                     // in the last one's window, or lies in the prefix, is seen whole)
                     const int last = qr.lim0 + qr.ncols / G - 1;
-                    if (br.kp + mt.y > br.prefix &&
-                        (br.kp + mt.y - 1 > qr.lim0 || last - br.kp >= br.window))
-                        st.clean_values(vb, tile, head, mt.y, br, lane);
-                    st.block(kb, vb, tile, head, mt.y, br.kp, p.scale_log2, lane, br);
+                    const bool whole = mt.y == kBS && (br.kp + kBS <= br.prefix ||
+                                                       (br.kp + kBS - 1 <= qr.lim0 &&
+                                                        last - br.kp < br.window));
+                    if (!whole) st.clean_values(vb, tile, head, mt.y, br, lane);
+                    st.block(kb, vb, tile, head, mt.y, br.kp, p.scale_log2, lane, br, whole);
                 } else if constexpr (Policy::kColumns)
                     st.block(kb, vb, tile, head, mt.y, mt.w * kBS, p.scale_log2, lane);
                 else if constexpr (kScored)

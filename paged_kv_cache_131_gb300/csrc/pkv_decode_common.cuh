@@ -51,11 +51,12 @@ struct SwizzledTile {
 // ---------------------------------------------------------------------------
 // Score rules (pkv_score_rules) as a policy applies them, everything in the
 // log2 domain: t = cap * tanh(y), y = scale q.k / cap, then a bias of -slope *
-// distance, then the mask.  tanh(y) = 1 - 2 / (1 + e^(2y)) costs two
-// special-function instructions and is off by a few 2^-24, whose limits (0 and
-// infinity of e^(2y)) come out as -1 and 1; below 1/4 that would be large beside
-// y (a cap far above the scores would swallow them), so there the series
-// y - y^3/3 + 2y^5/15 - 17y^7/315 + 62y^9/2835 is taken (its rest: 2^-27 of y).
+// distance, then the mask.  Up to |y| = 1 -- where a model's cap leaves most of its
+// scores -- tanh(y) is y times a polynomial of degree 6 in y^2 (fitted for this file
+// by least squares reweighted towards the smallest largest error: 2^-24.2 of the
+// value), fused multiply-adds alone.  Beyond, 1 - 2 / (1 + e^(2y)) costs two
+// special-function instructions and is off by a few 2^-24; its limits (0 and
+// infinity of e^(2y)) come out as -1 and 1.
 //
 // Softmax weights under rules stand 2^15 higher than 2^(t - max): as fp16 for
 // the P V MMA they keep 11 bits down to 2^-29 of the row's largest, and are off
@@ -70,6 +71,8 @@ struct BlockRules {
     int qpos;         // the (first) query token's position
     float cap_log2;   // softcap * log2(e), 0: not capped
     float cap_scale;  // scale / softcap
+    bool biased;      // there are slopes
+    uint32_t seen;    // (one query token) bits of the block's keys that it sees
 };
 
 __device__ __forceinline__ float rule_ex2(float x) {
@@ -84,23 +87,46 @@ __device__ __forceinline__ float rule_rcp(float x) {
     return y;
 }
 
-// A raw score q.k capped (in log2 units).
-__device__ __forceinline__ float capped_score(float raw, float cap_log2, float cap_scale) {
-    const float y = raw * cap_scale, y2 = y * y;
-    const float far = fmaf(-2.f, rule_rcp(1.f + rule_ex2(y * (2.f * kLog2e))), 1.f);
-    float near = fmaf(y2, 62.f / 2835.f, -17.f / 315.f);
-    near = fmaf(y2, near, 2.f / 15.f);
-    near = fmaf(y2, near, -1.f / 3.f);
-    near = fmaf(y * y2, near, y);
-    return cap_log2 * (fabsf(y) < 0.25f ? near : far);
+constexpr float kTanh0 = 0.99999995f, kTanh1 = -0.33332839f, kTanh2 = 0.13325204f,
+                kTanh3 = -0.05345703f, kTanh4 = 0.020289981f, kTanh5 = -0.0062033794f,
+                kTanh6 = 0.0010410226f;
+
+// tanh(y) for |y| <= 1 (the polynomial by halves: a shorter chain).
+__device__ __forceinline__ float tanh_near(float y) {
+    const float t = y * y, t2 = t * t;
+    const float lo = fmaf(t2, fmaf(t, kTanh3, kTanh2), fmaf(t, kTanh1, kTanh0));
+    const float hi = fmaf(t2, kTanh6, fmaf(t, kTanh5, kTanh4));
+    return y * fmaf(t2 * t2, hi, lo);
 }
 
-// A raw score under the rules, before the mask; slope in log2 units.
-__device__ __forceinline__ float ruled_score(float raw, float scale_log2, const BlockRules &br,
-                                             float slope, int distance) {
-    const float t = br.cap_log2 > 0.f ? capped_score(raw, br.cap_log2, br.cap_scale)
-                                      : raw * scale_log2;
-    return fmaf(-slope, fabsf(static_cast<float>(distance)), t);
+// tanh(y) for |y| > 1 (and NaN).
+__device__ __forceinline__ float tanh_far(float y) {
+    return fmaf(-2.f, rule_rcp(1.f + rule_ex2(y * (2.f * kLog2e))), 1.f);
+}
+
+// N raw scores q.k under the rules before the mask, in place: in log2 units; d(i)
+// gives score i's distance, slope(i) its head's slope (log2 units).  (Both forms of
+// the cap: with one or two warps a scheduler they cost less than a vote and a
+// branch, 129 us against 138 for 64 x 4 drafted tokens.)
+template <int N, class Distance, class Slope>
+__device__ __forceinline__ void rule_scores(float (&x)[N], float scale_log2, const BlockRules &br,
+                                            Distance d, Slope slope) {
+    if (br.cap_log2 > 0.f) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float y = x[i] * br.cap_scale;
+            const float near = tanh_near(y), far = tanh_far(y);
+            x[i] = br.cap_log2 * (fabsf(y) <= 1.f ? near : far);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] *= scale_log2;
+    }
+    if (br.biased) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            x[i] = fmaf(-slope(i), fabsf(static_cast<float>(d(i))), x[i]);
+    }
 }
 
 // Whether the token at position a sees the key at position b (b < L).
@@ -108,8 +134,10 @@ __device__ __forceinline__ bool rule_sees(int a, int b, int window, int prefix) 
     return (b <= a && a - b < window) || b < prefix;
 }
 
-// Bits of the block's nv keys that the token at br.qpos sees (every lane).
+// Bits of the block's nv keys that the token at br.qpos, the sequence's last, sees
+// (every lane).
 __device__ __forceinline__ uint32_t seen_keys(const BlockRules &br, int nv, int lane) {
+    if (nv == kBS && (br.qpos - br.kp < br.window || br.kp + kBS <= br.prefix)) return 0xFFFFu;
     return __ballot_sync(0xffffffffu,
                          lane < nv && rule_sees(br.qpos, br.kp + lane, br.window, br.prefix));
 }
@@ -244,14 +272,18 @@ struct MmaPolicy {
         }
         float x[4];  // token g: heads 2t, 2t+1; token g+8: heads 2t, 2t+1
         float mx[2] = {kNegInf, kNegInf};
+        if constexpr (kRules) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = sa[j] + sb[j];
+            rule_scores(
+                x, scale_log2, br, [&](int j) { return br.qpos - br.kp - g - 8 * (j >> 1); },
+                [&](int j) { return rc.slope[j & 1]; });
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int tok = g + 8 * (j >> 1);
             if constexpr (kRules) {
-                const int d = br.qpos - br.kp - tok;
-                const float v = ruled_score(sa[j] + sb[j], scale_log2, br, rc.slope[j & 1], d);
-                x[j] = tok < nv && rule_sees(br.qpos, br.kp + tok, br.window, br.prefix) ? v
-                                                                                         : kNegInf;
+                if (!((br.seen >> tok) & 1u)) x[j] = kNegInf;
             } else {
                 x[j] = tok < nv ? (sa[j] + sb[j]) * scale_log2 : kNegInf;
             }
@@ -270,7 +302,7 @@ struct MmaPolicy {
             if constexpr (kRules) {
                 // (scores that are all minus infinity: no weight)
                 const float safe = mnew == kNegInf ? 0.f : mnew;
-                alpha[h] = exp2f(m[h] - safe);
+                alpha[h] = rule_ex2(m[h] - safe);
                 ref[h] = safe - kRuleShift;
             } else {
                 alpha[h] = exp2f(m[h] - mnew);
@@ -279,18 +311,21 @@ struct MmaPolicy {
             m[h] = mnew;
         }
         // weights rows = tokens 0-7 / 8-15, columns = heads
-        const uint32_t p0 = pack_half2(exp2f(x[0] - ref[0]), exp2f(x[1] - ref[1]));
-        const uint32_t p1 = pack_half2(exp2f(x[2] - ref[0]), exp2f(x[3] - ref[1]));
+        const uint32_t p0 = pack_half2(weight(x[0] - ref[0]), weight(x[1] - ref[1]));
+        const uint32_t p1 = pack_half2(weight(x[2] - ref[0]), weight(x[3] - ref[1]));
         // the normaliser sums the same fp16-rounded weights the MMA applies
         const float2 u0 = unpack_half2(p0), u1 = unpack_half2(p1);
         l[0] = l[0] * alpha[0] + (u0.x + u1.x);
         l[1] = l[1] * alpha[1] + (u0.y + u1.y);
+        // (under rules a block that moves no maximum leaves O as it is)
+        if (!kRules || __any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            o[mt][0] *= alpha[0];
-            o[mt][1] *= alpha[1];
-            o[mt][2] *= alpha[0];
-            o[mt][3] *= alpha[1];
+            for (int mt = 0; mt < MT; ++mt) {
+                o[mt][0] *= alpha[0];
+                o[mt][1] *= alpha[1];
+                o[mt][2] *= alpha[0];
+                o[mt][3] *= alpha[1];
+            }
         }
         const uint32_t pb0 = movmatrix_trans(p0), pb1 = movmatrix_trans(p1);
         // O^T += V^T P^T; transposed-ldmatrix matrices: tokens 0-7 at dims
@@ -303,6 +338,10 @@ struct MmaPolicy {
             ldsm_x4_trans(a0, a1, a2, a3, vb + tile.at(vt, vcol + mt * 32));
             mma_16816(o[mt], a0, a1, a2, a3, pb0, pb1);
         }
+    }
+
+    __device__ __forceinline__ static float weight(float x) {
+        return kRules ? rule_ex2(x) : exp2f(x);
     }
 
     // The slopes of this lane's columns (slopes: the group's, fp32, or null).
@@ -452,10 +491,12 @@ struct MmaColsPolicy {
     }
 
     // One staged block whose first key is at position kp: key tile at kb,
-    // value tile at vb, this head's bytes from `head`; nv valid tokens.
+    // value tile at vb, this head's bytes from `head`; nv valid tokens.  whole
+    // (under rules): every column sees all 16 keys.
     __device__ __forceinline__ void block(uint32_t kb, uint32_t vb, SwizzledTile tile,
                                           uint32_t head, int nv, int kp, float scale_log2,
-                                          int lane, const BlockRules &br = {}) {
+                                          int lane, const BlockRules &br = {},
+                                          bool whole = false) {
         const int g = lane >> 2;
         const int rt = ((lane >> 3) & 1) * 8 + (lane & 7);
         const uint32_t kcol = head + (lane >> 4) * 16;
@@ -483,14 +524,19 @@ struct MmaColsPolicy {
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
             mx[c][0] = mx[c][1] = kNegInf;
+            if constexpr (kRules) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[c][e] = sa[c][e] + sb[c][e];
+                rule_scores(
+                    x[c], scale_log2, br,
+                    [&](int e) { return lim[c][e & 1] - kp - g - 8 * (e >> 1); },
+                    [&](int e) { return rc.slope[2 * c + (e & 1)]; });
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int tok = g + 8 * (e >> 1);
                 if constexpr (kRules) {
-                    const int a = lim[c][e & 1];
-                    const float v = ruled_score(sa[c][e] + sb[c][e], scale_log2, br,
-                                                rc.slope[2 * c + (e & 1)], a - kp - tok);
-                    x[c][e] = tok < nv && sees(c, e & 1, kp + tok, br) ? v : kNegInf;
+                    if (!whole && !(tok < nv && sees(c, e & 1, kp + tok, br))) x[c][e] = kNegInf;
                 } else {
                     const bool vis = tok < nv && kp + tok <= lim[c][e & 1];
                     x[c][e] = vis ? (sa[c][e] + sb[c][e]) * scale_log2 : kNegInf;
@@ -510,15 +556,15 @@ struct MmaColsPolicy {
                 const float mnew = fmaxf(m[c][h], v);
                 // a column with no visible key yet keeps m = -inf, l = 0, o = 0
                 msafe[c][h] = mnew == kNegInf ? 0.f : mnew;
-                alpha[c][h] = exp2f(m[c][h] - msafe[c][h]);
+                alpha[c][h] = weight(m[c][h] - msafe[c][h]);
                 if constexpr (kRules) msafe[c][h] -= kRuleShift;
                 m[c][h] = mnew;
             }
         uint32_t pb[NT][2];
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
-            const uint32_t p0 = pack_half2(exp2f(x[c][0] - msafe[c][0]), exp2f(x[c][1] - msafe[c][1]));
-            const uint32_t p1 = pack_half2(exp2f(x[c][2] - msafe[c][0]), exp2f(x[c][3] - msafe[c][1]));
+            const uint32_t p0 = pack_half2(weight(x[c][0] - msafe[c][0]), weight(x[c][1] - msafe[c][1]));
+            const uint32_t p1 = pack_half2(weight(x[c][2] - msafe[c][0]), weight(x[c][3] - msafe[c][1]));
             // the normaliser sums the same fp16-rounded weights the MMA applies
             const float2 u0 = unpack_half2(p0), u1 = unpack_half2(p1);
             l[c][0] = l[c][0] * alpha[c][0] + (u0.x + u1.x);
@@ -542,6 +588,10 @@ struct MmaColsPolicy {
 #pragma unroll
             for (int c = 0; c < NT; ++c) mma_16816(o[c][mt], a0, a1, a2, a3, pb[c][0], pb[c][1]);
         }
+    }
+
+    __device__ __forceinline__ static float weight(float x) {
+        return kRules ? rule_ex2(x) : exp2f(x);
     }
 
     // Whether column 8c + 2t + h sees position b (b below the sequence's end).
@@ -777,7 +827,15 @@ struct MmaFp8Policy {
         }
         float mx[2] = {kNegInf, kNegInf};
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int b = 0; b < NB; ++b) {
+            if constexpr (kRules) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[b][j] *= ks[b][j >> 1];
+                rule_scores(
+                    x[b], scale_log2, br[b],
+                    [&](int j) { return br[b].qpos - br[b].kp - token_of(lane, j >> 1); },
+                    [&](int j) { return rc.slope[j & 1]; });
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int r = j >> 1;  // token row: g or g+8
@@ -785,18 +843,14 @@ struct MmaFp8Policy {
                     // the reference follows the largest product of weight and value
                     // scale, so that product fits fp16 whatever the scales are
                     const int tok = token_of(lane, r);
-                    const BlockRules &w = br[b];
-                    const float v = ruled_score(x[b][j] * ks[b][r], scale_log2, w, rc.slope[j & 1],
-                                                w.qpos - w.kp - tok);
-                    const bool vis = tok < nv[b] &&
-                                     rule_sees(w.qpos, w.kp + tok, w.window, w.prefix);
-                    x[b][j] = vis ? v : kNegInf;
+                    if (!((br[b].seen >> tok) & 1u)) x[b][j] = kNegInf;
                     mx[j & 1] = fmaxf(mx[j & 1], x[b][j] + lv[b][r]);
                 } else {
                     x[b][j] = token_of(lane, r) < nv[b] ? (x[b][j] * ks[b][r]) * scale_log2 : kNegInf;
                     mx[j & 1] = fmaxf(mx[j & 1], x[b][j]);
                 }
             }
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 4));
@@ -809,7 +863,7 @@ struct MmaFp8Policy {
             const float mnew = fmaxf(m[h], mx[h]);  // finite: some token is valid
             if constexpr (kRules) {
                 const float safe = mnew == kNegInf ? 0.f : mnew;
-                alpha[h] = exp2f(m[h] - safe);
+                alpha[h] = rule_ex2(m[h] - safe);
                 ref[h] = safe - kRuleShift;
             } else {
                 alpha[h] = exp2f(m[h] - mnew);
@@ -825,7 +879,7 @@ struct MmaFp8Policy {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int r = j >> 1;
-                const float p = exp2f(x[b][j] - ref[j & 1]);
+                const float p = kRules ? rule_ex2(x[b][j] - ref[j & 1]) : exp2f(x[b][j] - ref[j & 1]);
                 l[j & 1] += p;
                 if constexpr (kRules) pw[j] = x[b][j] == kNegInf ? 0.f : p * vs[b][r];
                 else pw[j] = token_of(lane, r) < nv[b] ? p * (vs[b][r] * kWeightBoost) : 0.f;
@@ -835,12 +889,14 @@ struct MmaFp8Policy {
             pb[b][0] = movmatrix_trans(pack_half2(pw[0], pw[1]));
             pb[b][1] = movmatrix_trans(pack_half2(pw[2], pw[3]));
         }
+        if (!kRules || __any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            o[mt][0] *= alpha[0];
-            o[mt][1] *= alpha[1];
-            o[mt][2] *= alpha[0];
-            o[mt][3] *= alpha[1];
+            for (int mt = 0; mt < MT; ++mt) {
+                o[mt][0] *= alpha[0];
+                o[mt][1] *= alpha[1];
+                o[mt][2] *= alpha[0];
+                o[mt][3] *= alpha[1];
+            }
         }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {

@@ -13,14 +13,15 @@
 // nodes' probabilities are gathered into shared memory once), and all of them sum
 // a row when a child is rejected or the next token is drawn: each warp a stretch
 // of its CTA's share, the CTAs' sums exchanged through distributed shared memory.
-// The draw finds the CTA, then the warp, and that warp goes through its stretch
-// again (out of L2).
+// The draw finds the CTA and the warp from those sums, and that CTA goes through
+// the warp's stretch again (out of L2), a few elements a thread.
 //
-// Sums: an element of R is one fused multiply-add of the row's fp32 values (C as
-// a pair of fp32: one rounding), and a thread adds its elements into a pair of
-// fp32 (the error of each addition kept), which loses nothing that 64 bits would
-// hold; threads, warps and CTAs are added in fp64.  fp64 per element would take
-// longer than the row's bytes: this GPU's fp64 rate is 2 per cycle and SM.
+// Arithmetic: an element of R is one fused multiply-add of the row's fp32 values
+// (C as a pair of fp32: one rounding); sums, masses and tests are carried as
+// pairs of fp32 whose errors are kept (47 bits).  fp64 would hold as much, but its
+// rate here is 2 a cycle and SM, and every warp walks: the same kernel in fp64
+// took 22.6, 129 and 44 us for a chain of 5 nodes, 64 trees of 16 (V 128256) and
+// 32 of 63 without drafts.
 // Bound: HBM for many sequences (the rows of p and q), latency for few.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
@@ -35,8 +36,9 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kBatch = 4;  // vectors of either row that a thread has in flight
 constexpr int kMaxCluster = 8;
 constexpr int kMaxNodes = PKV_MAX_TREE_NODES;
 constexpr int kNodesPerLane = kMaxNodes / 32;
@@ -110,28 +112,95 @@ __device__ __forceinline__ void load_rest(const Rest &r, int i, int vocab, bool 
                 if (r.gone[g] == i + k) x[k] = 0.f;
 }
 
-// s + e += x, the rounding error of s kept in e.
-__device__ __forceinline__ void add_pair(float &s, float &e, float x) {
+// A number as the sum of two fp32, the second below half a step of the first.
+struct Pair {
+    float hi, lo;
+};
+
+__device__ __forceinline__ Pair renorm(float s, float e) {
+    const float h = __fadd_rn(s, e);
+    return {h, __fsub_rn(e, __fsub_rn(h, s))};
+}
+
+// The rounding error of s = a + b.
+__device__ __forceinline__ float sum_error(float a, float b, float s) {
+    const float t = __fsub_rn(s, a);
+    return __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
+}
+
+__device__ __forceinline__ Pair operator+(const Pair &a, const Pair &b) {
+    const float s = __fadd_rn(a.hi, b.hi);
+    return renorm(s, __fadd_rn(sum_error(a.hi, b.hi, s), __fadd_rn(a.lo, b.lo)));
+}
+
+__device__ __forceinline__ Pair operator-(const Pair &a, const Pair &b) {
+    return a + Pair{-b.hi, -b.lo};
+}
+
+__device__ __forceinline__ Pair operator*(const Pair &a, float b) {
+    const float p = __fmul_rn(a.hi, b);
+    return renorm(p, __fmaf_rn(a.lo, b, __fmaf_rn(a.hi, b, -p)));
+}
+
+__device__ __forceinline__ bool operator<(const Pair &a, const Pair &b) {
+    return a.hi < b.hi || (a.hi == b.hi && a.lo < b.lo);
+}
+
+__device__ __forceinline__ bool positive(const Pair &a) { return a.hi > 0.f; }
+
+// s += x, the rounding error kept in e.
+__device__ __forceinline__ void add_to(float &s, float &e, float x) {
     const float t = __fadd_rn(s, x);
-    const float b = __fsub_rn(t, s);
-    e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(x, b)));
+    e = __fadd_rn(e, sum_error(s, x, t));
     s = t;
 }
 
-__device__ __forceinline__ double warp_sum(double v) {
+__device__ __forceinline__ Pair shfl_xor(const Pair &v, int o) {
+    return {__shfl_xor_sync(kAll, v.hi, o), __shfl_xor_sync(kAll, v.lo, o)};
+}
+
+__device__ __forceinline__ Pair shfl(const Pair &v, int lane) {
+    return {__shfl_sync(kAll, v.hi, lane), __shfl_sync(kAll, v.lo, lane)};
+}
+
+__device__ __forceinline__ Pair lanes_sum(Pair v) {
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    for (int o = 16; o >= 1; o >>= 1) v = v + shfl_xor(v, o);
     return v;
 }
 
-__global__ void __launch_bounds__(kThreads)
+// The sum of the lanes below this one and (incl) of this one too.
+__device__ __forceinline__ Pair lanes_below(const Pair &v, int lane, Pair *incl) {
+    Pair run = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Pair y = {__shfl_up_sync(kAll, run.hi, o), __shfl_up_sync(kAll, run.lo, o)};
+        if (lane >= o) run = run + y;
+    }
+    *incl = run;
+    const Pair below = {__shfl_up_sync(kAll, run.hi, 1), __shfl_up_sync(kAll, run.lo, 1)};
+    return lane == 0 ? Pair{0.f, 0.f} : below;
+}
+
+// Lane of the share in which the running sum passes `goal`: the last one with
+// anything in it whose sum before it is not above the goal; -1 if all are empty.
+__device__ __forceinline__ int lane_of(const Pair &share, const Pair &before, const Pair &goal) {
+    const unsigned any = __ballot_sync(kAll, positive(share));
+    const unsigned fit = __ballot_sync(kAll, positive(share) && !(goal < before));
+    return fit != 0 ? 31 - __clz(fit) : __ffs(any) - 1;
+}
+
+__global__ void __launch_bounds__(kThreads, 3)
     tree_verify_kernel(const __grid_constant__ VerifyParams p) {
     // per node: its token's probability under its parent's target and drafts
     __shared__ float node_p[kMaxNodes], node_q[kMaxNodes], node_u[kMaxNodes];
     __shared__ int node_token[kMaxNodes];
     __shared__ int gone[kMaxNodes];
-    __shared__ double warp_part[2][kWarps];       // this CTA's warps, by parity of the pass
-    __shared__ double cta_part[2][kMaxCluster];   // every CTA's sum, written by it
+    __shared__ Pair warp_part[2][kWarps];       // this CTA's warps, by parity of the pass
+    __shared__ Pair cta_part[2][kMaxCluster];   // every CTA's sum, written by it
+    __shared__ Pair draw_part[kWarps];
+    __shared__ int draw_first, draw_last;
+    __shared__ Pair draw_before;
     auto cluster = cooperative_groups::this_cluster();
     const int cta = static_cast<int>(cluster.block_rank());
     const int ctas = static_cast<int>(cluster.num_blocks());
@@ -214,41 +283,70 @@ __global__ void __launch_bounds__(kThreads)
     };
     // The sum of the rest over the whole row, the same in every thread of the
     // cluster; its parts stay in warp_part / cta_part until the pass after next.
-    auto sum_rest = [&]() -> double {
+    auto sum_rest = [&]() -> Pair {
         float s = 0.f, e = 0.f;
-        for (int i = first + 4 * lane; i < last; i += 128) {
+        int i = first + 4 * lane;
+        // whole batches of 16-byte vectors, every load before the first use
+        if (vec && r.num_gone == 0) {
+            for (; i < min(last, 0); i += 128) {
+                float x[4];
+                load_rest(r, i, V, vec, x);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) add_to(s, e, x[k]);
+            }
+            for (; i + (kBatch - 1) * 128 + 4 <= min(last, V); i += kBatch * 128) {
+                float4 a[kBatch], b[kBatch];
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    a[j] = __ldg(reinterpret_cast<const float4 *>(r.p + i + j * 128));
+                    if (r.q != nullptr)
+                        b[j] = __ldg(reinterpret_cast<const float4 *>(r.q + i + j * 128));
+                }
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    if (r.q != nullptr) {
+                        a[j].x = rest_of(r, a[j].x, b[j].x);
+                        a[j].y = rest_of(r, a[j].y, b[j].y);
+                        a[j].z = rest_of(r, a[j].z, b[j].z);
+                        a[j].w = rest_of(r, a[j].w, b[j].w);
+                    }
+                    add_to(s, e, fmaxf(a[j].x, 0.f));
+                    add_to(s, e, fmaxf(a[j].y, 0.f));
+                    add_to(s, e, fmaxf(a[j].z, 0.f));
+                    add_to(s, e, fmaxf(a[j].w, 0.f));
+                }
+            }
+        }
+        for (; i < last; i += 128) {
             float x[4];
             load_rest(r, i, V, vec, x);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) add_pair(s, e, x[k]);
+            for (int k = 0; k < 4; ++k) add_to(s, e, x[k]);
         }
-        const double w = warp_sum(static_cast<double>(s) + static_cast<double>(e));
+        const Pair w = lanes_sum(renorm(s, e));
         const int half = pass & 1;
         ++pass;
         if (lane == 0) warp_part[half][warp] = w;
         __syncthreads();
-        if (static_cast<int>(threadIdx.x) < ctas) {
-            double c = 0.;
-            for (int i = 0; i < kWarps; ++i) c += warp_part[half][i];
-            *cluster.map_shared_rank(&cta_part[half][cta], threadIdx.x) = c;
+        if (warp == 0) {
+            const Pair c = lanes_sum(lane < kWarps ? warp_part[half][lane] : Pair{0.f, 0.f});
+            if (lane < ctas) *cluster.map_shared_rank(&cta_part[half][cta], lane) = c;
         }
         cluster.sync();
-        double total = 0.;
-        for (int i = 0; i < ctas; ++i) total += cta_part[half][i];
-        return total;
+        return lanes_sum(lane < ctas ? cta_part[half][lane] : Pair{0.f, 0.f});
     };
 
     // ---- the walk (every warp of the cluster alike)
     int at = 0, depth = 1;
     bool summed = false;  // the last pass summed r as it stands
-    double total = 0.;
+    Pair total{0.f, 0.f};
     if (cta == 0 && threadIdx.x == 0) path[0] = 0;
     for (;;) {
         open(at);
         summed = false;
         int step = -1;
         if (depth < p.max_depth) {
-            double W = 1., C = 0.;
+            Pair W{1.f, 0.f}, C{0.f, 0.f};
             bool empty = false;
             int seen = 0;  // tokens in `gone`
             for (int j = 0; j < kNodesPerLane && step < 0 && !empty; ++j) {
@@ -256,21 +354,22 @@ __global__ void __launch_bounds__(kThreads)
                 while (kids != 0 && step < 0 && !empty) {
                     const int k = 32 * j + __ffs(kids) - 1;
                     kids &= kids - 1;
-                    const double u = node_u[k], pt = fmaxf(node_p[k], 0.f);
-                    const double qt = fmaxf(node_q[k], 0.f);
+                    const float u = node_u[k], pt = fmaxf(node_p[k], 0.f);
+                    const float qt = fmaxf(node_q[k], 0.f);
                     if (drafted) {
-                        if (u * W * qt < fmax(pt - C * qt, 0.)) {
+                        const Pair have = Pair{pt, 0.f} - C * qt;
+                        if (positive(have) && (W * u) * qt < have) {
                             step = k;
                             break;
                         }
                         // rejected: the rest without what the drafts cover
                         const Rest before = r;
-                        C += W;
+                        C = C + W;
                         r.q = p.draft + (row0 + at) * p.draft_stride;
-                        r.c_hi = static_cast<float>(C);
-                        r.c_lo = static_cast<float>(C - static_cast<double>(r.c_hi));
-                        const double w = sum_rest();
-                        if (w > 0.) {
+                        r.c_hi = C.hi;
+                        r.c_lo = C.lo;
+                        const Pair w = sum_rest();
+                        if (positive(w)) {
                             W = total = w;
                             summed = true;
                         } else {
@@ -282,15 +381,16 @@ __global__ void __launch_bounds__(kThreads)
                         // (a guess that was rejected before has nothing left)
                         bool again = false;
                         for (int g = 0; g < seen; ++g) again = again || gone[g] == node_token[k];
-                        const double have = again ? 0. : pt;
-                        if (u * W < have) {
+                        const Pair have{again ? 0.f : pt, 0.f};
+                        if (W * u < have) {
                             step = k;
                             break;
                         }
-                        if (W - have <= 0.) {
+                        const Pair less = W - have;
+                        if (!positive(less)) {
                             empty = true;
                         } else {
-                            W -= have;
+                            W = less;
                             if (!again) {
                                 // every warp has read the list up to here
                                 __syncthreads();
@@ -317,69 +417,65 @@ __global__ void __launch_bounds__(kThreads)
         for (int d = depth + threadIdx.x; d < p.max_depth; d += kThreads) path[d] = -1;
         if (threadIdx.x == 0) p.path_lens[seq] = depth;
     }
-    if (!(total > 0.)) {
+    if (!positive(total)) {
         if (cta == 0 && threadIdx.x == 0) p.next_tokens[seq] = -1;
         return;
     }
-    // the CTA, then the warp, in whose share the running sum passes u * total; the
-    // last one with any mass where rounding leaves it past the end
-    const double goal = static_cast<double>(draw_u) * total;
-    double base = 0., base_in = 0.;
-    int c = -1;
-    for (int i = 0; i < ctas; ++i) {
-        const double x = cta_part[half][i];
-        if (x > 0. && base_in <= goal) {  // (base_in: the sum before this share)
-            c = i;
-            base = base_in;
+    const Pair goal = total * draw_u;
+    Pair incl;
+    {
+        // the CTA, then its warp, in whose share the running sum passes the goal
+        const Pair share = lane < ctas ? cta_part[half][lane] : Pair{0.f, 0.f};
+        const Pair before = lanes_below(share, lane, &incl);
+        const int c = lane_of(share, before, goal);
+        if (c != cta) return;
+        const Pair base = shfl(before, c);
+        const Pair part = lane < kWarps ? warp_part[half][lane] : Pair{0.f, 0.f};
+        const Pair start = base + lanes_below(part, lane, &incl);
+        const int w = lane_of(part, start, goal);
+        if (warp == w && lane == w) {
+            draw_first = first;
+            draw_last = last;
+            draw_before = start;
         }
-        base_in += x;
     }
-    if (c != cta) return;
-    int w = -1;
-    base_in = base;
-    double start = base;
-    for (int i = 0; i < kWarps; ++i) {
-        const double x = warp_part[half][i];
-        if (x > 0. && (w < 0 || base_in <= goal)) {
-            w = i;
-            start = base_in;
-        }
-        base_in += x;
-    }
-    if (w != warp) return;
-    // this warp's stretch again, 128 elements at a time
-    int token = -1, final_positive = -1;
-    double run = start;
-    for (int i = first; i < last && token < 0; i += 128) {
+    __syncthreads();
+    // its stretch again, the same number of neighbouring elements for each thread
+    const int each = ((draw_last - draw_first + kThreads - 1) / kThreads + 3) & ~3;
+    const int from = draw_first + static_cast<int>(threadIdx.x) * each;
+    const int to = min(from + each, draw_last);
+    float s = 0.f, e = 0.f;
+    for (int i = from; i < to; i += 4) {
         float x[4];
-        load_rest(r, i + 4 * lane, V, vec, x);
-        double own[4];
-        double s = 0.;
+        load_rest(r, i, V, vec, x);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) add_to(s, e, x[k]);
+    }
+    const Pair mine = renorm(s, e);
+    Pair before = lanes_below(mine, lane, &incl);
+    if (lane == 31) draw_part[warp] = incl;
+    __syncthreads();
+    {
+        const Pair part = lane < kWarps ? draw_part[lane] : Pair{0.f, 0.f};
+        const Pair start = draw_before + lanes_below(part, lane, &incl);
+        if (lane_of(part, start, goal) != warp) return;
+        before = shfl(start, warp) + before;
+    }
+    if (lane_of(mine, before, goal) != lane) return;
+    // this thread's elements one by one; the last one with anything in it where
+    // rounding leaves the sum at or below the goal
+    int token = -1;
+    Pair run = before;
+    for (int i = from; i < to; i += 4) {
+        float x[4];
+        load_rest(r, i, V, vec, x);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            s += static_cast<double>(x[k]);
-            own[k] = s;
+            if (x[k] > 0.f && (token < 0 || !(goal < run))) token = i + k;
+            run = run + Pair{x[k], 0.f};
         }
-        double before = s;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double y = __shfl_up_sync(kAll, before, o);
-            if (lane >= o) before += y;
-        }
-        const double end = __shfl_sync(kAll, before, 31);
-        before = run + (before - s);
-        int hit = -1, positive = -1;
-#pragma unroll
-        for (int k = 3; k >= 0; --k) {
-            if (x[k] > 0.f && before + own[k] > goal) hit = i + 4 * lane + k;
-            if (x[k] > 0.f && positive < 0) positive = i + 4 * lane + k;
-        }
-        const unsigned hits = __ballot_sync(kAll, hit >= 0), some = __ballot_sync(kAll, positive >= 0);
-        if (hits != 0) token = __shfl_sync(kAll, hit, __ffs(hits) - 1);
-        if (some != 0) final_positive = __shfl_sync(kAll, positive, 31 - __clz(some));
-        run += end;
     }
-    if (lane == 0) p.next_tokens[seq] = token >= 0 ? token : final_positive;
+    p.next_tokens[seq] = token;
 }
 
 }  // namespace
