@@ -256,6 +256,12 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
     return d;
 }
 
+__device__ __forceinline__ float fmin3(float a, float b, float c) {
+    float d;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -657,37 +663,84 @@ __device__ __forceinline__ void fetch_item(const ChunkParams &p, int n_big, int 
     for (int w = 0; w < kPartBlocks / 32; ++w) f.valid[w] = __ballot_sync(0xffffffffu, f.ids[w] >= 0);
 }
 
+constexpr float kNear = -1.f;
+
+// The n lowest of 16 bits (n may be anything).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+    return n >= kBS ? 0xFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
+}
+
 // The row's scores of this thread's 64 keys under the rules, in place: in units of
 // 1/a in the log2 domain (a returned), masked ones minus infinity, mx their maximum
-// times a.  The keys are four blocks of the tile's list from place v0 on, nbg of them
+// times a -- or (kNear returned) left raw, all of them seen and far below the cap.  The keys are four blocks of the tile's list from place v0 on, nbg of them
 // there, bad ones not in vmask.  Where the warp's rows see every key the masks are
-// passed over; capped scores up to the cap take a polynomial in packed pairs.
+// passed over.  Capped scores take a polynomial in packed pairs, the shorter one where
+// the warp's are all below 0.4 of the cap, a longer one up to the cap; only past it
+// do they need the special-function unit, which the weights already keep busy.
 __device__ __forceinline__ float rule_scores(const ChunkParams &p, uint32_t (&sx)[kGroupKeys],
                                              int nbg, uint32_t vmask, int v0, int pb, int skip,
                                              int prefix, int pos, float slope, float sl2,
                                              float &mx) {
-    int kp[kGroupKeys / kBS];  // positions of the blocks' first keys
-    bool whole = nbg == kGroupKeys / kBS && vmask == 0xFu, past = true;
-#pragma unroll
-    for (int b = 0; b < kGroupKeys / kBS; ++b) {
-        kp[b] = span_block(pb, skip, v0 + b) * kBS;
-        whole = whole && seen_whole(kp[b], pos, pos, p.rules.window, prefix);
-        past = past && kp[b] + kBS - 1 <= pos;
-    }
+    // positions of the blocks' first keys: consecutive but where the list skips
+    const int kp0 = span_block(pb, skip, v0) * kBS;
+    const bool even = v0 >= pb || v0 + kGroupKeys / kBS <= pb;
+    auto key_of = [&](int b) { return even ? kp0 + b * kBS : span_block(pb, skip, v0 + b) * kBS; };
+    const bool past = even && kp0 + kGroupKeys - 1 <= pos;
+    const bool whole = nbg == kGroupKeys / kBS && vmask == 0xFu &&
+                       ((past && pos - kp0 < p.rules.window) || (even && kp0 + kGroupKeys <= prefix));
     const bool fast = __all_sync(0xffffffffu, whole);
     float a = sl2;
     if (p.rules.cap_log2 > 0.f) {
         a = p.rules.cap_log2;
-        const float cs = p.rules.cap_scale;
-        const uint64_t cs2 = f32x2(cs, cs);
-        float top[4] = {0.f, 0.f, 0.f, 0.f};
+        // (columns past the step's keys hold an earlier step's scores, which must not
+        // choose the polynomial: the same call would not always round alike)
+        if (!__all_sync(0xffffffffu, nbg == kGroupKeys / kBS)) {
 #pragma unroll
-        for (int e = 0; e < kGroupKeys / 2; ++e)
-            top[e & 3] = fmax3(top[e & 3], fabsf(__uint_as_float(sx[2 * e])),
-                               fabsf(__uint_as_float(sx[2 * e + 1])));
-        // (a NaN score does not raise the maximum; the polynomial keeps it)
-        const float most = fmaxf(fmax3(top[0], top[1], top[2]), top[3]) * fabsf(cs);
-        if (__all_sync(0xffffffffu, most <= 1.f)) {
+            for (int e = 0; e < kGroupKeys; ++e)
+                if (e / kBS >= nbg) sx[e] = 0u;
+        }
+        // (a NaN score does not move the extremes; the polynomials keep it)
+        float lo[4], hi[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            hi[i] = kNegInf;
+            lo[i] = -kNegInf;
+        }
+#pragma unroll
+        for (int e = 0; e < kGroupKeys / 2; ++e) {
+            const float x0 = __uint_as_float(sx[2 * e]), x1 = __uint_as_float(sx[2 * e + 1]);
+            hi[e & 3] = fmax3(hi[e & 3], x0, x1);
+            lo[e & 3] = fmin3(lo[e & 3], x0, x1);
+        }
+        const float top = fmaxf(fmax3(hi[0], hi[1], hi[2]), hi[3]);
+        const float most = fmaxf(top, -fminf(fmin3(lo[0], lo[1], lo[2]), lo[3]));
+        const float cs = p.rules.cap_scale;
+        if (__all_sync(0xffffffffu, most <= p.rules.near_most)) {
+            const float n0 = p.rules.near[0], n1 = p.rules.near[1], n2 = p.rules.near[2],
+                        n3 = p.rules.near[3];
+            if (fast && p.rules.slopes == nullptr && n0 > 0.f) {
+                // (the capping rises with the score: the largest is that of the largest;
+                // the weights' loop does the others)
+                const float t = top * top;
+                mx = top * fmaf(t, fmaf(t, fmaf(t, n3, n2), n1), n0);
+                return kNear;
+            }
+            a = 1.f;
+            const uint64_t k0 = f32x2(n0, n0), k1 = f32x2(n1, n1), k2 = f32x2(n2, n2),
+                           k3 = f32x2(n3, n3);
+#pragma unroll
+            for (int e = 0; e < kGroupKeys / 2; ++e) {
+                const uint64_t x = f32x2(__uint_as_float(sx[2 * e]), __uint_as_float(sx[2 * e + 1]));
+                const uint64_t t = mul_f32x2(x, x);
+                uint64_t r = fma_f32x2(t, k3, k2);
+                r = fma_f32x2(t, r, k1);
+                r = fma_f32x2(t, r, k0);
+                const float2 v = f32x2_split(mul_f32x2(x, r));
+                sx[2 * e] = __float_as_uint(v.x);
+                sx[2 * e + 1] = __float_as_uint(v.y);
+            }
+        } else if (__all_sync(0xffffffffu, most * fabsf(cs) <= 1.f)) {
+            const uint64_t cs2 = f32x2(cs, cs);
             const uint64_t c0 = f32x2(dec::kTanh0, dec::kTanh0), c1 = f32x2(dec::kTanh1, dec::kTanh1),
                            c2 = f32x2(dec::kTanh2, dec::kTanh2), c3 = f32x2(dec::kTanh3, dec::kTanh3),
                            c4 = f32x2(dec::kTanh4, dec::kTanh4), c5 = f32x2(dec::kTanh5, dec::kTanh5),
@@ -721,7 +774,7 @@ __device__ __forceinline__ float rule_scores(const ChunkParams &p, uint32_t (&sx
             // keys at and before the row: the distance grows by one per key
 #pragma unroll
             for (int b = 0; b < kGroupKeys / kBS; ++b) {
-                const float bias = slope * static_cast<float>(kp[b] - pos);
+                const float bias = slope * static_cast<float>(kp0 + b * kBS - pos);
 #pragma unroll
                 for (int i = 0; i < kBS; ++i) {
                     uint32_t &x = sx[b * kBS + i];
@@ -731,7 +784,7 @@ __device__ __forceinline__ float rule_scores(const ChunkParams &p, uint32_t (&sx
         } else {
 #pragma unroll
             for (int b = 0; b < kGroupKeys / kBS; ++b) {
-                const float d0 = static_cast<float>(kp[b] - pos);
+                const float d0 = static_cast<float>(key_of(b) - pos);
 #pragma unroll
                 for (int i = 0; i < kBS; ++i) {
                     uint32_t &x = sx[b * kBS + i];
@@ -748,11 +801,20 @@ __device__ __forceinline__ float rule_scores(const ChunkParams &p, uint32_t (&sx
         const float s = a <= 0.f ? a : 1.f;
         if (a <= 0.f) a = 1.f;
 #pragma unroll
-        for (int e = 0; e < kGroupKeys; ++e) {
-            const int b = e / kBS, at = kp[b] + e % kBS;
-            const bool vis = b < nbg && ((vmask >> b) & 1u) &&
-                             dec::rule_sees(pos, at, p.rules.window, prefix);
-            sx[e] = vis ? __float_as_uint(__uint_as_float(sx[e]) * s) : __float_as_uint(kNegInf);
+        for (int b = 0; b < kGroupKeys / kBS; ++b) {
+            // bits of the block's keys that the row sees: up to its position, from its
+            // window's start on, or in the prefix
+            const int kp = key_of(b), d = pos - kp;
+            uint32_t seen = low_bits(d + 1);
+            if (d >= p.rules.window) seen &= ~low_bits(d - p.rules.window + 1);
+            seen |= low_bits(prefix - kp);
+            if (b >= nbg || !((vmask >> b) & 1u)) seen = 0u;
+#pragma unroll
+            for (int i = 0; i < kBS; ++i) {
+                uint32_t &x = sx[b * kBS + i];
+                x = (seen >> i) & 1u ? __float_as_uint(__uint_as_float(x) * s)
+                                     : __float_as_uint(kNegInf);
+            }
         }
     }
     float mr[8];
@@ -1084,9 +1146,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // finite (0 * NaN is not 0), which the rows that see them add
                     // at the end
                     bool dirty = false, touched = false;
-                    for (int b = 0; b < nb; ++b) {
-                        const int kp = span_block(pb, skip, blo + m * kStepBlocks + b) * kBS;
-                        if (seen_whole(kp, a0, a1, p.rules.window, prefix) && kp + kBS <= L) continue;
+                    const int mine = span_block(pb, skip, blo + m * kStepBlocks + lane) * kBS;
+                    uint32_t part_seen = __ballot_sync(
+                        0xffffffffu,
+                        lane < nb && !seen_whole(mine, a0, a1, p.rules.window, prefix));
+                    for (; part_seen != 0; part_seen &= part_seen - 1) {
+                        const int b = __ffs(part_seen) - 1;
+                        const int kp = __shfl_sync(0xffffffffu, mine, b);
                         uint8_t *vb = smem + Gm::kOffV + vs * Gm::kV + b * Gm::kVBlock;
                         const bool bad = clean_block<CH>(vb, L - kp, lane, &touched);
                         dirty = dirty || bad;
@@ -1296,13 +1362,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t a2 = f32x2(a, a), nms2 = f32x2(nms, nms);
                 uint64_t l2[4] = {0ull, 0ull, 0ull, 0ull};
                 uint32_t x[32];
+                if (kRules && a == kNear) {
+                    // capped scores far below the cap: x (n0 + n1 x^2 + ..) - m
+                    const float n0 = p.rules.near[0], n1 = p.rules.near[1],
+                                n2 = p.rules.near[2], n3 = p.rules.near[3];
+                    const uint64_t k0 = f32x2(n0, n0), k1 = f32x2(n1, n1), k2 = f32x2(n2, n2),
+                                   k3 = f32x2(n3, n3);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const float2 t = f32x2_split(fma_f32x2(
-                        f32x2(__uint_as_float(sx[2 * e]), __uint_as_float(sx[2 * e + 1])), a2, nms2));
-                    const float p0 = ex2(t.x), p1 = ex2(t.y);
-                    l2[e & 3] = add_f32x2(l2[e & 3], f32x2(p0, p1));
-                    x[e] = pack_half2(p0, p1);
+                    for (int e = 0; e < 32; ++e) {
+                        const uint64_t y = f32x2(__uint_as_float(sx[2 * e]),
+                                                 __uint_as_float(sx[2 * e + 1]));
+                        const uint64_t t2 = mul_f32x2(y, y);
+                        uint64_t r = fma_f32x2(t2, k3, k2);
+                        r = fma_f32x2(t2, r, k1);
+                        r = fma_f32x2(t2, r, k0);
+                        const float2 t = f32x2_split(fma_f32x2(y, r, nms2));
+                        const float p0 = ex2(t.x), p1 = ex2(t.y);
+                        l2[e & 3] = add_f32x2(l2[e & 3], f32x2(p0, p1));
+                        x[e] = pack_half2(p0, p1);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float2 t = f32x2_split(fma_f32x2(
+                            f32x2(__uint_as_float(sx[2 * e]), __uint_as_float(sx[2 * e + 1])), a2,
+                            nms2));
+                        const float p0 = ex2(t.x), p1 = ex2(t.y);
+                        l2[e & 3] = add_f32x2(l2[e & 3], f32x2(p0, p1));
+                        x[e] = pack_half2(p0, p1);
+                    }
                 }
                 tc::st32_halves<32>(tl + kTmemP + 64 * pb, x);
                 const float2 la = f32x2_split(add_f32x2(add_f32x2(l2[0], l2[1]), add_f32x2(l2[2], l2[3])));
@@ -1342,7 +1430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int b = 0; b < nblk; ++b) {
                         const int blk = span_block(pb, skip, part * kPartBlocks + b);
                         const int kp = blk * kBS;
-                        if (seen_whole(kp, a0, a1, p.rules.window, prefix) && kp + kBS <= L) continue;
+                        if (seen_whole(kp, a0, a1, p.rules.window, prefix)) continue;
                         const int64_t id = __ldg(p.block_tables +
                                                  static_cast<int64_t>(seq) * p.max_blocks_per_seq + blk);
                         if (id < 0 || id >= p.num_blocks) continue;

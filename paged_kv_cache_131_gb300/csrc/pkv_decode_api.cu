@@ -61,12 +61,22 @@ int make_rules(const pkv_score_rules *rules, float scale, RuleParams *out) {
         return PKV_ERR_INVALID;
     if (!aligned(rules->slopes, 4) || !aligned(rules->prefix_lens, 4)) return PKV_ERR_ALIGNMENT;
     out->cap_log2 = out->cap_scale = 0.f;
+    out->near_most = -1.f;
     if (rules->softcap > 0.f) {
         const double cap = rules->softcap;
         out->cap_log2 = static_cast<float>(cap * 1.4426950408889634);
         out->cap_scale = static_cast<float>(static_cast<double>(scale) / cap);
         if (!std::isfinite(out->cap_log2) || !std::isfinite(out->cap_scale))
             return PKV_ERR_INVALID;
+        // tanh(y) = y (c0 + c1 y^2 + c2 y^4 + c3 y^6) for |y| <= 0.4, off by 2^-23.3 of
+        // itself (fitted for this file, least squares reweighted towards the smallest
+        // largest error); outside this range of scales the powers leave fp32's
+        const double c[4] = {0.9999999019031751, -0.33331362466374176, 0.13270976805662424,
+                             -0.04755360366260839};
+        const double cs = std::fabs(static_cast<double>(scale) / cap);
+        double power = static_cast<double>(scale) * 1.4426950408889634;
+        for (int i = 0; i < 4; ++i, power *= cs * cs) out->near[i] = static_cast<float>(c[i] * power);
+        out->near_most = cs >= 1e-5 && cs <= 1e4 ? static_cast<float>(0.4 / cs) : -1.f;
     }
     out->window = rules->window > 0 ? rules->window : INT32_MAX;
     out->slopes = rules->slopes;

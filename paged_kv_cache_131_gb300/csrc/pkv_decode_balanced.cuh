@@ -52,6 +52,7 @@ namespace dec {
 
 constexpr int kMaxStages = 4;
 constexpr int kMaxStagesFp8 = 6;  // FP8 stages are half the size: keep as many bytes in flight
+constexpr int kMinBlocks = 4;
 constexpr int kMaxThreads = (kMaxBalancedKvHeads + 1) * 32;
 // Dynamic shared memory:
 //   ring   stages * (key tile, value tile[, key scales, value scales]),
@@ -356,7 +357,10 @@ __device__ __forceinline__ void balanced_body(const BalancedParams &p, uint8_t *
     // ---- empty sequences get zeros (no block of theirs is in any range)
     const int64_t Tb = cum[S];                 // blocks of one head group
     const int64_t T = Tb * p.groups;           // the whole (group, sequence, block) list
-    const int64_t N = min(static_cast<int64_t>(grid), T);
+    // (under rules a CTA takes kMinBlocks blocks or more: a sequence cut finer is
+    // sooner read, but later merged)
+    const int64_t N = min(static_cast<int64_t>(grid),
+                          kScored ? (T + kMinBlocks - 1) / kMinBlocks : T);
     bool zeros_due = false;
     for (int s = blockIdx.x; s < S && !zeros_due; s += grid) zeros_due = lens[s] == 0;
     if (zeros_due && (blockIdx.x >= N || warp < Hc)) {
@@ -570,6 +574,9 @@ __device__ __forceinline__ void balanced_body(const BalancedParams &p, uint8_t *
         br.window = p.rules.window;
         br.cap_log2 = p.rules.cap_log2;
         br.cap_scale = p.rules.cap_scale;
+        br.near_most = p.rules.near_most;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) br.near[i] = p.rules.near[i];
         br.biased = p.rules.slopes != nullptr;
     }
     // under rules: values of keys that the token does not see never reach it,

@@ -56,7 +56,8 @@ struct SwizzledTile {
 // by least squares reweighted towards the smallest largest error: 2^-24.2 of the
 // value), fused multiply-adds alone.  Beyond, 1 - 2 / (1 + e^(2y)) costs two
 // special-function instructions and is off by a few 2^-24; its limits (0 and
-// infinity of e^(2y)) come out as -1 and 1.
+// infinity of e^(2y)) come out as -1 and 1.  Where all of a warp's scores are below 0.4
+// of the cap a shorter polynomial with the scales multiplied in does (RuleParams).
 //
 // Softmax weights under rules stand 2^15 higher than 2^(t - max): as fp16 for
 // the P V MMA they keep 11 bits down to 2^-29 of the row's largest, and are off
@@ -71,6 +72,7 @@ struct BlockRules {
     int qpos;         // the (first) query token's position
     float cap_log2;   // softcap * log2(e), 0: not capped
     float cap_scale;  // scale / softcap
+    float near_most, near[4];  // (RuleParams)
     bool biased;      // there are slopes
     uint32_t seen;    // (one query token) bits of the block's keys that it sees
 };
@@ -105,18 +107,27 @@ __device__ __forceinline__ float tanh_far(float y) {
 }
 
 // N raw scores q.k under the rules before the mask, in place: in log2 units; d(i)
-// gives score i's distance, slope(i) its head's slope (log2 units).  (Both forms of
-// the cap: with one or two warps a scheduler they cost less than a vote and a
-// branch, 129 us against 138 for 64 x 4 drafted tokens.)
+// gives score i's distance, slope(i) its head's slope (log2 units).  Every lane.
 template <int N, class Distance, class Slope>
 __device__ __forceinline__ void rule_scores(float (&x)[N], float scale_log2, const BlockRules &br,
                                             Distance d, Slope slope) {
     if (br.cap_log2 > 0.f) {
+        bool near = true;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float y = x[i] * br.cap_scale;
-            const float near = tanh_near(y), far = tanh_far(y);
-            x[i] = br.cap_log2 * (fabsf(y) <= 1.f ? near : far);
+        for (int i = 0; i < N; ++i) near = near && fabsf(x[i]) <= br.near_most;
+        if (__all_sync(0xffffffffu, near)) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float t = x[i] * x[i];
+                x[i] *= fmaf(t, fmaf(t, fmaf(t, br.near[3], br.near[2]), br.near[1]), br.near[0]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float y = x[i] * br.cap_scale;
+                const float poly = tanh_near(y), limit = tanh_far(y);
+                x[i] = br.cap_log2 * (fabsf(y) <= 1.f ? poly : limit);
+            }
         }
     } else {
 #pragma unroll
@@ -127,6 +138,12 @@ __device__ __forceinline__ void rule_scores(float (&x)[N], float scale_log2, con
         for (int i = 0; i < N; ++i)
             x[i] = fmaf(-slope(i), fabsf(static_cast<float>(d(i))), x[i]);
     }
+}
+
+// floor(log2 x) of a normal x > 0 without the special-function unit.
+__device__ __forceinline__ float exponent_of(float x) {
+    const uint32_t e = (__float_as_uint(x) >> 23) & 0xFFu;
+    return __uint_as_float(0x4B000000u | e) - (8388608.f + 127.f);
 }
 
 // Whether the token at position a sees the key at position b (b < L).
@@ -283,7 +300,7 @@ struct MmaPolicy {
         for (int j = 0; j < 4; ++j) {
             const int tok = g + 8 * (j >> 1);
             if constexpr (kRules) {
-                if (!((br.seen >> tok) & 1u)) x[j] = kNegInf;
+                if (br.seen != 0xFFFFu && !((br.seen >> tok) & 1u)) x[j] = kNegInf;
             } else {
                 x[j] = tok < nv ? (sa[j] + sb[j]) * scale_log2 : kNegInf;
             }
@@ -818,12 +835,14 @@ struct MmaFp8Policy {
             for (int j = 0; j < 4; ++j) x[b][j] = sa[j] + sb[j];
         }
         // scale, mask, and the block max of each of the lane's two heads
-        float lv[NB][kLaneTokens];  // log2 of the value scales (bounded below: a zero has none)
+        // exponents of the value scales (bounded below: a zero has none): the weights'
+        // reference is one lower for what they leave out
+        float lv[NB][kLaneTokens];
         if constexpr (kRules) {
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int r = 0; r < kLaneTokens; ++r) lv[b][r] = fmaxf(__log2f(vs[b][r]), -64.f);
+                for (int r = 0; r < kLaneTokens; ++r) lv[b][r] = fmaxf(exponent_of(vs[b][r]), -64.f);
         }
         float mx[2] = {kNegInf, kNegInf};
 #pragma unroll
@@ -843,7 +862,7 @@ struct MmaFp8Policy {
                     // the reference follows the largest product of weight and value
                     // scale, so that product fits fp16 whatever the scales are
                     const int tok = token_of(lane, r);
-                    if (!((br[b].seen >> tok) & 1u)) x[b][j] = kNegInf;
+                    if (br[b].seen != 0xFFFFu && !((br[b].seen >> tok) & 1u)) x[b][j] = kNegInf;
                     mx[j & 1] = fmaxf(mx[j & 1], x[b][j] + lv[b][r]);
                 } else {
                     x[b][j] = token_of(lane, r) < nv[b] ? (x[b][j] * ks[b][r]) * scale_log2 : kNegInf;
@@ -864,7 +883,7 @@ struct MmaFp8Policy {
             if constexpr (kRules) {
                 const float safe = mnew == kNegInf ? 0.f : mnew;
                 alpha[h] = rule_ex2(m[h] - safe);
-                ref[h] = safe - kRuleShift;
+                ref[h] = safe - (kRuleShift - 1.f);
             } else {
                 alpha[h] = exp2f(m[h] - mnew);
                 ref[h] = mnew;

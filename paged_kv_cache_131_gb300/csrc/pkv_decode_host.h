@@ -81,6 +81,10 @@ int launch_grid(const GridParams &p, int D, int G, bool simt, int num_seqs,
 struct RuleParams {
     float cap_log2;   // softcap * log2(e); 0: not capped
     float cap_scale;  // scale / softcap
+    // scores far below the cap: |q.k| <= near_most takes x (k0 + k1 x^2 + ..), the
+    // capping's polynomial with the scales multiplied in (near_most < 0: not)
+    float near_most;
+    float near[4];
     int window;
     const float *slopes;
     const int32_t *prefix_lens;
