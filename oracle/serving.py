@@ -125,10 +125,14 @@ def scored_attention(q, k, v, block_tables, seq_lens, query_start, scale, num_kv
     weights and outputs may be off by.  Per key, in units of its weight: 2^-11 for
     the weight's rounding; the score's error in nats -- (D + 8) 2^-24 of
     sum |q||k| scale for the dot product, its scaling and the exponential's
-    argument, 33 2^-24 of the capped score for the capping (8 2^-24 of the cap from a
-    quarter of it on, less below), 4 2^-24 of slope * distance for the bias -- and 2^-20 for the exponential and sums of roundings.  A weight's
+    argument, for the capping 10 2^-24 of the cap up to caps of 355 (1 - 2 / (1 + e^2y):
+    2^-23 for the exponential's 2 units in its last place times the largest slope 1/2 of
+    tanh in its logarithm, 2^-24 / 2 for its argument, 2^-22 and 2^-23 for the quotient
+    and its divisor, which is at most 2, 2^-24 for the difference), for higher ones
+    14 2^-24 of the score (the same past the cap, where tanh is above 0.76; less below),
+    4 2^-24 of slope * distance for the bias -- and 2^-20 for the exponential and sums of roundings.  A weight's
     error moves the output by its share times (v - out).  Weights below fp16's
-    normal range are off by 2^-36 of the largest at most."""
+    normal range are off by 2^-32 of the largest at most."""
     q = np.asarray(q, np.float64)
     Tq, H, D = q.shape
     G, bs = H // num_kv_heads, k.shape[1]
@@ -155,7 +159,7 @@ def scored_attention(q, k, v, block_tables, seq_lens, query_start, scale, num_kv
                 err = (np.abs(K) @ np.abs(q[r, h])) * abs(scale) * (D + 8) * 2.0 ** -24
                 if softcap:
                     s = softcap * np.tanh(s / softcap)
-                    err = err + np.abs(s) * 33 * 2.0 ** -24
+                    err = err + (10 * softcap if softcap <= 355 else 14 * np.abs(s)) * 2.0 ** -24
                 if slopes is not None:
                     bias = float(slopes[h]) * np.abs(a - at)
                     s = s - bias
@@ -167,5 +171,5 @@ def scored_attention(q, k, v, block_tables, seq_lens, query_start, scale, num_kv
                 out[r, h] = o
                 tol[r, h] += (np.abs(o) * 2.0 ** -11 +
                               ((w * rel) @ (np.abs(V) + np.abs(o))) / w.sum() +
-                              len(at) * 2.0 ** -35 * np.abs(V).max() / w.sum())
+                              len(at) * 2.0 ** -31 * np.abs(V).max() / w.sum())
     return out, tol

@@ -51,13 +51,18 @@ struct SwizzledTile {
 // ---------------------------------------------------------------------------
 // Score rules (pkv_score_rules) as a policy applies them, everything in the
 // log2 domain: t = cap * tanh(y), y = scale q.k / cap, then a bias of -slope *
-// distance, then the mask.  Up to |y| = 1 -- where a model's cap leaves most of its
-// scores -- tanh(y) is y times a polynomial of degree 6 in y^2 (fitted for this file
-// by least squares reweighted towards the smallest largest error: 2^-24.2 of the
-// value), fused multiply-adds alone.  Beyond, 1 - 2 / (1 + e^(2y)) costs two
-// special-function instructions and is off by a few 2^-24; its limits (0 and
-// infinity of e^(2y)) come out as -1 and 1.  Where all of a warp's scores are below 0.4
-// of the cap a shorter polynomial with the scales multiplied in does (RuleParams).
+// distance, then the mask.
+//  - Where all of a warp's scores are below 0.4 of the cap -- where a model's cap
+//    leaves most of them -- tanh(y) is y times a polynomial of degree 3 in y^2 with the
+//    scales multiplied in (RuleParams), off by 2^-23.3 of itself.
+//  - Else 1 - 2 / (1 + e^(2y)), two special-function instructions, off by
+//    10 2^-24 (of the cap, once multiplied); its limits (0 and infinity of e^(2y))
+//    come out as -1 and 1.  For caps up to 512 in log2 units that is below 2^-11, a
+//    weight's own rounding.
+//  - With higher caps that would swallow small scores: up to |y| = 1 a polynomial of
+//    degree 6 in y^2 takes its place, off by 2^-24.2 of the value.
+// (Both polynomials fitted for this library by least squares reweighted towards the
+// smallest largest error.)
 //
 // Softmax weights under rules stand 2^15 higher than 2^(t - max): as fp16 for
 // the P V MMA they keep 11 bits down to 2^-29 of the row's largest, and are off
@@ -101,9 +106,11 @@ __device__ __forceinline__ float tanh_near(float y) {
     return y * fmaf(t2 * t2, hi, lo);
 }
 
-// tanh(y) for |y| > 1 (and NaN).
-__device__ __forceinline__ float tanh_far(float y) {
-    return fmaf(-2.f, rule_rcp(1.f + rule_ex2(y * (2.f * kLog2e))), 1.f);
+constexpr float kExpCapLog2 = 512.f;
+
+// tanh(y) of x = 2 y log2(e) (NaN stays).
+__device__ __forceinline__ float tanh_exp(float x) {
+    return fmaf(-2.f, rule_rcp(1.f + rule_ex2(x)), 1.f);
 }
 
 // N raw scores q.k under the rules before the mask, in place: in log2 units; d(i)
@@ -121,12 +128,16 @@ __device__ __forceinline__ void rule_scores(float (&x)[N], float scale_log2, con
                 const float t = x[i] * x[i];
                 x[i] *= fmaf(t, fmaf(t, fmaf(t, br.near[3], br.near[2]), br.near[1]), br.near[0]);
             }
+        } else if (br.cap_log2 <= kExpCapLog2) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                x[i] = br.cap_log2 * tanh_exp(x[i] * (br.cap_scale * (2.f * kLog2e)));
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const float y = x[i] * br.cap_scale;
-                const float poly = tanh_near(y), limit = tanh_far(y);
-                x[i] = br.cap_log2 * (fabsf(y) <= 1.f ? poly : limit);
+                x[i] = br.cap_log2 *
+                       (fabsf(y) <= 1.f ? tanh_near(y) : tanh_exp(y * (2.f * kLog2e)));
             }
         }
     } else {
