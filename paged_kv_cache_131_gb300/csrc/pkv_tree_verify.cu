@@ -17,8 +17,9 @@
 // the warp's stretch again (out of L2), a few elements a thread.
 //
 // Arithmetic: an element of R is one fused multiply-add of the row's fp32 values
-// (C as a pair of fp32: one rounding); sums, masses and tests are carried as
-// pairs of fp32 whose errors are kept (47 bits).  fp64 would hold as much, but its
+// (C as a pair of fp32: one rounding, 2^-24 of it), four neighbours are added in fp32
+// (as much again), and from there sums, masses and tests are carried as pairs of
+// fp32 whose errors are kept (47 bits).  fp64 would hold as much, but its
 // rate here is 2 a cycle and SM, and every warp walks: the same kernel in fp64
 // took 22.6, 129 and 44 us for a chain of 5 nodes, 64 trees of 16 (V 128256) and
 // 32 of 63 without drafts.
@@ -27,6 +28,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/pagedkv.h"
@@ -209,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     const int V = p.vocab;
     const bool drafted = p.draft != nullptr;
 
+    cluster.barrier_arrive();
     grid_dependency_wait();
     const int row0 = __ldg(p.query_start + seq), row1 = __ldg(p.query_start + seq + 1);
     int Q = row1 - row0;
@@ -218,6 +221,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     }
     int32_t *path = p.path + static_cast<int64_t>(seq) * p.max_depth;
     if (Q == 0) {  // (the whole cluster)
+        cluster.barrier_wait();
         if (cta == 0) {
             for (int d = threadIdx.x; d < p.max_depth; d += kThreads) path[d] = -1;
             if (threadIdx.x == 0) {
@@ -257,8 +261,8 @@ __global__ void __launch_bounds__(kThreads, 3)
     }
     const float draw_u = unit(__ldg(p.sample_u + seq));
     __syncthreads();
-    // (the first exchange writes other CTAs' shared memory: all have started)
-    cluster.sync();
+    // (the first exchange writes other CTAs' shared memory: all have started by then)
+    cluster.barrier_wait();
 
     int pass = 0;
     bool vec = false;
@@ -291,37 +295,39 @@ __global__ void __launch_bounds__(kThreads, 3)
             for (; i < min(last, 0); i += 128) {
                 float x[4];
                 load_rest(r, i, V, vec, x);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) add_to(s, e, x[k]);
+                add_to(s, e, (x[0] + x[1]) + (x[2] + x[3]));
             }
-            for (; i + (kBatch - 1) * 128 + 4 <= min(last, V); i += kBatch * 128) {
-                float4 a[kBatch], b[kBatch];
+            const int whole = min(last, V) - (kBatch - 1) * 128 - 4;
+            if (r.q == nullptr) {
+                for (; i <= whole; i += kBatch * 128) {
+                    float4 a[kBatch];
 #pragma unroll
-                for (int j = 0; j < kBatch; ++j) {
-                    a[j] = __ldg(reinterpret_cast<const float4 *>(r.p + i + j * 128));
-                    if (r.q != nullptr)
-                        b[j] = __ldg(reinterpret_cast<const float4 *>(r.q + i + j * 128));
+                    for (int j = 0; j < kBatch; ++j)
+                        a[j] = __ldg(reinterpret_cast<const float4 *>(r.p + i + j * 128));
+#pragma unroll
+                    for (int j = 0; j < kBatch; ++j)
+                        add_to(s, e, (fmaxf(a[j].x, 0.f) + fmaxf(a[j].y, 0.f)) +
+                                         (fmaxf(a[j].z, 0.f) + fmaxf(a[j].w, 0.f)));
                 }
+            } else {
+                for (; i <= whole; i += kBatch * 128) {
+                    float4 a[kBatch], b[kBatch];
 #pragma unroll
-                for (int j = 0; j < kBatch; ++j) {
-                    if (r.q != nullptr) {
-                        a[j].x = rest_of(r, a[j].x, b[j].x);
-                        a[j].y = rest_of(r, a[j].y, b[j].y);
-                        a[j].z = rest_of(r, a[j].z, b[j].z);
-                        a[j].w = rest_of(r, a[j].w, b[j].w);
+                    for (int j = 0; j < kBatch; ++j) {
+                        a[j] = __ldg(reinterpret_cast<const float4 *>(r.p + i + j * 128));
+                        b[j] = __ldg(reinterpret_cast<const float4 *>(r.q + i + j * 128));
                     }
-                    add_to(s, e, fmaxf(a[j].x, 0.f));
-                    add_to(s, e, fmaxf(a[j].y, 0.f));
-                    add_to(s, e, fmaxf(a[j].z, 0.f));
-                    add_to(s, e, fmaxf(a[j].w, 0.f));
+#pragma unroll
+                    for (int j = 0; j < kBatch; ++j)
+                        add_to(s, e, (rest_of(r, a[j].x, b[j].x) + rest_of(r, a[j].y, b[j].y)) +
+                                         (rest_of(r, a[j].z, b[j].z) + rest_of(r, a[j].w, b[j].w)));
                 }
             }
         }
         for (; i < last; i += 128) {
             float x[4];
             load_rest(r, i, V, vec, x);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) add_to(s, e, x[k]);
+            add_to(s, e, (x[0] + x[1]) + (x[2] + x[3]));
         }
         const Pair w = lanes_sum(renorm(s, e));
         const int half = pass & 1;
@@ -338,6 +344,7 @@ __global__ void __launch_bounds__(kThreads, 3)
 
     // ---- the walk (every warp of the cluster alike)
     int at = 0, depth = 1;
+    int mine_gone[kNodesPerLane], seen = 0;  // fixed guesses rejected at this node
     bool summed = false;  // the last pass summed r as it stands
     Pair total{0.f, 0.f};
     if (cta == 0 && threadIdx.x == 0) path[0] = 0;
@@ -345,10 +352,12 @@ __global__ void __launch_bounds__(kThreads, 3)
         open(at);
         summed = false;
         int step = -1;
+        seen = 0;
+#pragma unroll
+        for (int g = 0; g < kNodesPerLane; ++g) mine_gone[g] = -1;
         if (depth < p.max_depth) {
             Pair W{1.f, 0.f}, C{0.f, 0.f};
             bool empty = false;
-            int seen = 0;  // tokens in `gone`
             for (int j = 0; j < kNodesPerLane && step < 0 && !empty; ++j) {
                 unsigned kids = __ballot_sync(kAll, up[j] == at);
                 while (kids != 0 && step < 0 && !empty) {
@@ -378,9 +387,13 @@ __global__ void __launch_bounds__(kThreads, 3)
                             empty = true;
                         }
                     } else {
-                        // (a guess that was rejected before has nothing left)
+                        // (a guess that was rejected before has nothing left; lane l of
+                        // every warp holds rejected tokens l, 32 + l, ..)
+                        const int token = node_token[k];
                         bool again = false;
-                        for (int g = 0; g < seen; ++g) again = again || gone[g] == node_token[k];
+#pragma unroll
+                        for (int g = 0; g < kNodesPerLane; ++g) again = again || mine_gone[g] == token;
+                        again = __any_sync(kAll, again);
                         const Pair have{again ? 0.f : pt, 0.f};
                         if (W * u < have) {
                             step = k;
@@ -392,12 +405,10 @@ __global__ void __launch_bounds__(kThreads, 3)
                         } else {
                             W = less;
                             if (!again) {
-                                // every warp has read the list up to here
-                                __syncthreads();
-                                if (threadIdx.x == 0) gone[seen] = node_token[k];
-                                __syncthreads();
+#pragma unroll
+                                for (int g = 0; g < kNodesPerLane; ++g)
+                                    if (seen == 32 * g + lane) mine_gone[g] = token;
                                 ++seen;
-                                r.num_gone = seen;
                             }
                         }
                     }
@@ -411,6 +422,15 @@ __global__ void __launch_bounds__(kThreads, 3)
     }
 
     // ---- the next token
+    if (seen > 0) {  // (every thread alike)
+        if (warp == 0) {
+#pragma unroll
+            for (int g = 0; g < kNodesPerLane; ++g)
+                if (mine_gone[g] >= 0) gone[32 * g + lane] = mine_gone[g];
+        }
+        __syncthreads();
+        r.num_gone = seen;
+    }
     if (!summed) total = sum_rest();
     const int half = (pass - 1) & 1;
     if (cta == 0) {
@@ -478,6 +498,40 @@ __global__ void __launch_bounds__(kThreads, 3)
     p.next_tokens[seq] = token;
 }
 
+// CTAs of a sequence's cluster: as many (up to 8, and a vector of 16 bytes for each
+// thread) as let all sequences' clusters run at once, since a sequence that starts when
+// another ends adds its whole chain to the call -- 64 sequences of V 128256: 33.6 us
+// with 6 CTAs, all at once; 37.7 with 7 and 40.2 with 8, which do not all fit; 43.7
+// with 4.  Returns a negative number on a CUDA error.
+int cluster_size(int num_seqs, int vocab) {
+    constexpr int kDevices = 256;
+    static std::atomic<int> fits[kDevices][kMaxCluster];  // 1 + clusters at once; 0: not asked
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_failure(e, "cudaGetDevice");
+    const int most = std::max(1, std::min(kMaxCluster, (vocab + 4 * kThreads - 1) / (4 * kThreads)));
+    for (int c = most; c > 1; --c) {
+        int n = dev < kDevices ? fits[dev][c - 1].load(std::memory_order_relaxed) - 1 : -1;
+        if (n < 0) {
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = c;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(static_cast<unsigned>(c));
+            cfg.blockDim = dim3(kThreads);
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&n, tree_verify_kernel, &cfg);
+            if (e != cudaSuccess) return cuda_failure(e, "cudaOccupancyMaxActiveClusters");
+            if (dev < kDevices) fits[dev][c - 1].store(n + 1, std::memory_order_relaxed);
+        }
+        if (n >= num_seqs) return c;
+    }
+    return 1;
+}
+
 }  // namespace
 }  // namespace pkv
 
@@ -524,7 +578,8 @@ extern "C" int pkv_tree_verify(int32_t *path, int32_t max_depth, int32_t *path_l
     p.vocab = vocab_size;
     p.err = device_error_record();
     if (p.err == nullptr) return PKV_ERR_CUDA;
-    const int ctas = kMaxCluster;
+    const int ctas = cluster_size(num_seqs, vocab_size);
+    if (ctas < 0) return PKV_ERR_CUDA;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
