@@ -47,7 +47,7 @@
 //    more than 2^8 (the weights stay <= 256): then each thread rescales its
 //    half of the row's O in tensor memory first.  The result O / l does not
 //    depend on which reference was used.
-// A tile whose causal range fits one partition writes fp16 out; otherwise
+// A tile whose range fits one partition writes fp16 out; otherwise
 // every partition leaves fp32 partial states (m, l, O) and, per softmax warp,
 // the last CTA of the tile to take a ticket merges them with a log-sum-exp
 // rescale.  No CTA waits for another.
@@ -82,6 +82,11 @@ constexpr int kVStages = 2;                    // value ring depth (steps)
 constexpr int kPartTokens = 4096;              // KV partition
 constexpr int kClaimLead = 1;                  // steps staged after the next item is claimed
 constexpr int kPartBlocks = kPartTokens / kBS;
+// under rules partitions are twice as long: an item that leaves a partial state costs
+// its softmax warps about 8 us (stores, ticket, merge), a tenth of a partition's steps
+constexpr int kRulePartBlocks = 2 * kPartBlocks;
+template <bool kRules>
+constexpr int part_blocks = kRules ? kRulePartBlocks : kPartBlocks;
 // softmax: eight warps; warp 3 + 4 wh + q takes the rows (tensor-memory
 // lanes) 32 q + 16 wh .. + 15, two threads per row: lanes 16 h + i take keys
 // 64 h .. 64 h + 63 of a step and the head dimensions (D/2) h .. of O
@@ -162,7 +167,9 @@ struct ItemInfo {
     int nsteps, nblk, L, Q;
     int q0, nparts, done, prefix;
     uint32_t valid[kPartBlocks / 32];  // one bit per block of the partition: id in range
-    int pb, skip, pad0, pad1;  // (under rules) see Span
+    int pb, skip;    // (under rules) see Span
+    int all_valid;   // (under rules) every id in range
+    int pad;
 };
 
 // Shared memory (from a 1024-aligned base): the query tile being staged,
@@ -294,7 +301,8 @@ __device__ __forceinline__ bool seq_geo(const ChunkParams &p, int s, int G, bool
     sg.rows = Q * G;
     if (sg.rows < p.min_rows || sg.rows == 0) return false;
     sg.tiles = (sg.rows + kRows - 1) / kRows;
-    sg.parts = (L + kPartTokens - 1) / kPartTokens;
+    constexpr int kTokens = part_blocks<kRules> * kBS;
+    sg.parts = (L + kTokens - 1) / kTokens;
     sg.prefix = 0;
     if constexpr (kRules) {
         if (p.rules.prefix_lens != nullptr)
@@ -303,7 +311,7 @@ __device__ __forceinline__ bool seq_geo(const ChunkParams &p, int s, int G, bool
             // a tile's window spans window + 128 / G - 1 positions at most
             const int most = (sg.prefix + kBS - 1) / kBS +
                              (p.rules.window + kRows / G) / kBS + 2;
-            sg.parts = min(sg.parts, (most + kPartBlocks - 1) / kPartBlocks);
+            sg.parts = min(sg.parts, (most + kRulePartBlocks - 1) / kRulePartBlocks);
         }
     }
     return true;
@@ -550,14 +558,14 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const __grid_constant_
     }
 }
 
-// Block ids of an item's partition: lane l holds blocks l, 32 + l, 64 + l and
-// 96 + l of it; -1 past the item or out of range (recorded when `report`).
+// Block ids of an item's partition: lane l holds blocks l, 32 + l, .. of it; -1 past the item or out of range (recorded when `report`).
 // (pb, skip: under rules the list of blocks is a tile's Span.)
+template <int W>
 __device__ __forceinline__ void load_ids(const ChunkParams &p, int seq, int blo, int nblk,
-                                         int lane, bool report, int (&ids)[kPartBlocks / 32],
-                                         int pb = 0, int skip = 0) {
+                                         int lane, bool report, int (&ids)[W], int pb = 0,
+                                         int skip = 0) {
 #pragma unroll
-    for (int w = 0; w < kPartBlocks / 32; ++w) {
+    for (int w = 0; w < W; ++w) {
         const int b = w * 32 + lane;
         int id = -1;
         if (b < nblk) {
@@ -574,10 +582,11 @@ __device__ __forceinline__ void load_ids(const ChunkParams &p, int seq, int blo,
 }
 
 // Block b's id (every lane calls).
-__device__ __forceinline__ int id_of(const int (&ids)[kPartBlocks / 32], int b) {
+template <int W>
+__device__ __forceinline__ int id_of(const int (&ids)[W], int b) {
     int v = -1;
 #pragma unroll
-    for (int w = 0; w < kPartBlocks / 32; ++w) {
+    for (int w = 0; w < W; ++w) {
         const int x = __shfl_sync(0xffffffffu, ids[w], b & 31);
         if ((b >> 5) == w) v = x;
     }
@@ -601,16 +610,17 @@ __device__ __forceinline__ int3 decode_item(const SeqGeo &sg, int local, int G, 
 
 // An item as the key producer takes it from the list (every lane holds the
 // scalars; block ids are spread over the lanes).
+template <bool kRules>
 struct Fetched {
     int done, seq, part, kvh, tile, nsteps, nblk, L, Q, q0, nparts;
-    int prefix, pb, skip;  // (under rules)
-    int ids[kPartBlocks / 32];
-    uint32_t valid[kPartBlocks / 32];
+    int prefix, pb, skip, all_valid;  // (under rules)
+    int ids[part_blocks<kRules> / 32];
+    uint32_t valid[kPartBlocks / 32];  // (without)
 };
 
 template <bool kRules>
 __device__ __forceinline__ void fetch_item(const ChunkParams &p, int n_big, int total, int G,
-                                           int logG, int lane, Fetched &f) {
+                                           int logG, int lane, Fetched<kRules> &f) {
     if constexpr (kRules) {
         // items in list order until one has blocks (the list ends every search)
         for (;;) {
@@ -632,28 +642,30 @@ __device__ __forceinline__ void fetch_item(const ChunkParams &p, int n_big, int 
             const int part = local / per, rest = local - part * per;
             const int tile = sg.tiles - 1 - rest / p.num_kv_heads;
             const Span sp = tile_span(sg, tile, G, p.rules.window);
-            const int blo = part * kPartBlocks;
+            const int blo = part * kRulePartBlocks;
             if (blo >= sp.nblk) continue;
             f.seq = seq;
             f.part = part;
             f.kvh = rest % p.num_kv_heads;
             f.tile = tile;
-            f.nblk = min(kPartBlocks, sp.nblk - blo);
+            f.nblk = min(kRulePartBlocks, sp.nblk - blo);
             f.nsteps = (f.nblk + kStepBlocks - 1) / kStepBlocks;
             f.L = sg.L;
             f.Q = sg.Q;
             f.q0 = sg.q0;
-            f.nparts = (sp.nblk + kPartBlocks - 1) / kPartBlocks;
+            f.nparts = (sp.nblk + kRulePartBlocks - 1) / kRulePartBlocks;
             f.prefix = sg.prefix;
             f.pb = sp.pb;
             f.skip = sp.skip;
             load_ids(p, seq, blo, f.nblk, lane, true, f.ids, sp.pb, sp.skip);
+            bool all = true;
 #pragma unroll
-            for (int w = 0; w < kPartBlocks / 32; ++w)
-                f.valid[w] = __ballot_sync(0xffffffffu, f.ids[w] >= 0);
+            for (int w = 0; w < kRulePartBlocks / 32; ++w)
+                all = all && (f.ids[w] >= 0 || 32 * w + lane >= f.nblk);
+            f.all_valid = __all_sync(0xffffffffu, all);
             return;
         }
-    }
+    } else {
     int item = 0;
     if (lane == 0) item = atomicAdd(p.work, 1);
     item = __shfl_sync(0xffffffffu, item, 0);
@@ -687,6 +699,7 @@ __device__ __forceinline__ void fetch_item(const ChunkParams &p, int n_big, int 
     load_ids(p, seq, blo, f.nblk, lane, true, f.ids);
 #pragma unroll
     for (int w = 0; w < kPartBlocks / 32; ++w) f.valid[w] = __ballot_sync(0xffffffffu, f.ids[w] >= 0);
+    }
 }
 
 // What a kernel's scores follow: nothing more than the causal order, or rules, of
@@ -694,6 +707,14 @@ __device__ __forceinline__ void fetch_item(const ChunkParams &p, int n_big, int 
 // are compiled in or left out (one kernel with all of it took 536 and 740 us where
 // the kernels without a cap, and with the bias, take FIXME and FIXME).
 constexpr int kPlain = 0, kRuled = 1, kCapped = 2, kBiased = 4;
+
+// Step n of an item, as its place in the item's list of steps: under a bias by
+// distance from the newest keys to the oldest, so that the first step sets the rows'
+// references (the other way round a steep slope moves them, and O, at every step).
+template <int kMode>
+__device__ __forceinline__ int place_of(int n, int nsteps) {
+    return (kMode & kBiased) != 0 ? nsteps - 1 - n : n;
+}
 
 constexpr float kNear = -1.f;
 
@@ -958,7 +979,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int total = __ldcg(p.big_cum + n_big);
         int gs = 0;  // steps staged
         bool ok = true;
-        Fetched cur;
+        Fetched<kRules> cur;
         fetch_item<kRules>(p, n_big, total, G, logG, lane, cur);
         for (int it = 0; ok; ++it) {
             const int slot = it & 1;
@@ -984,9 +1005,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         in.prefix = cur.prefix;
                         in.pb = cur.pb;
                         in.skip = cur.skip;
-                    }
+                        in.all_valid = cur.all_valid;
+                    } else {
 #pragma unroll
-                    for (int w = 0; w < kPartBlocks / 32; ++w) in.valid[w] = cur.valid[w];
+                        for (int w = 0; w < kPartBlocks / 32; ++w) in.valid[w] = cur.valid[w];
+                    }
                 }
                 mbar_arrive(br.q_full(slot));
             }
@@ -1005,7 +1028,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the next item is taken when this one's last steps are staged,
             // a ring's depth before its softmax ends: the CTAs that finish
             // first take the next items (its lookups overlap those steps)
-            Fetched nxt;
+            Fetched<kRules> nxt;
             nxt.done = 1;
             const int fetch_at = max(cur.nsteps - kClaimLead, 0);
             for (int n = 0; n < cur.nsteps; ++n, ++gs) {
@@ -1014,13 +1037,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
-                const int nb = min(kStepBlocks, cur.nblk - n * kStepBlocks);
+                const int sn = place_of<kMode>(n, cur.nsteps);
+                const int nb = min(kStepBlocks, cur.nblk - sn * kStepBlocks);
                 if (lane == 0) mbar_arrive_expect_tx(br.k_full(ks), nb * CH * kBS * 128);
                 __syncwarp();
                 // lane l: block l / CH of the step, chunk l % CH (a bad block
                 // reads rows before the cache: zeros)
                 const int b = min(lane / CH, kStepBlocks - 1), c = lane % CH;
-                const int id = id_of(cur.ids, n * kStepBlocks + b);
+                const int id = id_of(cur.ids, sn * kStepBlocks + b);
                 if (lane < nb * CH)
                     tensor_g2s_3d(sb + Gm::kOffK + ks * Gm::kK + c * (kStepKeys * 128) +
                                       b * (kBS * 128),
@@ -1055,18 +1079,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(br.q_empty(slot));
             if (done) break;
-            int ids[kPartBlocks / 32];
-            load_ids(p, seq, part * kPartBlocks, nblk, lane, false, ids, pb, skip);
+            int ids[part_blocks<kRules> / 32];
+            load_ids(p, seq, part * part_blocks<kRules>, nblk, lane, false, ids, pb, skip);
             for (int n = 0; n < nsteps; ++n, ++gs) {
                 const int vs = gs % kVStages;
                 if (gs >= kVStages && !wait_all(br.v_empty(vs), ((gs / kVStages) - 1) & 1)) {
                     ok = false;
                     break;
                 }
-                const int nb = min(kStepBlocks, nblk - n * kStepBlocks);
+                const int sn = place_of<kMode>(n, nsteps);
+                const int nb = min(kStepBlocks, nblk - sn * kStepBlocks);
                 if (lane == 0) mbar_arrive_expect_tx(br.v_full(vs), nb * Gm::kVBlock);
                 __syncwarp();
-                const int id = id_of(ids, n * kStepBlocks + min(lane, kStepBlocks - 1));
+                const int id = id_of(ids, sn * kStepBlocks + min(lane, kStepBlocks - 1));
                 if (lane < nb)
                     tensor_g2s_3d(sb + Gm::kOffV + vs * Gm::kV + lane * Gm::kVBlock, &p.tm_v, 0,
                                   id >= 0 ? id * kBS : -kBS, kvh * CH, br.v_full(vs));
@@ -1123,7 +1148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // one MMA per k step over the step's keys (an MMA of
                     // N 64 or less costs the issuing thread about as much as
                     // one of N 128, so fewer and wider ones are faster)
-                    const int nb = min(kStepBlocks, nblk - n * kStepBlocks);
+                    const int nb = min(kStepBlocks, nblk - place_of<kMode>(n, nsteps) * kStepBlocks);
                     const uint32_t idesc = tc::idesc_f16_f32(kRows, nb * kBS, false, false);
                     const uint32_t k_s = sb + Gm::kOffK + ks * Gm::kK;
 #pragma unroll
@@ -1153,7 +1178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const ItemInfo &in = info[slot];
             const int done = in.done, nsteps = in.nsteps, nblk = in.nblk, L = in.L;
-            const int blo = in.part * kPartBlocks;
+            const int blo = in.part * part_blocks<kRules>;
             int pb = 0, skip = 0, prefix = 0, a0 = 0, a1 = 0;
             if constexpr (kRules) {
                 pb = in.pb;
@@ -1168,7 +1193,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (done) break;
             for (int m = 0; m < nsteps && ok; ++m) {
                 const int g = gs + m, vs = g % kVStages;
-                const int nb = min(kStepBlocks, nblk - m * kStepBlocks);
+                const int sm = place_of<kMode>(m, nsteps);
+                const int nb = min(kStepBlocks, nblk - sm * kStepBlocks);
                 ok = wait_all(br.v_full(vs), (g / kVStages) & 1);
                 if (!ok) break;
                 const uint32_t v_s = sb + Gm::kOffV + vs * Gm::kV;
@@ -1177,9 +1203,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // sequence's end zeroed, and the others' elements that are not
                     // finite (0 * NaN is not 0), which the rows that see them add
                     // at the end
-                    if (!clear.has(blo + m * kStepBlocks, nb)) {
+                    if (!clear.has(blo + sm * kStepBlocks, nb)) {
                     bool dirty = false, touched = false;
-                    const int mine = span_block(pb, skip, blo + m * kStepBlocks + lane) * kBS;
+                    const int mine = span_block(pb, skip, blo + sm * kStepBlocks + lane) * kBS;
                     uint32_t part_seen = __ballot_sync(
                         0xffffffffu,
                         lane < nb && !seen_whole(mine, a0, a1, p.rules.window, prefix));
@@ -1256,16 +1282,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int nparts = in.nparts;
             const int in_pb = in.pb, in_skip = in.skip, in_prefix = in.prefix;
             uint32_t valid[kPartBlocks / 32];
-#pragma unroll
-            for (int w = 0; w < kPartBlocks / 32; ++w) valid[w] = in.valid[w];
             // every block of the item in range (the usual case): the steps
-            // need no look-up in the array above
+            // need no look-up in the array above (under rules: in the table)
             bool all_valid = true;
+            if constexpr (kRules) {
+                all_valid = in.all_valid != 0;
+            } else {
 #pragma unroll
-            for (int w = 0; w < kPartBlocks / 32; ++w) {
-                const int nbw = min(max(nblk - 32 * w, 0), 32);
-                const uint32_t need = nbw == 32 ? 0xffffffffu : ((1u << nbw) - 1u);
-                all_valid = all_valid && (valid[w] & need) == need;
+                for (int w = 0; w < kPartBlocks / 32; ++w) valid[w] = in.valid[w];
+#pragma unroll
+                for (int w = 0; w < kPartBlocks / 32; ++w) {
+                    const int nbw = min(max(nblk - 32 * w, 0), 32);
+                    const uint32_t need = nbw == 32 ? 0xffffffffu : ((1u << nbw) - 1u);
+                    all_valid = all_valid && (valid[w] & need) == need;
+                }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(br.q_empty(slot));
@@ -1308,12 +1338,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(br.s_free());
-                const int nb = min(kStepBlocks, nblk - n * kStepBlocks);
+                const int sn = place_of<kMode>(n, nsteps);
+                const int nb = min(kStepBlocks, nblk - sn * kStepBlocks);
                 const int nbg = min(max(nb - 4 * h, 0), 4);  // this thread's blocks
                 const int kbase = part * kPartTokens + n * kStepKeys + kGroupKeys * h;
                 const int b0 = n * kStepBlocks + 4 * h;
                 uint32_t vmask = 0xFu;
-                if (!all_valid) vmask = (valid[b0 >> 5] >> (b0 & 31)) & 0xFu;
+                if constexpr (kRules) {
+                    if (!all_valid) {
+                        vmask = 0u;
+                        for (int b = 0; b < nbg; ++b) {
+                            const int64_t id = __ldg(
+                                p.block_tables + static_cast<int64_t>(seq) * p.max_blocks_per_seq +
+                                span_block(pb, skip, part * kRulePartBlocks + sn * kStepBlocks + 4 * h + b));
+                            if (id >= 0 && id < p.num_blocks) vmask |= 1u << b;
+                        }
+                    }
+                } else if (!all_valid) {
+                    vmask = (valid[b0 >> 5] >> (b0 & 31)) & 0xFu;
+                }
                 // the maximum of the raw scores first (independent of the
                 // masks, so the two overlap); it stands, scaled once, when
                 // every key of the warp is visible and the scale is not
@@ -1321,7 +1364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // maximum taken again
                 float mx, a;
                 if constexpr (kRules) {
-                    const int v = part * kPartBlocks + n * kStepBlocks;
+                    const int v = part * kRulePartBlocks + sn * kStepBlocks;
                     const bool usual =
                         all_valid && nb == kStepBlocks &&
                         ((kMode & kBiased) != 0 ? clear.has_past(v, kStepBlocks)
@@ -1471,7 +1514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int a0 = L - Q + tile * (kRows >> logG);
                     const int a1 = min(a0 + (kRows >> logG), L) - 1;
                     for (int b = 0; b < nblk; ++b) {
-                        const int blk = span_block(pb, skip, part * kPartBlocks + b);
+                        const int blk = span_block(pb, skip, part * kRulePartBlocks + b);
                         const int kp = blk * kBS;
                         if (seen_whole(kp, a0, a1, p.rules.window, prefix)) continue;
                         const int64_t id = __ldg(p.block_tables +
