@@ -741,8 +741,8 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
 // them in units of 1/a (returns a > 0), or raw ones far below the cap (returns kNear;
 // the weights' loop caps them).  The keys are four blocks of the tile's list from
 // place v0 on, nbg of them there, bad ones not in vmask.
-// usual (the same for the whole warp): every row of the tile sees every key of the
-// step, none of them behind its position under a bias.
+// usual (the same for the whole warp): its rows see every key of the step, none of them
+// behind their positions under a bias.
 template <int kMode>
 __device__ __forceinline__ float rule_scores(const ChunkParams &p, uint32_t (&sx)[kGroupKeys],
                                              bool usual, int nbg, uint32_t vmask, int v0, int pb,
@@ -869,48 +869,50 @@ __device__ __forceinline__ float rule_scores(const ChunkParams &p, uint32_t (&sx
             if constexpr (kCap) t = cap * (exp_form ? dec::tanh_exp(t * c2) : t);
             else t *= sl2;
             if constexpr (kBias) t = fmaf(-slope, fabsf(d0 - static_cast<float>(i)), t);
-            t = (seen >> i) & 1u ? t : kNegInf;
-            x = __float_as_uint(t);
-            mr[i & 7] = fmaxf(mr[i & 7], t);
+            // (all ones where the bit is set)
+            const uint32_t m = static_cast<uint32_t>(static_cast<int32_t>(seen << (31 - i)) >> 31);
+            x = (__float_as_uint(t) & m) | (0xFF800000u & ~m);
         }
+#pragma unroll
+        for (int i = 0; i < kBS / 2; ++i)
+            mr[i] = fmax3(mr[i], __uint_as_float(sx[b * kBS + 2 * i]),
+                          __uint_as_float(sx[b * kBS + 2 * i + 1]));
     }
     mx = fmax3(fmax3(mr[0], mr[1], mr[2]), fmax3(mr[3], mr[4], mr[5]), fmaxf(mr[6], mr[7]));
     return 1.f;
 }
 
 // Value block `vb` ([chunk][token][128 B]): rows from `end` on zeroed, and of the
-// others the elements that are not finite; true if there were any.
+// others the elements that are not finite.  Bit 0: there were any; bit 1: this lane
+// wrote something.  (Every load before the first check: one warp does this, between
+// the copies' arrival and the MMAs.)
 template <int CH>
-__device__ __noinline__ bool clean_block(uint8_t *vb, int end, int lane, bool *touched) {
-    bool bad = false;
-    for (int i = lane; i < CH * kBS * 8; i += 32) {
-        uint4 *at = reinterpret_cast<uint4 *>(vb + i * 16);
-        const int token = (i >> 3) & (kBS - 1);
-        if (token >= end) {
-            *at = make_uint4(0u, 0u, 0u, 0u);
-            *touched = true;
-            continue;
-        }
-        const uint4 x = *at;
-        uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        bool mine = false;
+__device__ __forceinline__ uint32_t clean_block(uint8_t *vb, int end, int lane) {
+    constexpr int kUnits = CH * kBS * 8 / 32;
+    uint4 x[kUnits];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if ((w[k] & 0x7C00u) == 0x7C00u) {
-                w[k] &= 0xFFFF0000u;
-                mine = true;
+    for (int j = 0; j < kUnits; ++j) x[j] = *reinterpret_cast<uint4 *>(vb + (32 * j + lane) * 16);
+    uint32_t out = 0;
+#pragma unroll
+    for (int j = 0; j < kUnits; ++j) {
+        const int token = ((32 * j + lane) >> 3) & (kBS - 1);
+        uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+        // an exponent of all ones carries into its half's sign bit
+        uint32_t bad = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) bad |= (w[k] & 0x7C007C00u) + 0x04000400u;
+        if (token >= end || (bad & 0x80008000u) != 0) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (token >= end || (w[k] & 0x7C00u) == 0x7C00u) w[k] &= 0xFFFF0000u;
+                if (token >= end || (w[k] & 0x7C000000u) == 0x7C000000u) w[k] &= 0xFFFFu;
             }
-            if ((w[k] & 0x7C000000u) == 0x7C000000u) {
-                w[k] &= 0xFFFFu;
-                mine = true;
-            }
-        }
-        if (mine) {
-            *at = make_uint4(w[0], w[1], w[2], w[3]);
-            *touched = bad = true;
+            *reinterpret_cast<uint4 *>(vb + (32 * j + lane) * 16) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+            out |= token >= end ? 2u : 3u;
         }
     }
-    return bad;
+    return out;
 }
 
 template <int D, int kMode>
@@ -1204,7 +1206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // finite (0 * NaN is not 0), which the rows that see them add
                     // at the end
                     if (!clear.has(blo + sm * kStepBlocks, nb)) {
-                    bool dirty = false, touched = false;
+                    uint32_t found = 0;
                     const int mine = span_block(pb, skip, blo + sm * kStepBlocks + lane) * kBS;
                     uint32_t part_seen = __ballot_sync(
                         0xffffffffu,
@@ -1213,11 +1215,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int b = __ffs(part_seen) - 1;
                         const int kp = __shfl_sync(0xffffffffu, mine, b);
                         uint8_t *vb = smem + Gm::kOffV + vs * Gm::kV + b * Gm::kVBlock;
-                        const bool bad = clean_block<CH>(vb, L - kp, lane, &touched);
-                        dirty = dirty || bad;
+                        found |= clean_block<CH>(vb, L - kp, lane);
                     }
-                    if (touched) fence_proxy_async_smem();
-                    if (__any_sync(0xffffffffu, dirty) && lane == 0) misc[1 + (it & 1)] = it + 1;
+                    if (found != 0) fence_proxy_async_smem();
+                    if (__any_sync(0xffffffffu, found & 1u) && lane == 0) misc[1 + (it & 1)] = it + 1;
                     __syncwarp();
                     }
                 } else if (m == nsteps - 1) {
@@ -1365,10 +1366,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float mx, a;
                 if constexpr (kRules) {
                     const int v = part * kRulePartBlocks + sn * kStepBlocks;
-                    const bool usual =
-                        all_valid && nb == kStepBlocks &&
-                        ((kMode & kBiased) != 0 ? clear.has_past(v, kStepBlocks)
-                                                : clear.has(v, kStepBlocks));
+                    bool usual = all_valid && nb == kStepBlocks;
+                    if (usual && !((kMode & kBiased) != 0 ? clear.has_past(v, kStepBlocks)
+                                                          : clear.has(v, kStepBlocks))) {
+                        // (not for the tile, but maybe for this warp's 16 rows)
+                        const int v0 = v + 4 * h, kp = span_block(pb, skip, v0) * kBS;
+                        const bool past = kp + kGroupKeys - 1 <= pos;
+                        usual = __all_sync(
+                            0xffffffffu,
+                            (v0 >= pb || v0 + 4 <= pb) &&
+                                ((past && pos - kp < p.rules.window) ||
+                                 (kp + kGroupKeys <= prefix && (past || (kMode & kBiased) == 0))));
+                    }
                     a = rule_scores<kMode>(p, sx, usual, nbg, vmask, v + 4 * h, pb, skip, prefix,
                                            pos, slope, sl2, mx);
                 } else {
