@@ -28,8 +28,10 @@ struct Sizes {
     int64_t bal_bytes;
 };
 
+// scored: under score rules, which need no more of anything than without (so the
+// workspace sized without them does), but other shared memory on the balanced schedule.
 Sizes sizes(int64_t S, int64_t H, int64_t Hk, int64_t D, int64_t Tq, int64_t max_q,
-            int64_t max_len) {
+            int64_t max_len, bool scored) {
     Sizes z{};
     const int64_t G = H / Hk;
     z.tiles = std::max<int64_t>(1, (max_q * G + kRows - 1) / kRows);
@@ -43,7 +45,7 @@ Sizes sizes(int64_t S, int64_t H, int64_t Hk, int64_t D, int64_t Tq, int64_t max
     // cheaper policy, so it is used whenever the tile kernel runs anyway)
     z.col_tiles = (max_q * G <= 8 || max_q * G > 16) ? 1 : 2;
     z.bal = dec::balanced_shape(static_cast<int>(S), static_cast<int>(Hk), static_cast<int>(G),
-                                static_cast<int>(D), sm_count(), false, 8 * z.col_tiles);
+                                static_cast<int>(D), sm_count(), false, 8 * z.col_tiles, scored);
     if (!z.bal.ok) z.col_tiles = 0;
     z.bal_bytes = z.bal.ok ? dec::align256(z.bal.workspace) : 0;
     return z;
@@ -62,7 +64,7 @@ extern "C" size_t pkv_chunk_workspace_bytes(int32_t num_seqs, int32_t num_heads,
         max_seq_len <= 0)
         return 0;
     const auto z = pkv::chunk::sizes(num_seqs, num_heads, num_kv_heads, head_dim,
-                                     num_query_tokens, max_query_len, max_seq_len);
+                                     num_query_tokens, max_query_len, max_seq_len, false);
     return static_cast<size_t>(z.bal_bytes + z.list_bytes + z.counters_bytes + z.ml_bytes +
                                z.o_bytes);
 }
@@ -103,7 +105,7 @@ int chunk_attention(void *out, const void *q, const void *k_cache, const void *v
         if (st != PKV_OK) return st;
     }
     const auto z = sizes(num_seqs, num_heads, num_kv_heads, head_dim, num_query_tokens,
-                         max_query_len, max_seq_len);
+                         max_query_len, max_seq_len, scored);
     // work items (and their prefix sums) are 32-bit: at most
     // (sum of tiles <= Tq*G/64 + S) * partitions * Hk of them
     const int64_t tiles_sum = (static_cast<int64_t>(num_query_tokens) * G + kRows - 1) / kRows +

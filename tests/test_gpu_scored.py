@@ -384,6 +384,26 @@ def test_calls_in_flight_together_and_captured():
     assert pkv.pkv_get_device_error()[0] == 0
 
 
+@pytest.mark.parametrize("H,Hk", [(1, 1), (8, 2)])
+def test_many_sequences(H, Hk):
+    """Lengths, prefixes and left-out blocks of 2500 sequences in shared memory."""
+    S = 2500
+    lens = [1 + (7 * i) % 60 for i in range(S)]
+    rules = dict(window=9, prefix_lens=np.arange(S) % 5)
+    c = Case(93, lens, [1] * S, H, Hk, 64)
+    want = want_of(c, rules)
+    for chunk in (False, True):
+        check(c.run(chunk, **rules), want, str(chunk))
+    # chunks of up to 20 tokens: both kernels of the call
+    news = [1 + (3 * i) % min(20, n) for i, n in enumerate(lens)]
+    c = Case(94, lens, news, H, Hk, 64)
+    rows = set(range(0, len(c.q), 97))
+    got, (ref, tol) = c.run(True, **rules), want_of(c, rules, rows)
+    r = sorted(rows)
+    check(got[r], (ref[r], tol[r]))
+    assert pkv.pkv_get_device_error()[0] == 0
+
+
 def test_outputs_stay_inside_their_buffer():
     c = Case(91, [300, 20], [45, 2], 8, 4, 64)
     c.upload(softcap=5.0, slopes=slopes_of(8))
