@@ -374,9 +374,8 @@ typedef struct pkv_score_rules {
  * maxima, sums and outputs are fp32; softmax weights are rounded to fp16 (each by
  * 2^-11 of itself or, where that is more, by 2^-39 of the row's largest) and
  * the sum they are divided by holds them rounded.  A block whose id is outside
- * [0, num_blocks) is skipped and recorded.  NaN or infinities in positions past
- * the sequence's length are not seen; in positions inside a block that the token
- * reads but does not see, they are not either.
+ * [0, num_blocks) is skipped and recorded.  What a position that the token does not
+ * see holds, infinities and NaN included, does not reach its output.
  *  rules      HOST pointer, read during the call only; not NULL
  *  workspace  pkv_decode_workspace_bytes(...) bytes, as for
  *             pkv_decode_attention: zero-filled before first use, left so
@@ -397,7 +396,8 @@ int pkv_decode_attention_scored(void *out, const void *q, const void *k_cache,
                                 pkv_stream_t stream);
 
 /* The same over FP8 caches (layout of pkv_cache_write_fp8; caches and scales
- * 16-byte aligned). */
+ * 16-byte aligned); a weight is rounded to fp16 times its value's scale, and summed
+ * as it was. */
 int pkv_decode_attention_scored_fp8(void *out, const void *q, const void *k_cache,
                                     const void *v_cache, const float *k_scale,
                                     const float *v_scale, const int32_t *block_tables,
@@ -409,7 +409,11 @@ int pkv_decode_attention_scored_fp8(void *out, const void *q, const void *k_cach
                                     pkv_stream_t stream);
 
 /* pkv_chunk_attention under score rules: new token j of a sequence is at
- * position L - Q + j.  Workspace (pkv_chunk_workspace_bytes), other arguments,
+ * position L - Q + j.  What a position holds does not reach the rows that do not see
+ * it.  Chunks of more than 16 rows (new tokens times group size; 8 where max_query_len
+ * allows for such chunks) have their weights rounded by 2^-32 of the row's largest
+ * instead of 2^-39, against a sum that holds them as they were; the last bits of their
+ * results may depend on the other rows of the call.  Workspace (pkv_chunk_workspace_bytes), other arguments,
  * shapes, ordering and errors as pkv_chunk_attention. */
 int pkv_chunk_attention_scored(void *out, const void *q, const void *k_cache,
                                const void *v_cache, const int32_t *block_tables,

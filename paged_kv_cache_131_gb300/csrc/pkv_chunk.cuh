@@ -51,6 +51,20 @@
 // every partition leaves fp32 partial states (m, l, O) and, per softmax warp,
 // the last CTA of the tile to take a ticket merges them with a log-sum-exp
 // rescale.  No CTA waits for another.
+//
+// Under score rules (pkv_score_rules) the same, but
+//  * a tile's keys are a list of blocks (Span): the prefix's, then those from the
+//    first row's window on; partitions of 8192 tokens divide that list, and an item
+//    whose partition the list does not reach is passed over when it is taken;
+//  * the softmax applies the rules to the scores (rule_scores); most steps are seen
+//    whole by every row (Clear) and pass the masks over;
+//  * a step that is not has its value blocks' elements that are not finite zeroed
+//    before the MMAs and added at the end by the rows that see them.
+// What bounds it (4 x 2048 new tokens of up to 8192, H 32, Hk 8, D 128, clock reads in
+// a copy, cycles a step of 2700 with a cap): the softmax warps, two a scheduler: the
+// scores' extremes 700, weights 1150 (690 without a cap: its polynomial is four packed
+// multiply-adds a pair), scores' load 190, votes and waits 300, an item's output 430;
+// issue slots 39% busy, tensor pipe 28%.
 #pragma once
 
 #include <cuda.h>
