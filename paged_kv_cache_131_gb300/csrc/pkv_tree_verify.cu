@@ -43,7 +43,6 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBatch = 4;  // vectors of either row that a thread has in flight
 constexpr int kMaxCluster = 8;
 constexpr int kMaxNodes = PKV_MAX_TREE_NODES;
-constexpr int kNodesPerLane = kMaxNodes / 32;
 constexpr unsigned kAll = 0xffffffffu;
 
 struct VerifyParams {
@@ -197,7 +196,8 @@ __global__ void __launch_bounds__(kThreads, 3)
     // per node: its token's probability under its parent's target and drafts
     __shared__ float node_p[kMaxNodes], node_q[kMaxNodes], node_u[kMaxNodes];
     __shared__ int node_token[kMaxNodes];
-    __shared__ int gone[kMaxNodes];
+    __shared__ int node_up[kMaxNodes];      // its parent; -1: never a child
+    __shared__ int gone[kWarps][kMaxNodes];  // fixed guesses rejected at this node, by warp
     __shared__ Pair warp_part[2][kWarps];       // this CTA's warps, by parity of the pass
     __shared__ Pair cta_part[2][kMaxCluster];   // every CTA's sum, written by it
     __shared__ Pair draw_part[kWarps];
@@ -235,10 +235,12 @@ __global__ void __launch_bounds__(kThreads, 3)
         const int64_t row = row0 + k;
         const int parent = __ldg(p.parents + row), token = __ldg(p.tokens + row);
         float a = 0.f, b = 0.f;
+        int up = -1;
         if (k > 0 && parent >= 0) {
             if (parent >= k || token < 0 || token >= V) {
                 if (cta == 0) record_error(p.err, PKV_DEVERR_TREE, row);
             } else {
+                up = parent;
                 a = __ldg(p.target + (row0 + parent) * p.target_stride + token);
                 if (drafted) b = __ldg(p.draft + (row0 + parent) * p.draft_stride + token);
             }
@@ -247,17 +249,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         node_q[k] = b;
         node_u[k] = unit(__ldg(p.accept_u + row));
         node_token[k] = token;
-    }
-    // every warp: the parents, node 32 j + lane in up[j] (-1: never a child)
-    int up[kNodesPerLane];
-#pragma unroll
-    for (int j = 0; j < kNodesPerLane; ++j) {
-        const int k = 32 * j + lane;
-        up[j] = -1;
-        if (k > 0 && k < Q) {
-            const int parent = __ldg(p.parents + row0 + k), token = __ldg(p.tokens + row0 + k);
-            if (parent >= 0 && parent < k && token >= 0 && token < V) up[j] = parent;
-        }
+        node_up[k] = up;
     }
     const float draw_u = unit(__ldg(p.sample_u + seq));
     __syncthreads();
@@ -273,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         r.p = p.target + (row0 + at) * p.target_stride;
         r.q = nullptr;
         r.c_hi = r.c_lo = 0.f;
-        r.gone = gone;
+        r.gone = gone[warp];
         r.num_gone = 0;
         const uintptr_t pa = reinterpret_cast<uintptr_t>(r.p) & 15;
         const float *q = drafted ? p.draft + (row0 + at) * p.draft_stride : r.p;
@@ -344,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 3)
 
     // ---- the walk (every warp of the cluster alike)
     int at = 0, depth = 1;
-    int mine_gone[kNodesPerLane], seen = 0;  // fixed guesses rejected at this node
+    int seen = 0;  // fixed guesses rejected at this node (r.num_gone once they are all)
     bool summed = false;  // the last pass summed r as it stands
     Pair total{0.f, 0.f};
     if (cta == 0 && threadIdx.x == 0) path[0] = 0;
@@ -353,13 +345,12 @@ __global__ void __launch_bounds__(kThreads, 3)
         summed = false;
         int step = -1;
         seen = 0;
-#pragma unroll
-        for (int g = 0; g < kNodesPerLane; ++g) mine_gone[g] = -1;
         if (depth < p.max_depth) {
             Pair W{1.f, 0.f}, C{0.f, 0.f};
             bool empty = false;
-            for (int j = 0; j < kNodesPerLane && step < 0 && !empty; ++j) {
-                unsigned kids = __ballot_sync(kAll, up[j] == at);
+            for (int j = (at + 1) >> 5; j < (Q + 31) >> 5 && step < 0 && !empty; ++j) {
+                const int node = 32 * j + lane;
+                unsigned kids = __ballot_sync(kAll, node < Q && node_up[node] == at);
                 while (kids != 0 && step < 0 && !empty) {
                     const int k = 32 * j + __ffs(kids) - 1;
                     kids &= kids - 1;
@@ -387,12 +378,10 @@ __global__ void __launch_bounds__(kThreads, 3)
                             empty = true;
                         }
                     } else {
-                        // (a guess that was rejected before has nothing left; lane l of
-                        // every warp holds rejected tokens l, 32 + l, ..)
+                        // (a guess that was rejected before has nothing left)
                         const int token = node_token[k];
                         bool again = false;
-#pragma unroll
-                        for (int g = 0; g < kNodesPerLane; ++g) again = again || mine_gone[g] == token;
+                        for (int g = lane; g < seen; g += 32) again = again || gone[warp][g] == token;
                         again = __any_sync(kAll, again);
                         const Pair have{again ? 0.f : pt, 0.f};
                         if (W * u < have) {
@@ -405,9 +394,8 @@ __global__ void __launch_bounds__(kThreads, 3)
                         } else {
                             W = less;
                             if (!again) {
-#pragma unroll
-                                for (int g = 0; g < kNodesPerLane; ++g)
-                                    if (seen == 32 * g + lane) mine_gone[g] = token;
+                                if (lane == 0) gone[warp][seen] = token;
+                                __syncwarp();
                                 ++seen;
                             }
                         }
@@ -422,15 +410,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     }
 
     // ---- the next token
-    if (seen > 0) {  // (every thread alike)
-        if (warp == 0) {
-#pragma unroll
-            for (int g = 0; g < kNodesPerLane; ++g)
-                if (mine_gone[g] >= 0) gone[32 * g + lane] = mine_gone[g];
-        }
-        __syncthreads();
-        r.num_gone = seen;
-    }
+    r.num_gone = seen;
     if (!summed) total = sum_rest();
     const int half = (pass - 1) & 1;
     if (cta == 0) {
