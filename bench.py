@@ -95,11 +95,11 @@ L2_NOTE = ("flushed between timed steps (write a 2x L2 buffer, then read another
 
 CSRC = os.path.join(ROOT, "paged_kv_cache_131_gb300", "csrc")
 DECODE_SOURCES = [os.path.join(CSRC, f)
-                  for f in ("pkv_decode_balanced.cu", "pkv_decode_common.cuh", "pkv_device.cuh",
-                            "pkv_tensor_map.cu")]
+                  for f in ("pkv_decode_balanced.cu", "pkv_decode_balanced.cuh", "pkv_decode_common.cuh",
+                            "pkv_device.cuh", "pkv_tensor_map.cu")]
 WRITE_SOURCES = [os.path.join(CSRC, "pkv_write.cu")]
 CHUNK_SOURCES = [os.path.join(CSRC, f)
-                 for f in ("pkv_chunk.cu", "pkv_tcgen05.cuh", "pkv_device.cuh",
+                 for f in ("pkv_chunk.cu", "pkv_chunk.cuh", "pkv_tcgen05.cuh", "pkv_device.cuh",
                            "pkv_decode_common.cuh", "pkv_decode_host.h", "pkv_tensor_map.cu")]
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "decode_kernel_dram_traffic.txt")
 WRITE_TRAFFIC_FILE = os.path.join(ROOT, "profiles", "cache_write_kernel_dram_traffic.txt")

@@ -634,6 +634,8 @@ def pkv_tree_accept(caches, num_layers: int, path, ctx_lens, block_tables, block
 
 def _rules(softcap, window, slopes, prefix_lens, num_heads, num_seqs, dev):
     import torch
+    if not 0 <= window < 2 ** 31:  # (ctypes would wrap it)
+        raise ValueError(f"window must be in [0, 2^31), got {window}")
     return pkv_score_rules(
         softcap, window,
         None if slopes is None else _arg(slopes, "slopes", torch.float32, (num_heads,), dev),

@@ -572,7 +572,8 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const __grid_constant_
     }
 }
 
-// Block ids of an item's partition: lane l holds blocks l, 32 + l, .. of it; -1 past the item or out of range (recorded when `report`).
+// Block ids of an item's partition: lane l holds blocks l, 32 + l, .. of it; -1 past
+// the item or out of range (recorded when `report`).
 // (pb, skip: under rules the list of blocks is a tile's Span.)
 template <int W>
 __device__ __forceinline__ void load_ids(const ChunkParams &p, int seq, int blo, int nblk,
@@ -1221,20 +1222,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // finite (0 * NaN is not 0), which the rows that see them add
                     // at the end
                     if (!clear.has(blo + sm * kStepBlocks, nb)) {
-                    uint32_t found = 0;
-                    const int mine = span_block(pb, skip, blo + sm * kStepBlocks + lane) * kBS;
-                    uint32_t part_seen = __ballot_sync(
-                        0xffffffffu,
-                        lane < nb && !seen_whole(mine, a0, a1, p.rules.window, prefix));
-                    for (; part_seen != 0; part_seen &= part_seen - 1) {
-                        const int b = __ffs(part_seen) - 1;
-                        const int kp = __shfl_sync(0xffffffffu, mine, b);
-                        uint8_t *vb = smem + Gm::kOffV + vs * Gm::kV + b * Gm::kVBlock;
-                        found |= clean_block<CH>(vb, L - kp, lane);
-                    }
-                    if (found != 0) fence_proxy_async_smem();
-                    if (__any_sync(0xffffffffu, found & 1u) && lane == 0) misc[1 + (it & 1)] = it + 1;
-                    __syncwarp();
+                        uint32_t found = 0;
+                        const int mine = span_block(pb, skip, blo + sm * kStepBlocks + lane) * kBS;
+                        uint32_t part_seen = __ballot_sync(
+                            0xffffffffu,
+                            lane < nb && !seen_whole(mine, a0, a1, p.rules.window, prefix));
+                        for (; part_seen != 0; part_seen &= part_seen - 1) {
+                            const int b = __ffs(part_seen) - 1;
+                            const int kp = __shfl_sync(0xffffffffu, mine, b);
+                            uint8_t *vb = smem + Gm::kOffV + vs * Gm::kV + b * Gm::kVBlock;
+                            found |= clean_block<CH>(vb, L - kp, lane);
+                        }
+                        if (found != 0) fence_proxy_async_smem();
+                        if (__any_sync(0xffffffffu, found & 1u) && lane == 0) misc[1 + (it & 1)] = it + 1;
+                        __syncwarp();
                     }
                 } else if (m == nsteps - 1) {
                     // value rows at and past the sequence end hold anything
@@ -1396,34 +1397,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                     a = rule_scores<kMode>(p, sx, usual, nbg, vmask, v + 4 * h, pb, skip, prefix,
                                            pos, slope, sl2, mx);
                 } else {
-                const bool fast = __all_sync(0xffffffffu, nbg == 4 && vmask == 0xFu &&
-                                                              kbase + kGroupKeys - 1 <= lim &&
-                                                              sl2 >= 0.f);
-                float mr[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) mr[i] = kNegInf;
-#pragma unroll
-                for (int e = 0; e < kGroupKeys / 2; ++e)
-                    mr[e & 7] = fmax3(mr[e & 7], __uint_as_float(sx[2 * e]),
-                                      __uint_as_float(sx[2 * e + 1]));
-                mx = fmax3(fmax3(mr[0], mr[1], mr[2]), fmax3(mr[3], mr[4], mr[5]),
-                                 fmaxf(mr[6], mr[7]));
-                if (!fast) {
+                    const bool fast = __all_sync(0xffffffffu, nbg == 4 && vmask == 0xFu &&
+                                                                  kbase + kGroupKeys - 1 <= lim &&
+                                                                  sl2 >= 0.f);
+                    float mr[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) mr[i] = kNegInf;
 #pragma unroll
-                    for (int e = 0; e < kGroupKeys; ++e) {
-                        const bool vis = e < nbg * kBS && ((vmask >> (e >> 4)) & 1u) && kbase + e <= lim;
-                        const float t = vis ? __uint_as_float(sx[e]) * sl2 : kNegInf;
-                        sx[e] = __float_as_uint(t);
-                        mr[e & 7] = fmaxf(mr[e & 7], t);
-                    }
+                    for (int e = 0; e < kGroupKeys / 2; ++e)
+                        mr[e & 7] = fmax3(mr[e & 7], __uint_as_float(sx[2 * e]),
+                                          __uint_as_float(sx[2 * e + 1]));
                     mx = fmax3(fmax3(mr[0], mr[1], mr[2]), fmax3(mr[3], mr[4], mr[5]),
-                               fmaxf(mr[6], mr[7]));
-                } else {
-                    mx *= sl2;
-                }
-                a = fast ? sl2 : 1.f;
+                                     fmaxf(mr[6], mr[7]));
+                    if (!fast) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) mr[i] = kNegInf;
+#pragma unroll
+                        for (int e = 0; e < kGroupKeys; ++e) {
+                            const bool vis = e < nbg * kBS && ((vmask >> (e >> 4)) & 1u) && kbase + e <= lim;
+                            const float t = vis ? __uint_as_float(sx[e]) * sl2 : kNegInf;
+                            sx[e] = __float_as_uint(t);
+                            mr[e & 7] = fmaxf(mr[e & 7], t);
+                        }
+                        mx = fmax3(fmax3(mr[0], mr[1], mr[2]), fmax3(mr[3], mr[4], mr[5]),
+                                   fmaxf(mr[6], mr[7]));
+                    } else {
+                        mx *= sl2;
+                    }
+                    a = fast ? sl2 : 1.f;
                 }
                 // the row's other half: the thread 16 lanes away
                 const float mo = __shfl_xor_sync(0xffffffffu, mx, 16);

@@ -357,8 +357,9 @@ __device__ __forceinline__ void balanced_body(const BalancedParams &p, uint8_t *
     // ---- empty sequences get zeros (no block of theirs is in any range)
     const int64_t Tb = cum[S];                 // blocks of one head group
     const int64_t T = Tb * p.groups;           // the whole (group, sequence, block) list
-    // (under rules a CTA takes kMinBlocks blocks or more: a sequence cut finer is
-    // sooner read, but later merged)
+    // Under rules a CTA takes kMinBlocks blocks or more: a sequence cut finer is sooner
+    // read, but later merged, two of its pieces at a time (one sequence of 1041 tokens:
+    // 23.3 us with at least one block, 17.3 with two, 14.2 with four, 14.8 with eight).
     const int64_t N = min(static_cast<int64_t>(grid),
                           kScored ? (T + kMinBlocks - 1) / kMinBlocks : T);
     bool zeros_due = false;

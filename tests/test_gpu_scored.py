@@ -427,6 +427,10 @@ def test_refused_tensors():
         for chunk in (False, True):
             with pytest.raises(ValueError):
                 c.call(chunk)
+    for rules in (dict(window=-1), dict(window=2 ** 31), dict(window=2 ** 32 + 5)):
+        c.rules = rules
+        with pytest.raises(ValueError):
+            c.call(False)
     c.rules = dict(softcap=-1.0)
     with pytest.raises(pkv.PkvError):
         c.call(False)
