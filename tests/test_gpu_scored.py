@@ -271,6 +271,25 @@ def test_caps_of_every_size(cap):
         check(c.run(chunk, softcap=cap), c.want(softcap=cap), f"{cap} {chunk}")
 
 
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 3.0])
+def test_scales_of_either_sign(scale):
+    for news in ([1, 1], [3, 2], [40, 150]):
+        c = Case([95, len(news)], [200, 160], news, 8, 2, 64, spread=1.0)
+        c.scale = scale
+        for rules in (dict(softcap=3.0), dict(softcap=800.0, prefix_lens=[90, 0]), dict(window=30),
+                      dict(softcap=2.0, slopes=slopes_of(8), window=90)):
+            check(c.run(news != [1, 1], **rules), want_of(c, rules), f"{news} {rules}")
+
+
+def test_slopes_of_either_sign():
+    slopes = (slopes_of(8) * np.where(np.arange(8) % 3 == 1, -0.05, 1.0)).astype(np.float32)
+    slopes[4] = 0
+    for news in ([1, 1], [3, 2], [40, 150]):
+        c = Case([96, len(news)], [300, 160], news, 8, 2, 128)
+        for rules in (dict(slopes=slopes), dict(slopes=slopes, softcap=6.0, prefix_lens=[200, 160])):
+            check(c.run(news != [1, 1], **rules), want_of(c, rules), f"{news} {rules}")
+
+
 def test_masked_places_may_hold_anything():
     # decode: positions before the window and behind the prefix, in the same blocks
     for fp8 in (False, True):
