@@ -294,11 +294,17 @@ __device__ __forceinline__ void balanced_body(const BalancedParams &p, uint8_t *
         }
         if constexpr (Policy::kColumns) {
             // -1: not this kernel's (no new token, or more columns than it holds)
-            const int nq = __ldg(p.query_start + s + 1) - __ldg(p.query_start + s);
-            if (nq > L || nq < 0) {
+            const int q0 = __ldg(p.query_start + s), q1 = __ldg(p.query_start + s + 1);
+            const int nq = q1 - q0;
+            if (q0 < 0 || q1 < q0 || q1 > p.num_query_tokens || nq > L) {
                 if (blockIdx.x == 0) record_error(p.err, PKV_DEVERR_SEQ_LEN, s);
                 L = -1;
-            } else if (nq == 0 || nq * G > p.max_cols) {
+            } else if (nq > p.max_cols / G) {
+                // (no other kernel of the call takes it: past max_query_len)
+                if (p.active_ctas == nullptr && blockIdx.x == 0)
+                    record_error(p.err, PKV_DEVERR_SEQ_LEN, s);
+                L = -1;
+            } else if (nq == 0) {
                 L = -1;
             }
         }

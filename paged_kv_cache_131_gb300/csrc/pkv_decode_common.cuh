@@ -850,16 +850,24 @@ struct MmaFp8Policy {
 #pragma unroll
                 for (int r = 0; r < kLaneTokens; ++r) lv[b][r] = fmaxf(__log2f(vs[b][r]), -64.f);
         }
+        float flat[NB * 4];  // (the scores of both blocks take one vote)
+        if constexpr (kRules) {
+#pragma unroll
+            for (int i = 0; i < NB * 4; ++i) flat[i] = x[i >> 2][i & 3] * ks[i >> 2][(i >> 1) & 1];
+            rule_scores(
+                flat, scale_log2, br[0],
+                [&](int i) {
+                    const BlockRules &w = br[i >> 2];
+                    return w.qpos - w.kp - token_of(lane, (i >> 1) & 1);
+                },
+                [&](int i) { return rc.slope[i & 1]; });
+        }
         float mx[2] = {kNegInf, kNegInf};
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             if constexpr (kRules) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[b][j] *= ks[b][j >> 1];
-                rule_scores(
-                    x[b], scale_log2, br[b],
-                    [&](int j) { return br[b].qpos - br[b].kp - token_of(lane, j >> 1); },
-                    [&](int j) { return rc.slope[j & 1]; });
+                for (int j = 0; j < 4; ++j) x[b][j] = flat[4 * b + j];
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {

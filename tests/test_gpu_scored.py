@@ -375,6 +375,35 @@ def test_bad_lengths():
                                              np.delete(tol, range(20, 50), 0)))
 
 
+@pytest.mark.parametrize("news", [[2, 1, 2], [30, 2, 17]])
+def test_bad_query_starts(news):
+    """Starts outside the rows, falling, or past the bound that the call was sized for:
+    skipped and recorded, the others as they are."""
+    lens = [90, 60, 77]
+    rules = dict(softcap=4.0, window=33)
+    c = Case([97, news[0]], lens, news, 8, 2, 64)
+    ref, tol = want_of(c, rules)
+    good = c.start.copy()
+    for at, value, bad in ((0, -3, {0}), (3, good[3] + 1, {2}), (2, good[1] - 1, {1, 2}),
+                           (1, 10 ** 6, {0, 1}), (1, -2 ** 31, {0, 1})):
+        c.start = good.copy()
+        c.start[at] = value
+        got = c.run(True, **rules)
+        assert pkv.pkv_get_device_error()[0] == 3
+        for i in {0, 1, 2} - bad:
+            rows = slice(good[i], good[i + 1])
+            check(got[rows], (ref[rows], tol[rows]), f"{at} {value} sequence {i}")
+    # more new tokens than max_query_len says (and than the call's kernels hold)
+    c.start = good.copy()
+    c.upload(**rules)
+    if news[0] == 30:
+        c.maxq = 2
+        got = c.call(True).cpu().numpy().astype(float)
+        assert pkv.pkv_get_device_error()[0] == 3
+        assert (got[:30] == 7).all() and (got[32:] == 7).all()
+        check(got[30:32], (ref[30:32], tol[30:32]))
+
+
 def test_calls_in_flight_together_and_captured():
     c = Case(90, [500, 90, 1000], [30, 4, 1], 8, 2, 128)
     rules = dict(softcap=11.0, window=200, prefix_lens=[4, 4, 4])
