@@ -8,9 +8,9 @@
 // 128), window 4096 and a prefix of 4: 155 us, 6.56 TB/s of 1.02 GB (605 us without
 // the rules).  Bound by HBM in fp16 (8 x 32768 tokens with a bias: 162 us, 6.6 TB/s);
 // by the consumers' instructions for drafted tokens (64 x 4: 122 us where the calls
-// without rules take 114) and in FP8 (16 sequences of 8000 to 32768, capped: 132 us
-// where those take 115 and the bytes 103): 850 a head and two blocks there, issue slots
-// 41% busy with two warps a scheduler, and a chain of conversion, scores, cap,
+// without rules take 114) and in FP8 (16 sequences of 8000 to 32768, capped: 128 us
+// where those take 115 and the bytes 103): about 850 a head and two blocks there, issue
+// slots 44% busy with two warps a scheduler, and a chain of conversion, scores, cap,
 // maximum, weights and P V behind each step.
 #include "pkv_decode_balanced.cuh"
 

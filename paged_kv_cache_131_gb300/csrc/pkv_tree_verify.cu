@@ -20,10 +20,13 @@
 // (C as a pair of fp32: one rounding, 2^-24 of it), four neighbours are added in fp32
 // (as much again), and from there sums, masses and tests are carried as pairs of
 // fp32 whose errors are kept (47 bits).  fp64 would hold as much, but its
-// rate here is 2 a cycle and SM, and every warp walks: the same kernel in fp64
+// rate here is 2 a cycle and SM, and every warp walks: the first kernel, in fp64,
 // took 22.6, 129 and 44 us for a chain of 5 nodes, 64 trees of 16 (V 128256) and
-// 32 of 63 without drafts.
-// Bound: HBM for many sequences (the rows of p and q), latency for few.
+// 32 of 63 without drafts, with pairs 9.3, 41 and 13.5.
+// Bound: latency.  64 trees of 16 nodes (V 128256) take 35 us with inputs from HBM, 30
+// from the L2, where their rows are 70 MB (10.4 us): the chain of the slowest sequence,
+// up to six passes of 3 to 6 us; one chain of 5 takes 7.7: starts, nodes,
+// probabilities, a row and the draw, each behind the one before.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
