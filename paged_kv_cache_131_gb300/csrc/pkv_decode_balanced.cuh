@@ -107,13 +107,15 @@ __device__ __forceinline__ int cta_of(int64_t f, int64_t T, int64_t N) {
 // merged eight at a time (bounded registers).
 // kvh is the KV head, hl its index within its head group (the partial rows
 // are laid out per group member).
-template <int D, int R>
+// IN_FLIGHT: floats a lane has in flight.
+template <int D, int R, int IN_FLIGHT>
 __device__ void combine_partials(const BalancedParams &p, int kvh, int hl, int c_a, int c_b,
                                  int64_t f_s, int64_t T, int64_t N, int lane, int64_t row0,
                                  int ncols, int Gq) {
     constexpr int G = R < 8 ? R : 8;  // rows per pass
     constexpr int DPL = D / 32;
-    constexpr int U = (32 / (G * DPL)) < 1 ? 1 : ((32 / (G * DPL)) > 4 ? 4 : 32 / (G * DPL));
+    constexpr int W = IN_FLIGHT / (G * DPL), M = IN_FLIGHT / 8;
+    constexpr int U = W < 1 ? 1 : (W > M ? M : W);
     const int Hc = p.heads_per_cta;
     const int nc = c_b - c_a + 1;
     // first partial row of contributor c_a + j
@@ -363,11 +365,22 @@ __device__ __forceinline__ void balanced_body(const BalancedParams &p, uint8_t *
     // ---- empty sequences get zeros (no block of theirs is in any range)
     const int64_t Tb = cum[S];                 // blocks of one head group
     const int64_t T = Tb * p.groups;           // the whole (group, sequence, block) list
-    // Under rules a CTA takes kMinBlocks blocks or more: a sequence cut finer is sooner
-    // read, but later merged, two of its pieces at a time (one sequence of 1041 tokens:
-    // 23.3 us with at least one block, 17.3 with two, 14.2 with four, 14.8 with eight).
-    const int64_t N = min(static_cast<int64_t>(grid),
-                          kScored ? (T + kMinBlocks - 1) / kMinBlocks : T);
+    // Under rules a CTA takes `least` blocks or more: a sequence of B blocks cut into
+    // pieces of b is sooner read, but its B / b pieces are merged by one warp, a few at a
+    // time, so b grows as the root of B (the average over the sequences).  us with at
+    // least 1, 2, 4, 8, 16 blocks: one sequence of 1041 tokens (B 66, least 4) 23.3, 17.3,
+    // 13.1, 15.1, 19.4; two of up to 32108 with 2 KV heads (B 1100, least 16) 33 with 4,
+    // 23 with 8, 22 with 16; one of 32768 (least 22) 60, 60, 53 with 4, 8, 16.
+    int64_t pieces = T;
+    if constexpr (kScored) {
+        int least = kMinBlocks;
+        if constexpr (!Policy::kColumns) {  // (the columns' kernels have no registers for it)
+            const float each = static_cast<float>(T) / (static_cast<float>(S) * p.groups);
+            least = max(kMinBlocks, static_cast<int>(sqrtf(0.25f * each)));
+        }
+        pieces = (T + least - 1) / least;
+    }
+    const int64_t N = min(static_cast<int64_t>(grid), pieces);
     bool zeros_due = false;
     for (int s = blockIdx.x; s < S && !zeros_due; s += grid) zeros_due = lens[s] == 0;
     if (zeros_due && (blockIdx.x >= N || warp < Hc)) {
@@ -523,6 +536,9 @@ __device__ __forceinline__ void balanced_body(const BalancedParams &p, uint8_t *
     if (!p.defer_wait) grid_dependency_wait();  // outputs and partials are written below
 
     QueryRows qr{p.q, p.out, 0, H, kvh, G, 0};  // the current sequence's query rows
+    // (more in flight: two sequences of up to 32108 tokens 43.6 -> 33.1 us; the columns'
+    // kernels would spill, 122 -> 131 us for 64 x 4 drafted tokens)
+    constexpr int kInFlight = kScored && !Policy::kColumns ? 64 : 32;
     auto finish = [&](int vseq) {
         const int hg = grouped ? vseq / S : 0, seq = vseq - hg * S;
         const int64_t fg = static_cast<int64_t>(hg) * Tb;
@@ -556,10 +572,10 @@ __device__ __forceinline__ void balanced_body(const BalancedParams &p, uint8_t *
         if (last) {
             __syncwarp();  // memory order: lane 0's acquire before every lane's loads
             if constexpr (Policy::kColumns)
-                combine_partials<D, Policy::kRows>(p, kvh, hl, c_a, c_b, f_s, T, N, lane,
+                combine_partials<D, Policy::kRows, kInFlight>(p, kvh, hl, c_a, c_b, f_s, T, N, lane,
                                                    qr.row0, qr.ncols, G);
             else
-                combine_partials<D, G>(p, kvh, hl, c_a, c_b, f_s, T, N, lane, seq, G, G);
+                combine_partials<D, G, kInFlight>(p, kvh, hl, c_a, c_b, f_s, T, N, lane, seq, G, G);
         }
     };
 
