@@ -328,8 +328,9 @@ int pkv_decode_attention_fp8(void *out, const void *q, const void *k_cache, cons
  * before that kernel's completion the call reads only seq_lens, query_start,
  * q and block_tables, so such a kernel must not write those.
  * Supported: head_dim 64 or 128, block_size 16, group size 1, 2, 4 or 8.
- * Rows of a sequence whose Q exceeds max_query_len or L, or whose L exceeds
- * its block table or max_seq_len, are skipped and recorded as
+ * Rows of a sequence whose Q exceeds max_query_len or L, whose L exceeds
+ * its block table or max_seq_len, whose starts lie outside the rows or fall, or
+ * that starts below the sequence before it, are skipped and recorded as
  * PKV_DEVERR_SEQ_LEN; a bad block id is skipped and recorded.
  * Returns PKV_ERR_WORKSPACE when the workspace is missing or too small. */
 int pkv_chunk_attention(void *out, const void *q, const void *k_cache, const void *v_cache,

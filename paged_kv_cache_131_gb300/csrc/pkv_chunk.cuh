@@ -305,7 +305,8 @@ __device__ __forceinline__ bool seq_geo(const ChunkParams &p, int s, int G, bool
     const int q0 = __ldg(p.query_start + s), q1 = __ldg(p.query_start + s + 1);
     const int Q = q1 - q0;
     if (L < 0 || L > p.max_blocks_per_seq * kBS || L > p.max_seq_len || Q < 0 || Q > L ||
-        Q > p.max_query_len || q0 < 0 || q1 > p.num_query_tokens) {
+        Q > p.max_query_len || q0 < 0 || q1 > p.num_query_tokens ||
+        dec::starts_fall(p.query_start, s, q0, p.num_query_tokens)) {
         if (report) record_error(p.err, PKV_DEVERR_SEQ_LEN, s);
         return false;
     }

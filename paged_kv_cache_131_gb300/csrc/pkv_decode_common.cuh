@@ -31,6 +31,14 @@ constexpr int kBS = 16;  // tokens per physical block on the decode path
 constexpr float kNegInf = -INFINITY;
 constexpr float kLog2e = 1.44269504088896341f;
 
+// Whether sequence s (from row q0 on) starts below the one before it, whose rows then
+// are not its own to write.  (A start outside the rows takes its own sequences out.)
+__device__ __forceinline__ bool starts_fall(const int32_t *query_start, int s, int q0,
+                                            int num_query_tokens) {
+    const int before = s > 0 ? __ldg(query_start + s - 1) : 0;
+    return before > q0 && before <= num_query_tokens;
+}
+
 // Where byte b of token t's row sits in a staged tile.  The tensor copy
 // stores the tile chunk-major -- chunk c (bytes [c*C, (c+1)*C) of every row)
 // is 16 rows of C bytes -- and swizzles the 16-byte units of each row: unit
