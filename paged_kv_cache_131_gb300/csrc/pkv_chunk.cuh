@@ -303,10 +303,10 @@ __device__ __forceinline__ bool seq_geo(const ChunkParams &p, int s, int G, bool
                                         SeqGeo &sg) {
     const int L = __ldg(p.seq_lens + s);
     const int q0 = __ldg(p.query_start + s), q1 = __ldg(p.query_start + s + 1);
-    const int Q = q1 - q0;
-    if (L < 0 || L > p.max_blocks_per_seq * kBS || L > p.max_seq_len || Q < 0 || Q > L ||
-        Q > p.max_query_len || q0 < 0 || q1 > p.num_query_tokens ||
-        dec::starts_fall(p.query_start, s, q0, p.num_query_tokens)) {
+    const bool in = q0 >= 0 && q1 >= q0 && q1 <= p.num_query_tokens;  // (so q1 - q0 fits)
+    const int Q = in ? q1 - q0 : 0;
+    if (!in || L < 0 || L > p.max_blocks_per_seq * kBS || L > p.max_seq_len || Q > L ||
+        Q > p.max_query_len || dec::starts_fall(p.query_start, s, q0, p.num_query_tokens)) {
         if (report) record_error(p.err, PKV_DEVERR_SEQ_LEN, s);
         return false;
     }
@@ -447,8 +447,9 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const __grid_constant_
             }
         } else if (s < p.num_seqs && p.max_cols > 0) {
             const int L = __ldg(p.seq_lens + s);
-            const int Q = __ldg(p.query_start + s + 1) - __ldg(p.query_start + s);
-            if (Q > 0 && Q <= L && Q * G <= p.max_cols && L <= p.max_blocks_per_seq * kBS)
+            const int q0 = __ldg(p.query_start + s), q1 = __ldg(p.query_start + s + 1);
+            const int Q = q0 >= 0 && q1 >= q0 && q1 <= p.num_query_tokens ? q1 - q0 : 0;
+            if (Q > 0 && Q <= L && Q <= p.max_cols / G && L <= p.max_blocks_per_seq * kBS)
                 my_dec = static_cast<unsigned long long>((L + kBS - 1) / kBS);
             if constexpr (kRules) {
                 if (my_dec > 0) {
