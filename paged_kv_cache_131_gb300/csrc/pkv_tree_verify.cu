@@ -217,8 +217,9 @@ __global__ void __launch_bounds__(kThreads, 3)
     cluster.barrier_arrive();
     grid_dependency_wait();
     const int row0 = __ldg(p.query_start + seq), row1 = __ldg(p.query_start + seq + 1);
-    int Q = row1 - row0;
-    if (row0 < 0 || row1 > p.num_nodes || Q < 0 || Q > kMaxNodes) {
+    const bool in = row0 >= 0 && row1 >= row0 && row1 <= p.num_nodes;  // (so row1 - row0 fits)
+    int Q = in ? row1 - row0 : 0;
+    if (!in || Q > kMaxNodes) {
         if (cta == 0 && threadIdx.x == 0) record_error(p.err, PKV_DEVERR_SEQ_LEN, seq);
         Q = 0;
     }

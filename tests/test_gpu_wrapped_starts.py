@@ -57,3 +57,21 @@ def test_chunk(start, scored):
     assert kind == 3 and index in (0, 1, 2)
     # sequences 0 to 2 end or begin at a bad start
     assert (got[:c.start[3]] == 7).all() and right(got)
+
+
+@pytest.mark.parametrize("drafted", [True, False])
+@pytest.mark.parametrize("start", [(HI, LO), (HI, LO + 4), (HI - 3, LO), (HI - 255, LO), (HI, LO + 255)])
+def test_verify(start, drafted):
+    from test_gpu_verify import call, check, make
+    c = make(np.random.default_rng([112, drafted]), [3, 5, 4, 6], 50, drafted)
+    check(c, 4, call(c, 4))
+    bad = dict(c, start=c["start"].copy())
+    bad["start"][1:3] = start
+    path, lens, nxt = call(bad, 4)
+    kind, index = pkv.pkv_get_device_error()
+    assert kind == 3 and index in (0, 1, 2)
+    for i in range(3):
+        assert path[i].tolist() == [-1] * 4 and lens[i] == 0 and nxt[i] == -1
+    want = call(c, 4)
+    assert np.array_equal(path[3], want[0][3])
+    assert (lens[3], nxt[3]) == (want[1][3], want[2][3])
