@@ -196,9 +196,11 @@ int pkv_copy_blocks(void *cache, pkv_view view, int32_t num_layers, int32_t bloc
  *  workspace     device scratch, 16-byte aligned, of at least
  *                pkv_decode_workspace_bytes(...) bytes (or NULL, see above).
  *                It must be zero-filled before its first use (e.g. by
- *                pkv_decode_workspace_init); every call that records no
- *                PKV_DEVERR_TIMEOUT leaves it zero-filled again.  Calls that
- *                share a workspace must not overlap on the GPU.
+ *                pkv_decode_workspace_init), and again after a call that records
+ *                PKV_DEVERR_TIMEOUT.  Otherwise decode and chunk calls of any kind
+ *                and shape, FP8 and under score rules, may follow one another
+ *                on it; what other code writes into it has to be zeroed again.
+ *                Calls that share a workspace must not overlap on the GPU.
  *  Ordering: the launch may overlap the previous kernel in the stream when
  *  that kernel signals programmatic launch completion (pkv_cache_write does).
  *  Before that kernel's completion the call reads only q, block_tables and
@@ -289,8 +291,8 @@ int pkv_cache_write_fp8(const void *k, const void *v, const int64_t *slot_mappin
  * and values are dequantized as value(code) * scale of their row; the result
  * is the attention of pkv_decode_attention on those values.  Needs
  * 16-byte aligned caches and scales and a workspace of
- * pkv_decode_workspace_bytes(...) bytes (zero-filled before first use, left
- * zero-filled).  Other arguments and errors as pkv_decode_attention.
+ * pkv_decode_workspace_bytes(...) bytes (zero-filled before its first use, as for
+ * pkv_decode_attention).  Other arguments and errors as pkv_decode_attention.
  */
 int pkv_decode_attention_fp8(void *out, const void *q, const void *k_cache, const void *v_cache,
                              const float *k_scale, const float *v_scale,
@@ -322,7 +324,8 @@ int pkv_decode_attention_fp8(void *out, const void *q, const void *k_cache, cons
  *   max_query_len   host bound on every Q (sizes the launch)
  *   max_seq_len     host bound on every L (sizes the launch and workspace)
  *   workspace       pkv_chunk_workspace_bytes(...) bytes, zeroed once
- *                   (pkv_decode_workspace_init); every call leaves it zeroed
+ *                   (pkv_decode_workspace_init), as for pkv_decode_attention
+ *                   and with the same calls
  * Ordering: as for pkv_decode_attention, the launch may overlap a previous
  * kernel that signals programmatic launch completion (pkv_cache_write does);
  * before that kernel's completion the call reads only seq_lens, query_start,
@@ -379,7 +382,7 @@ typedef struct pkv_score_rules {
  * see holds, infinities and NaN included, does not reach its output.
  *  rules      HOST pointer, read during the call only; not NULL
  *  workspace  pkv_decode_workspace_bytes(...) bytes, as for
- *             pkv_decode_attention: zero-filled before first use, left so
+ *             pkv_decode_attention: zero-filled before its first use
  * Runs on the balanced schedule alone: shapes that it does not take (num_seqs
  * whose lengths do not fit shared memory beside two stages, or num_seqs *
  * max_blocks_per_seq above 2^31 - 1) return PKV_ERR_UNSUPPORTED.  Other

@@ -29,7 +29,9 @@ struct Sizes {
 };
 
 // scored: under score rules, which need no more of anything than without (so the
-// workspace sized without them does), but other shared memory on the balanced schedule.
+// workspace sized without them does), but other shared memory on the balanced schedule,
+// whose grid and scratch may be smaller.  The tile kernel's part then lies elsewhere than
+// without rules; nothing in it has to hold over from one call to the next.
 Sizes sizes(int64_t S, int64_t H, int64_t Hk, int64_t D, int64_t Tq, int64_t max_q,
             int64_t max_len, bool scored) {
     Sizes z{};
@@ -47,7 +49,8 @@ Sizes sizes(int64_t S, int64_t H, int64_t Hk, int64_t D, int64_t Tq, int64_t max
     z.bal = dec::balanced_shape(static_cast<int>(S), static_cast<int>(Hk), static_cast<int>(G),
                                 static_cast<int>(D), sm_count(), false, 8 * z.col_tiles, scored);
     if (!z.bal.ok) z.col_tiles = 0;
-    z.bal_bytes = z.bal.ok ? dec::align256(z.bal.workspace) : 0;
+    // (the room for tickets at the start is kept by every call)
+    z.bal_bytes = z.bal.ok ? dec::align256(z.bal.workspace) : dec::kTicketBytes;
     return z;
 }
 

@@ -412,9 +412,13 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const __grid_constant_
     // schedule streams, and 128-key steps of the tile kernel's items
     __shared__ unsigned long long dec_blocks;
     __shared__ float tile_steps;
+    // sequences of several partitions, whose tiles' tickets are set to zero here: the
+    // workspace may hold another call's partial states there
+    __shared__ int cut_seq[1024], cut_tiles[1024], cuts;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         run[0] = run[1] = 0;
+        cuts = 0;
         dec_blocks = 0ull;
         tile_steps = 0.f;
     }
@@ -424,6 +428,11 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const __grid_constant_
         SeqGeo sg;
         const bool mine = s < p.num_seqs && seq_geo<kRules>(p, s, G, true, sg);
         const int cnt = mine ? seq_items<kRules>(sg, G, p.num_kv_heads) : 0;
+        if (mine && sg.parts > 1) {
+            const int e = atomicAdd(&cuts, 1);
+            cut_seq[e] = s;
+            cut_tiles[e] = sg.tiles;
+        }
         float my_steps = 0.f;
         unsigned long long my_dec = 0;
         if (mine) {
@@ -516,10 +525,18 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const __grid_constant_
             p.big_seq[ea] = s;
             p.big_cum[ea] = ec;
         }
+        for (int e = 0; e < cuts; ++e) {
+            const int per = cut_tiles[e] * kSoftmaxWarps;  // a KV head's tickets
+            int *at = p.counters + static_cast<int64_t>(cut_seq[e]) * p.num_kv_heads * p.num_tiles *
+                                       kSoftmaxWarps;
+            for (int i = threadIdx.x; i < per * p.num_kv_heads; i += blockDim.x)
+                at[static_cast<int64_t>(i / per) * p.num_tiles * kSoftmaxWarps + i % per] = 0;
+        }
         __syncthreads();
         if (threadIdx.x == blockDim.x - 1) {
             run[0] = ea + (mine ? 1 : 0);
             run[1] = ec + cnt;
+            cuts = 0;
         }
         __syncthreads();
     }
@@ -1601,8 +1618,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   kSoftmaxWarps +
                               (warp - 3);
                 last = atom_add_acq_rel_gpu(ticket, 1) == nparts - 1;
-                // every partition has taken its ticket: leave the workspace zeroed
-                if (last) st_relaxed_gpu(ticket, 0);
             }
             last = __shfl_sync(0xffffffffu, last, 0);
             __syncwarp();  // memory order: lane 0's acquire before every lane's loads

@@ -290,9 +290,9 @@ int pkv_decode_attention_ex(void *out, const void *q, const void *k_cache, const
         if (workspace == nullptr || static_cast<int64_t>(workspace_bytes) < need)
             return PKV_ERR_WORKSPACE;
         uint8_t *ws = static_cast<uint8_t *>(workspace);
-        const int64_t c_bytes = align256(static_cast<int64_t>(num_seqs) * num_heads * 4);
+        const int64_t own = grid_ticket_bytes(num_seqs, num_heads), c_bytes = kTicketBytes + own;
         const int64_t ml_bytes = align256(static_cast<int64_t>(num_seqs) * num_heads * P * 8);
-        p.counters = reinterpret_cast<int *>(ws);
+        p.counters = reinterpret_cast<int *>(own > 0 ? ws + kTicketBytes : ws);
         p.part_ml = reinterpret_cast<float2 *>(ws + c_bytes);
         p.part_o = reinterpret_cast<float *>(ws + c_bytes + ml_bytes);
         // the combine's per-partition weights must fit in the (reused) ring
@@ -309,6 +309,11 @@ int pkv_decode_attention_ex(void *out, const void *q, const void *k_cache, const
     }
     p.err = device_error_record();
     if (p.err == nullptr) return PKV_ERR_CUDA;
+    const int64_t own = P > 1 ? grid_ticket_bytes(num_seqs, num_heads) : 0;
+    if (own > 0) {
+        const cudaError_t e = cudaMemsetAsync(p.counters, 0, static_cast<size_t>(own), s);
+        if (e != cudaSuccess) return cuda_failure(e, "cudaMemsetAsync(tickets)");
+    }
     return launch_grid(p, head_dim, G, simt, num_seqs, s);
 }
 

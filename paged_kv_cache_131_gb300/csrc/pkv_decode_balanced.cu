@@ -69,8 +69,8 @@ BalancedShape balanced_shape(int num_seqs, int num_kv_heads, int G, int D, int n
     r.ctas_per_sm = std::max(1, std::min({(228 * 1024) / (r.smem + 1024), 2048 / threads, 32}));
     r.grid = std::max(1, num_sms) * r.ctas_per_sm;
     const int64_t slots = 2 * static_cast<int64_t>(r.grid) * hc * rows;
-    r.workspace = align256(static_cast<int64_t>(num_seqs) * num_kv_heads * 4) +
-                  align256(slots * 8) + slots * D * 4;
+    r.workspace = kTicketBytes + align256(slots * 8) + slots * D * 4;
+    if (static_cast<int64_t>(r.grid) * hc * 4 > kTicketBytes) r.ok = false;
     return r;
 }
 
@@ -81,11 +81,10 @@ int setup_balanced(BalancedParams &p, const BalancedShape &shape, int rows, void
     p.heads_per_cta = shape.heads;
     p.groups = shape.groups;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const int64_t c_bytes = align256(static_cast<int64_t>(p.num_seqs) * p.num_kv_heads * 4);
     const int64_t slots = 2 * static_cast<int64_t>(shape.grid) * shape.heads * rows;
     p.counters = reinterpret_cast<int *>(ws);
-    p.part_ml = reinterpret_cast<float2 *>(ws + c_bytes);
-    p.part_o = reinterpret_cast<float *>(ws + c_bytes + align256(slots * 8));
+    p.part_ml = reinterpret_cast<float2 *>(ws + kTicketBytes);
+    p.part_o = reinterpret_cast<float *>(ws + kTicketBytes + align256(slots * 8));
     // maps over whole rows (all heads); a box covers one head group
     const int full_row = shape.row_bytes * shape.groups;
     const int box = shape.row_bytes / chunk_bytes_for_row(shape.row_bytes);

@@ -563,10 +563,10 @@ __device__ __forceinline__ void balanced_body(const BalancedParams &p, uint8_t *
         const int c_a = cta_of(f_s, T, N), c_b = cta_of(f_e - 1, T, N);
         int last = 0;
         if (lane == 0) {
-            int *ticket = p.counters + static_cast<int64_t>(seq) * Hk + kvh;
+            int *ticket = p.counters + c_a * Hc + hl;
             const int prev = atom_add_acq_rel_gpu(ticket, 1);
             last = prev == c_b - c_a;
-            // every contributor has taken its ticket: leave the workspace zeroed
+            // every contributor has taken its ticket: leave it at zero
             if (last) st_relaxed_gpu(ticket, 0);
         }
         last = __shfl_sync(0xffffffffu, last, 0);

@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kThreads)
         int *ticket = p.counters + static_cast<int64_t>(seq) * p.num_kv_heads + kvh;
         const int prev = atom_add_acq_rel_gpu(ticket, 1);
         const int last = prev == nparts - 1;
-        // every partition has taken its ticket: leave the workspace zeroed
+        // every partition has taken its ticket: leave it at zero
         if (last) st_relaxed_gpu(ticket, 0);
         misc[1] = last;
     }
@@ -309,9 +309,13 @@ int grid_smem_bytes(int D, int G, int partition_blocks) {
            4 * 4 + kWarps * kBS * G * 4;
 }
 
+int64_t grid_ticket_bytes(int64_t S, int64_t H) {
+    return S * H * 4 > kTicketBytes ? align256(S * H * 4) : 0;
+}
+
 int64_t grid_workspace_bytes(int64_t S, int64_t H, int64_t D, int64_t P) {
     if (P <= 1) return 0;
-    return align256(S * H * 4) + align256(S * H * P * 8) + S * H * P * D * 4;
+    return kTicketBytes + grid_ticket_bytes(S, H) + align256(S * H * P * 8) + S * H * P * D * 4;
 }
 
 int launch_grid(const GridParams &p, int D, int G, bool simt, int num_seqs,

@@ -63,7 +63,7 @@ struct GridParams {
     int num_partitions;    // P, grid.z
     int partition_blocks;  // partition_size / 16
     int64_t num_blocks;
-    int *counters;    // [S * Hk] tickets, zero between calls
+    int *counters;    // [S * Hk] tickets, zero before and after a call
     float2 *part_ml;  // [S, H, P] (m, l)
     float *part_o;    // [S, H, P, D]
     ErrorRecord *err;
@@ -73,6 +73,9 @@ struct GridParams {
 int grid_ring_bytes(int D);
 int grid_smem_bytes(int D, int G, int partition_blocks);
 int64_t grid_workspace_bytes(int64_t S, int64_t H, int64_t D, int64_t P);
+// Bytes of tickets that do not fit the room at the workspace's start: they then lie
+// behind it and are zeroed by each call.
+int64_t grid_ticket_bytes(int64_t S, int64_t H);
 int launch_grid(const GridParams &p, int D, int G, bool simt, int num_seqs,
                 cudaStream_t stream);
 
@@ -92,6 +95,13 @@ struct RuleParams {
 
 // Argument checks of the rules and their device form.  Returns a PKV status.
 int make_rules(const pkv_score_rules *rules, float scale, RuleParams *out);
+
+// Every decode and chunk call's workspace starts with room for tickets that lie between
+// calls at zero (the last taker puts its ticket back), whatever the calls' kinds and
+// shapes: nothing else is ever written there, so that one call's partial states are not
+// the next one's tickets.  The balanced schedule needs grid * heads_per_cta of them, at
+// most 64 an SM, 64 KB on the 256 SMs that sizes without a device assume.
+constexpr int64_t kTicketBytes = 64 << 10;
 
 // Balanced schedule.
 struct BalancedParams {
@@ -131,7 +141,9 @@ struct BalancedParams {
     // first ones) instead of the whole grid; written by an earlier kernel
     const int *active_ctas;
     int64_t num_blocks;
-    int *counters;    // [S * Hk] tickets, zero between calls
+    // [grid * heads_per_cta] tickets, zero between calls: a sequence that several CTAs
+    // share takes those of the first of them (no other one goes on into the next CTA)
+    int *counters;
     float2 *part_ml;  // [2 * grid][heads_per_cta][rows]
     float *part_o;    // [2 * grid][heads_per_cta][rows][D]
     ErrorRecord *err;

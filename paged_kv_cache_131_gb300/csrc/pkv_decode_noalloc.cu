@@ -108,13 +108,12 @@ extern "C" int pkv_decode_attention_noalloc(void *out, const void *q, const void
     }
     void *scratch = scratch_on_current_device();
     if (scratch == nullptr) return PKV_ERR_CUDA;
-    // The ticket counters must start at zero; the scratch keeps whatever the
-    // previous call (of any shape) left, so clear the counter region (at most
-    // num_seqs * num_heads int32, at the start of the scratch) every call.
-    const size_t counters = (static_cast<size_t>(num_seqs) * num_heads * 4 + 255) / 256 * 256;
-    cudaError_t e = cudaMemsetAsync(scratch, 0, std::min(counters, kScratchBytes),
+    // The tickets at the start of the scratch lie at zero between calls, but a
+    // call that gave up (PKV_DEVERR_TIMEOUT) may have left some taken, and no
+    // caller can reach the scratch to zero it: clear them every call.
+    cudaError_t e = cudaMemsetAsync(scratch, 0, static_cast<size_t>(dec::kTicketBytes),
                                     reinterpret_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return cuda_failure(e, "cudaMemsetAsync(no-alloc scratch counters)");
+    if (e != cudaSuccess) return cuda_failure(e, "cudaMemsetAsync(no-alloc scratch tickets)");
     return pkv_decode_attention_ex(out, q, k_cache, v_cache, block_tables, seq_lens, scale,
                                    num_heads, num_kv_heads, head_dim, block_size, num_seqs,
                                    max_blocks_per_seq, max_seq_len, num_blocks, scratch,
