@@ -848,7 +848,7 @@ struct MmaFp8Policy {
             for (int j = 0; j < 4; ++j) x[b][j] = sa[j] + sb[j];
         }
         // scale, mask, and the block max of each of the lane's two heads
-        // log2 of the value scales (bounded below: a zero has none).  (Their exponents
+        // log2 of the value scales' sizes (bounded below: a zero has none).  (Their exponents
         // alone would do and spare the special-function unit, but took no less time, and
         // leave the row's largest product to be rounded: 3.0e-4 against 2.2e-4 off.)
         float lv[NB][kLaneTokens];
@@ -856,7 +856,7 @@ struct MmaFp8Policy {
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int r = 0; r < kLaneTokens; ++r) lv[b][r] = fmaxf(__log2f(vs[b][r]), -64.f);
+                for (int r = 0; r < kLaneTokens; ++r) lv[b][r] = fmaxf(__log2f(fabsf(vs[b][r])), -64.f);
         }
         float flat[NB * 4];  // (the scores of both blocks take one vote)
         if constexpr (kRules) {
