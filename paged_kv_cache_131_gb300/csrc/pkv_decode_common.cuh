@@ -60,9 +60,11 @@ struct SwizzledTile {
 // Score rules (pkv_score_rules) as a policy applies them, everything in the
 // log2 domain: t = cap * tanh(y), y = scale q.k / cap, then a bias of -slope *
 // distance, then the mask.
-//  - Where all of a warp's scores are below 0.4 of the cap -- where a model's cap
-//    leaves most of them -- tanh(y) is y times a polynomial of degree 3 in y^2 with the
-//    scales multiplied in (RuleParams), off by 2^-23.3 of itself.
+//  - For a score below 0.4 of the cap -- where a model's cap leaves most of them --
+//    tanh(y) is y times a polynomial of degree 3 in y^2 with the scales multiplied in
+//    (RuleParams), off by 2^-23.3 of itself.  Which form a score takes rests on that
+//    score alone: where all of a warp's take this one the others are passed over, but
+//    what lies in a place that a row does not see changes no bit of the row.
 //  - Else 1 - 2 / (1 + e^(2y)), two special-function instructions, off by
 //    10 2^-24 (of the cap, once multiplied); its limits (0 and infinity of e^(2y))
 //    come out as -1 and 1.  For caps up to 512 in log2 units that is below 2^-11, a
@@ -127,25 +129,30 @@ template <int N, class Distance, class Slope>
 __device__ __forceinline__ void rule_scores(float (&x)[N], float scale_log2, const BlockRules &br,
                                             Distance d, Slope slope) {
     if (br.cap_log2 > 0.f) {
+        auto below = [&](float v) {
+            const float t = v * v;
+            return v * fmaf(t, fmaf(t, fmaf(t, br.near[3], br.near[2]), br.near[1]), br.near[0]);
+        };
         bool near = true;
 #pragma unroll
         for (int i = 0; i < N; ++i) near = near && fabsf(x[i]) <= br.near_most;
         if (__all_sync(0xffffffffu, near)) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float t = x[i] * x[i];
-                x[i] *= fmaf(t, fmaf(t, fmaf(t, br.near[3], br.near[2]), br.near[1]), br.near[0]);
-            }
+            for (int i = 0; i < N; ++i) x[i] = below(x[i]);
         } else if (br.cap_log2 <= kExpCapLog2) {
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                x[i] = br.cap_log2 * tanh_exp(x[i] * (br.cap_scale * (2.f * kLog2e)));
+            for (int i = 0; i < N; ++i) {
+                const float far =
+                    br.cap_log2 * tanh_exp(x[i] * (br.cap_scale * (2.f * kLog2e)));
+                x[i] = fabsf(x[i]) <= br.near_most ? below(x[i]) : far;
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const float y = x[i] * br.cap_scale;
-                x[i] = br.cap_log2 *
-                       (fabsf(y) <= 1.f ? tanh_near(y) : tanh_exp(y * (2.f * kLog2e)));
+                const float far = br.cap_log2 * (fabsf(y) <= 1.f ? tanh_near(y)
+                                                                 : tanh_exp(y * (2.f * kLog2e)));
+                x[i] = fabsf(x[i]) <= br.near_most ? below(x[i]) : far;
             }
         }
     } else {
