@@ -537,6 +537,24 @@ __device__ __forceinline__ void balanced_body(const BalancedParams &p, uint8_t *
     if (!p.defer_wait) grid_dependency_wait();  // outputs and partials are written below
 
     QueryRows qr{p.q, p.out, 0, H, kvh, G, 0};  // the current sequence's query rows
+    BlockRules br{};
+    if constexpr (kScored) {
+        br.window = p.rules.window;
+        br.cap_log2 = p.rules.cap_log2;
+        br.cap_scale = p.rules.cap_scale;
+        br.near_most = p.rules.near_most;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) br.near[i] = p.rules.near[i];
+        br.biased = p.rules.slopes != nullptr;
+    }
+    // (a block that ends by the first token's position and starts in the last one's
+    // window, or lies in the prefix, is seen whole)
+    auto seen_whole = [&](int kp) {
+        return kp + kBS <= br.prefix || (kp + kBS - 1 <= qr.lim0 &&
+                                         qr.lim0 + qr.ncols / G - 1 - kp < br.window);
+    };
+    bool dirty = false;  // (columns) values left out of the current sequence's blocks
+
     // (more in flight: two sequences of up to 32108 tokens 43.6 -> 33.1 us; the columns'
     // kernels would spill, 122 -> 131 us for 64 x 4 drafted tokens)
     constexpr int kInFlight = kScored && !Policy::kColumns ? 64 : 32;
@@ -545,6 +563,22 @@ __device__ __forceinline__ void balanced_body(const BalancedParams &p, uint8_t *
         const int64_t fg = static_cast<int64_t>(hg) * Tb;
         const int64_t f_s = fg + cum[seq], f_e = fg + cum[seq + 1];
         const int64_t qrow = static_cast<int64_t>(seq) * H + kvh * G;
+        if constexpr (kScored && Policy::kColumns) {
+            if (dirty) {
+                dirty = false;
+                const int end = static_cast<int>(min(f_e, f1) - f_s);
+                for (int i = static_cast<int>(max(f_s, f0) - f_s); i < end; ++i) {
+                    const int blk = i < (pre[seq] + kBS - 1) / kBS ? i : i + skip[seq];
+                    const int nv = min(kBS, lens[seq] - blk * kBS);
+                    const int64_t id = __ldg(p.block_tables +
+                                             static_cast<int64_t>(seq) * p.max_blocks_per_seq + blk);
+                    br.kp = blk * kBS;
+                    if ((nv < kBS || !seen_whole(br.kp)) && id >= 0 && id < p.num_blocks)
+                        st.add_values(p.v_cache + (id * kBS * Hk + kvh) * D,
+                                      static_cast<int64_t>(Hk) * D, nv, br, lane);
+                }
+            }
+        }
         if (f_s >= f0 && f_e <= f1) {
             if constexpr (Policy::kColumns) st.write_output(qr, lane);
             else st.write_output(p.out + qrow * D, lane);
@@ -593,16 +627,6 @@ __device__ __forceinline__ void balanced_body(const BalancedParams &p, uint8_t *
         }
     };
 
-    BlockRules br{};
-    if constexpr (kScored) {
-        br.window = p.rules.window;
-        br.cap_log2 = p.rules.cap_log2;
-        br.cap_scale = p.rules.cap_scale;
-        br.near_most = p.rules.near_most;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) br.near[i] = p.rules.near[i];
-        br.biased = p.rules.slopes != nullptr;
-    }
     // under rules: values of keys that the token does not see never reach it,
     // whatever they hold
     auto hide = [&](uint32_t vb, uint32_t head, BlockRules &b, int nv) {
@@ -712,13 +736,8 @@ __device__ __forceinline__ void balanced_body(const BalancedParams &p, uint8_t *
                 if (Policy::kZeroTailRows && (!kScored || Policy::kColumns) && mt.y < kBS)
                     zero_tail_rows<D>(vb, tile, head, mt.y, lane);
                 if constexpr (kScored && Policy::kColumns) {
-                    // (a block that ends by the first token's position and starts
-                    // in the last one's window, or lies in the prefix, is seen whole)
-                    const int last = qr.lim0 + qr.ncols / G - 1;
-                    const bool whole = mt.y == kBS && (br.kp + kBS <= br.prefix ||
-                                                       (br.kp + kBS - 1 <= qr.lim0 &&
-                                                        last - br.kp < br.window));
-                    if (!whole) st.clean_values(vb, tile, head, mt.y, br, lane);
+                    const bool whole = mt.y == kBS && seen_whole(br.kp);
+                    if (!whole && st.clean_values(vb, tile, head, mt.y, lane)) dirty = true;
                     st.block(kb, vb, tile, head, mt.y, br.kp, p.scale_log2, lane, br, whole);
                 } else if constexpr (Policy::kColumns)
                     st.block(kb, vb, tile, head, mt.y, mt.w * kBS, p.scale_log2, lane);

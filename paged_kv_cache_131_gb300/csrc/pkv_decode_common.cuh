@@ -185,12 +185,6 @@ __device__ __forceinline__ void lds128(uint32_t (&w)[4], uint32_t addr) {
                  : "r"(addr));
 }
 
-__device__ __forceinline__ float lds_half(uint32_t addr) {
-    unsigned short u;
-    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(u) : "r"(addr));
-    return __half2float(__ushort_as_half(u));
-}
-
 // Whether one head's fp16 slice of value rows [0, nv) holds an infinity or a NaN
 // (every lane).
 template <int D>
@@ -652,12 +646,20 @@ struct MmaColsPolicy {
 
     // A block that some column does not see whole: a masked weight is 0, but 0
     // times an infinity or a NaN is not, so the value rows' elements that are
-    // not finite are zeroed in the tile and added to the columns that see them
-    // (their weight, however small, leaves such an element what it is).  The
-    // checks are calls, so that the state stays in registers.
-    __device__ __forceinline__ void clean_values(uint32_t vb, SwizzledTile tile, uint32_t head,
-                                                 int nv, const BlockRules &br, int lane) {
-        if (!any_non_finite<D>(vb, tile, head, nv, lane)) return;
+    // not finite are zeroed in the tile, and added to the columns that see them (whose
+    // weight leaves such an element what it is) once the sequence's last block of this
+    // CTA is in: O is rescaled until then, and 0 times an infinity is a NaN.  The checks
+    // are calls, so that the state stays in registers; true: there were some.
+    __device__ __forceinline__ static bool clean_values(uint32_t vb, SwizzledTile tile,
+                                                        uint32_t head, int nv, int lane) {
+        if (!any_non_finite<D>(vb, tile, head, nv, lane)) return false;
+        zero_non_finite<D>(vb, tile, head, nv, lane);
+        return true;
+    }
+
+    // values: the head's part of the block's first row in the cache, rows apart.
+    __device__ __forceinline__ void add_values(const __half *values, int64_t apart, int nv,
+                                               const BlockRules &br, int lane) {
         const int g = lane >> 2;
 #pragma unroll 1
         for (int tok = 0; tok < nv; ++tok)
@@ -665,7 +667,7 @@ struct MmaColsPolicy {
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float v = lds_half(vb + tile.at(tok, head + (16 * mt + g + 8 * i) * 2));
+                    const float v = __half2float(values[tok * apart + 16 * mt + g + 8 * i]);
                     if (isfinite(v)) continue;
 #pragma unroll
                     for (int c = 0; c < NT; ++c)
@@ -673,8 +675,6 @@ struct MmaColsPolicy {
                         for (int h = 0; h < 2; ++h)
                             if (sees(c, h, br.kp + tok, br)) o[c][mt][2 * i + h] += v;
                 }
-        __syncwarp();
-        zero_non_finite<D>(vb, tile, head, nv, lane);
     }
 
     __device__ __forceinline__ float l_total(int c, int h) const {
