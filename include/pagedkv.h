@@ -334,7 +334,9 @@ int pkv_decode_attention_fp8(void *out, const void *q, const void *k_cache, cons
  * Rows of a sequence whose Q exceeds max_query_len or L, whose L exceeds
  * its block table or max_seq_len, whose starts lie outside the rows or fall, or
  * that starts below the sequence before it, are skipped and recorded as
- * PKV_DEVERR_SEQ_LEN; a bad block id is skipped and recorded.
+ * PKV_DEVERR_SEQ_LEN; a bad block id is skipped and recorded.  A sequence of
+ * length 0 is left out of the call: its rows, however many, are not written, and
+ * nothing is recorded.
  * Returns PKV_ERR_WORKSPACE when the workspace is missing or too small. */
 int pkv_chunk_attention(void *out, const void *q, const void *k_cache, const void *v_cache,
                         const int32_t *block_tables, const int32_t *seq_lens,
@@ -453,6 +455,12 @@ int pkv_chunk_attention_scored(void *out, const void *q, const void *k_cache,
  *    max_tokens and, where it needs blocks, the blocks needed up to it fit the
  *    list; else it keeps its length and entries, and its rows get slot -1.
  *  - out_lens[i] = N if granted (or N <= L), else L: compare with new_lens.
+ *    A refused sequence's rows hold no tokens of it.  The write skips them (slot
+ *    -1); the attention behind it is given length 0 for that sequence, e.g.
+ *    out_lens[i] == new_lens[i] ? out_lens[i] : 0, which leaves it out, and
+ *    pkv_tree_accept a path of -1 (its table entries past L are not its own).
+ *    With its kept length L the rows would be taken for its last Q tokens, or,
+ *    if there are not so many, be recorded as an error.
  *  - query_start[i] = new tokens asked for by the sequences before i, at most
  *    max_tokens; rows from query_start[num_seqs] on get slot -1 and position 0,
  *    so the writes of a step captured for max_tokens rows skip them.

@@ -745,7 +745,9 @@ def pkv_resize_sequences(block_tables, seq_lens, new_lens, out_lens, free_blocks
     int32 [S] (out_lens may be seq_lens); free_blocks: CUDA int32 [capacity], a
     stack of free_count[0] entries; free_count, out_free_count: CUDA int32 [1] (may
     be the same); query_start: CUDA int32 [S + 1]; slot_mapping, positions: CUDA
-    int64 [max_tokens] (positions may be None).
+    int64 [max_tokens] (positions may be None).  Sequences for which rows or blocks
+    do not last keep their length; the step's attentions are to leave them out:
+    torch.where(out_lens == new_lens, out_lens, 0) as their seq_lens.
     """
     import torch
     i32, i64 = torch.int32, torch.int64

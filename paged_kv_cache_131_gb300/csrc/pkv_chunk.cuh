@@ -305,6 +305,7 @@ __device__ __forceinline__ bool seq_geo(const ChunkParams &p, int s, int G, bool
     const int q0 = __ldg(p.query_start + s), q1 = __ldg(p.query_start + s + 1);
     const bool in = q0 >= 0 && q1 >= q0 && q1 <= p.num_query_tokens;  // (so q1 - q0 fits)
     const int Q = in ? q1 - q0 : 0;
+    if (in && L == 0) return false;  // left out of the call, whatever its rows
     if (!in || L < 0 || L > p.max_blocks_per_seq * kBS || L > p.max_seq_len || Q > L ||
         Q > p.max_query_len || dec::starts_fall(p.query_start, s, q0, p.num_query_tokens)) {
         if (report) record_error(p.err, PKV_DEVERR_SEQ_LEN, s);

@@ -295,11 +295,14 @@ __device__ __forceinline__ void balanced_body(const BalancedParams &p, uint8_t *
             L = L < 0 ? 0 : cap;
         }
         if constexpr (Policy::kColumns) {
-            // -1: not this kernel's (no new token, or more columns than it holds)
+            // -1: not this kernel's (no new token, or more columns than it holds; left out)
             const int q0 = __ldg(p.query_start + s), q1 = __ldg(p.query_start + s + 1);
             const int nq = q1 - q0;
-            if (q0 < 0 || q1 < q0 || q1 > p.num_query_tokens || nq > L ||
-                starts_fall(p.query_start, s, q0, p.num_query_tokens)) {
+            const bool in = q0 >= 0 && q1 >= q0 && q1 <= p.num_query_tokens;
+            if (in && L == 0) {
+                L = -1;  // left out of the call, whatever its rows
+            } else if (!in || nq > L ||
+                       starts_fall(p.query_start, s, q0, p.num_query_tokens)) {
                 if (blockIdx.x == 0) record_error(p.err, PKV_DEVERR_SEQ_LEN, s);
                 L = -1;
             } else if (nq > p.max_cols / G) {

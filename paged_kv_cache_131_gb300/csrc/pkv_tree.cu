@@ -401,6 +401,7 @@ __device__ __forceinline__ bool seq_geo(const TreeParams &p, int s, int G, bool 
     const int q0 = __ldg(p.query_start + s), q1 = __ldg(p.query_start + s + 1);
     const bool in = q0 >= 0 && q1 >= q0 && q1 <= p.num_query_tokens;  // (so q1 - q0 fits)
     const int Q = in ? q1 - q0 : 0;
+    if (in && L == 0) return false;  // left out of the call, whatever its rows
     if (!in || L < Q || L > p.max_seq_len || L > static_cast<int64_t>(p.max_blocks) * kBS ||
         Q > p.max_query_len) {
         if (report) record_error(p.err, PKV_DEVERR_SEQ_LEN, s);
