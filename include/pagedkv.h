@@ -714,7 +714,12 @@ int pkv_tree_accept(const pkv_cache_desc *descs, int32_t num_descs, int32_t num_
  * running sum of R passes sample_uniforms[i] times its whole sum; an empty R
  * (W = 0) stands back for the last one that was not.  A path of max_depth nodes
  * ends there, with the next token drawn from p.
- * Tests and sums are carried in 64 bits (an element of R is rounded to 32).
+ * An element of R is rounded to 32 bits (two fused multiply-adds), four
+ * neighbours are added in 32 bits, and from there sums, masses and tests are
+ * carried in pairs of fp32 (47 bits): a sum of R is off by 2^-22 of itself at most,
+ * and by what such errors of the earlier masses, as C, take from its elements.  A
+ * result can differ from the definition's only where a comparison is closer to its
+ * border than that.
  *  path           device int32 [num_seqs, max_depth], written: the accepted
  *                 nodes, then -1
  *  path_lens      device int32 [num_seqs], written: accepted nodes, node 0
@@ -726,6 +731,9 @@ int pkv_tree_accept(const pkv_cache_desc *descs, int32_t num_descs, int32_t num_
  *  target_probs   device fp32 [num_nodes] rows of vocab_size at target_stride
  *                 elements (>= vocab_size); rows sum to 1 up to rounding.
  *                 Negative values and NaN count as 0; infinities are not handled.
+ *                 Where a node's two rows do not start at the same place within 16
+ *                 bytes (strides of four elements and aligned bases see to it) they
+ *                 are read element by element, with the same results.
  *  draft_probs    the same at draft_stride, or NULL; leaves' rows are not read
  *  accept_uniforms, sample_uniforms  device fp32 [num_nodes], [num_seqs], in
  *                 [0, 1) (others are taken as the nearest of these)

@@ -16,9 +16,9 @@
 // The draw finds the CTA and the warp from those sums, and that CTA goes through
 // the warp's stretch again (out of L2), a few elements a thread.
 //
-// Arithmetic: an element of R is one fused multiply-add of the row's fp32 values
-// (C as a pair of fp32: one rounding, 2^-24 of it), four neighbours are added in fp32
-// (as much again), and from there sums, masses and tests are carried as pairs of
+// Arithmetic: an element of R is two fused multiply-adds of the row's fp32 values (C as
+// a pair of fp32; 2^-24 of it each), four neighbours are added in fp32 (two more such
+// roundings: 2^-22 of a sum in all), and from there sums, masses and tests are carried as pairs of
 // fp32 whose errors are kept (47 bits).  fp64 would hold as much, but its
 // rate here is 2 a cycle and SM, and every warp walks: the first kernel, in fp64,
 // took 22.6, 129 and 44 us for a chain of 5 nodes, 64 trees of 16 (V 128256) and
