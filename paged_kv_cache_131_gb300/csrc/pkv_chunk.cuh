@@ -292,7 +292,8 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 }
 
 // Geometry of sequence s for this kernel; false if the sequence is not
-// ours (too few rows) or invalid (recorded when `report`).
+// ours (too few rows) or invalid (recorded when `report`, which the plan passes; the
+// items' takers look at listed sequences alone).
 struct SeqGeo {
     int L, Q, q0, rows, tiles, parts;
     int prefix;  // (under rules) positions below are seen by every token, <= L
@@ -307,7 +308,8 @@ __device__ __forceinline__ bool seq_geo(const ChunkParams &p, int s, int G, bool
     const int Q = in ? q1 - q0 : 0;
     if (in && L == 0) return false;  // left out of the call, whatever its rows
     if (!in || L < 0 || L > p.max_blocks_per_seq * kBS || L > p.max_seq_len || Q > L ||
-        Q > p.max_query_len || dec::starts_fall(p.query_start, s, q0, p.num_query_tokens)) {
+        Q > p.max_query_len ||
+        (report && dec::starts_fall(p.query_start, s, q0, p.num_query_tokens))) {
         if (report) record_error(p.err, PKV_DEVERR_SEQ_LEN, s);
         return false;
     }
