@@ -528,12 +528,14 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const __grid_constant_
             p.big_seq[ea] = s;
             p.big_cum[ea] = ec;
         }
-        for (int e = 0; e < cuts; ++e) {
-            const int per = cut_tiles[e] * kSoftmaxWarps;  // a KV head's tickets
-            int *at = p.counters + static_cast<int64_t>(cut_seq[e]) * p.num_kv_heads * p.num_tiles *
-                                       kSoftmaxWarps;
-            for (int i = threadIdx.x; i < per * p.num_kv_heads; i += blockDim.x)
-                at[static_cast<int64_t>(i / per) * p.num_tiles * kSoftmaxWarps + i % per] = 0;
+        // (a warp takes a sequence's KV head: 32 bytes a tile)
+        for (int i = warp; i < cuts * p.num_kv_heads; i += static_cast<int>(blockDim.x >> 5)) {
+            const int e = i / p.num_kv_heads, kvh = i - e * p.num_kv_heads;
+            uint4 *at = reinterpret_cast<uint4 *>(
+                p.counters + (static_cast<int64_t>(cut_seq[e]) * p.num_kv_heads + kvh) *
+                                 p.num_tiles * kSoftmaxWarps);
+            for (int j = lane; j < cut_tiles[e] * (kSoftmaxWarps / 4); j += 32)
+                at[j] = make_uint4(0u, 0u, 0u, 0u);
         }
         __syncthreads();
         if (threadIdx.x == blockDim.x - 1) {
