@@ -320,7 +320,8 @@ int pkv_decode_attention_fp8(void *out, const void *q, const void *k_cache, cons
  *   num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks:
  *                   as for pkv_decode_attention
  *   query_start     int32 [num_seqs + 1], device: query_start[0] = 0,
- *                   non-decreasing, query_start[num_seqs] = num_query_tokens
+ *                   non-decreasing, query_start[num_seqs] <= num_query_tokens
+ *                   (rows behind it are left as they are)
  *   max_query_len   host bound on every Q (sizes the launch)
  *   max_seq_len     host bound on every L (sizes the launch and workspace)
  *   workspace       pkv_chunk_workspace_bytes(...) bytes, zeroed once

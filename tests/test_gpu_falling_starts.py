@@ -47,3 +47,22 @@ def test_rows_of_the_sequence_before(news, back, scored):
         assert kind == 3 and index in (1, 2)
         assert (np.abs(got[:news[0]] - ref[:news[0]]) <= tol[:news[0]]).all()
         assert (got[news[0]:] == 7).all()
+
+
+@pytest.mark.parametrize("scored", [False, True])
+@pytest.mark.parametrize("news", [[30, 2, 17], [2, 1, 2], [4, 0, 3]])
+def test_rows_behind_the_last_sequence(news, scored):
+    c = Case([113, news[0]], [90, 60, 77], news, 8, 2, 64)
+    rules = dict(softcap=6.0) if scored else {}
+    T, ref, tol = len(c.q), *c.want(**rules)
+    tol = tol + 90 * 2.0 ** -25 * 6.0  # (as above)
+    c.q = np.concatenate([c.q, np.full((9, 8, 64), np.nan, np.float16)])
+    c.upload(**rules)
+    if scored:
+        c.call(True)
+    else:
+        pkv.pkv_chunk_attention(c.d["out"], c.d["q"], *c.d["codes"], c.d["tables"], c.d["lens"],
+                                c.d["start"], c.scale, 8, 2, 64, 16, c.maxq, c.maxl, c.NB, c.d["ws"])
+    got = c.d["out"].cpu().numpy().astype(float)
+    assert pkv.pkv_get_device_error()[0] == 0
+    assert (np.abs(got[:T] - ref) <= tol).all() and (got[T:] == 7).all()
