@@ -772,8 +772,8 @@ int pkv_tree_verify(int32_t *path, int32_t max_depth, int32_t *path_lens, int32_
  *  - The first call on a device, with that device current, looks up the
  *    array's device address (cudaGetSymbolAddress); make that first call
  *    before any stream capture.
- *  - Every call clears the array's ticket counters on `stream` before the
- *    kernel (the array keeps the previous call's contents otherwise).
+ *  - Every call clears the array's tickets on `stream` before the kernel
+ *    (a call that gave up may have left some taken).
  *  - All calls share the one array: calls that overlap on the GPU (other
  *    streams, other threads) race and corrupt each other's results.
  *  - A shape whose scratch need exceeds PKV_NOALLOC_SCRATCH_BYTES is refused

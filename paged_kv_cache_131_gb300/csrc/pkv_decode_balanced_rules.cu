@@ -7,8 +7,8 @@
 // a window's call reads what it sees: 64 sequences of up to 32768 tokens (H 32, Hk 8, D
 // 128), window 4096 and a prefix of 4: 155 us, 6.56 TB/s of 1.02 GB (605 us without
 // the rules).  Bound by HBM in fp16 (8 x 32768 tokens with a bias: 162 us, 6.6 TB/s);
-// by the consumers' instructions for drafted tokens (64 x 4: 122 us where the calls
-// without rules take 114) and in FP8 (16 sequences of 8000 to 32768, capped: 128 us
+// by the consumers' instructions for drafted tokens (64 x 4: 124 us where the calls
+// without rules take 114) and in FP8 (16 sequences of 8000 to 32768, capped: 131 us
 // where those take 115 and the bytes 103): about 850 a head and two blocks there, issue
 // slots 44% busy with two warps a scheduler, and a chain of conversion, scores, cap,
 // maximum, weights and P V behind each step.
