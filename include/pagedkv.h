@@ -199,7 +199,8 @@ int pkv_copy_blocks(void *cache, pkv_view view, int32_t num_layers, int32_t bloc
  *                pkv_decode_workspace_init), and again after a call that records
  *                PKV_DEVERR_TIMEOUT.  Otherwise decode and chunk calls of any kind
  *                and shape, FP8 and under score rules, may follow one another
- *                on it; what other code writes into it has to be zeroed again.
+ *                on it; what anything else writes into it (pkv_tree_attention,
+ *                whose scratch is its own) has to be zeroed again.
  *                Calls that share a workspace must not overlap on the GPU.
  *  Ordering: the launch may overlap the previous kernel in the stream when
  *  that kernel signals programmatic launch completion (pkv_cache_write does).
